@@ -607,6 +607,109 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
                                  int64_t n, int64_t k, void* out, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------- key/value cache
+ *
+ * A paged cache of keys and values held in NVFP4, and attention over it.
+ * The cache is `pages` pages of `page_size` tokens each; a token's slot is
+ * page * page_size + its offset in the page.  Per token and head the `dim`
+ * values of the key are quantized as one row of nvfp4_quantize (groups of 16
+ * along dim) with the fixed global scale global_scale_k, those of the value
+ * with global_scale_v (device floats, or NULL for factor 1):
+ *   k_codes, v_codes    device uint8 [pages, heads, page_size, dim/2], 16-byte aligned
+ *   k_scales, v_scales  device uint8 [pages, heads, page_size, dim/16], 16-byte aligned
+ * page_size >= 1, dim a multiple of 16 and at most 256, pages * page_size <
+ * 2^31.  The struct is read during the call only; the memory is the caller's.
+ * Slots that were never written may hold any bytes: no call reads a token
+ * outside the slots or contexts that it is given.
+ */
+typedef struct nvfp4_kv_cache {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* global_scale_k;
+  const float* global_scale_v;
+  int64_t pages, page_size, heads, dim;
+} nvfp4_kv_cache;
+
+/*
+ * nvfp4_kv_write -- quantize the keys and values of `tokens` tokens into
+ * their slots; the same codes and scales as nvfp4_quantize gives for the rows.
+ *   k, v    device, type dt: element (t, h, d) at t * token_stride + h *
+ *           head_stride + d (strides in elements, any values >= 0: slices of
+ *           a fused projection need no copy)
+ *   slots   device int64 [tokens]; a token whose slot lies outside
+ *           [0, pages * page_size) is skipped (padding).  Two tokens with the
+ *           same slot leave it undefined.
+ * Errors: bad dtype or cache, tokens < 0, negative stride, NULL pointer, k
+ * or v not aligned to its element; UNSUPPORTED for tokens * dim / 8 >= 2^31.
+ */
+nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
+                            int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                            hipStream_t stream);
+
+/*
+ * nvfp4_kv_read -- the keys and values held in `slots`, dequantized to dt:
+ * T(e2m1(q) * (e4m3(s) * g/2688)), as nvfp4_dequantize.
+ *   slots  device int64 [tokens]; a slot outside [0, pages * page_size) gives zeros
+ *   k, v   device [tokens, heads, dim] of type dt, 16-byte aligned, written
+ * Errors: as nvfp4_kv_write.
+ */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k,
+                           void* v, nvfp4_dtype dt, hipStream_t stream);
+
+/*
+ * nvfp4_kv_attention -- softmax attention of `tokens` query tokens over the
+ * cached keys and values of their sequences, float32 accumulation, for
+ * decoding steps (one or a few queries a sequence) and for prompts.
+ * Sequence b has queries query_starts[b] .. query_starts[b + 1] - 1 (n of
+ * them) and a context of L = context_lens[b] cached tokens, the queries' own
+ * included.  Its token j lies at offset j % page_size of page
+ * page_table[b, j / page_size].  Query i stands at position p = L - n + i and
+ * sees key j when j < L, j <= p (with causal), j > p - window (with causal
+ * and window > 0), and the page's number lies in [0, pages).  Query head h
+ * reads kv head h / (query_heads / heads):
+ *     s_j = scale * q . k_j,  lse = log(sum_j exp(s_j)),
+ *     out = T( sum_j exp(s_j - lse) v_j )
+ * with out = 0 and lse = -inf for a query that sees no key.
+ *   q             device, type dt: element (t, h, d) at t * q_token_stride +
+ *                 h * q_head_stride + d
+ *   page_table    device int32 [seqs, table_pages]
+ *   context_lens  device int32 [seqs]
+ *   query_starts  device int32 [seqs + 1], non-decreasing within [0, tokens];
+ *                 NULL: one query a sequence (tokens == seqs)
+ *   max_queries   at least the largest n (1 with query_starts NULL)
+ *   max_context   at least the largest L, at most table_pages * page_size;
+ *                 sizes the launch, so a tight bound helps
+ *   scale         > 0 and finite, times q . k (1 / sqrt(dim) as a rule)
+ *   out           device [tokens, query_heads, dim] of type dt, 16-byte
+ *                 aligned; rows of tokens outside every sequence are not written
+ *   lse           device float [tokens, query_heads], natural logarithm, or NULL
+ *   workspace     device, nvfp4_kv_attention_workspace_size() bytes (the same
+ *                 arguments), 256-byte aligned; may be NULL when that is 0
+ * The cached values are exact in the products (codes times block scales fit
+ * float16; the global scales multiply scores and sums in float32); each
+ * probability is rounded to float16 before its product with the values, for
+ * float32 q to a pair of float16.
+ * Errors: bad dtype or cache, negative or zero sizes (tokens or seqs = 0 is
+ * a no-op), query_heads not a multiple of heads, query_starts NULL with
+ * tokens != seqs or max_queries != 1, window < 0 or window > 0 without
+ * causal, scale not positive, max_context out of range, NULL or misaligned
+ * pointers, workspace too small; UNSUPPORTED for sizes of 2^31 or more,
+ * query_heads or seqs above 65535.
+ */
+size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
+                                         int64_t seqs, int64_t max_queries, int64_t max_context,
+                                         int64_t window);
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
+                                int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
+                                const int32_t* page_table, int64_t seqs, int64_t table_pages,
+                                const int32_t* context_lens, const int32_t* query_starts,
+                                int64_t max_queries, int64_t max_context, float scale, int causal,
+                                int64_t window, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
 /*
  * Test hook: treat every device as having this gcnArchName (NULL restores the
  * real query).  Lets host-only tests reach the unsupported-device error.

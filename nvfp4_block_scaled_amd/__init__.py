@@ -21,6 +21,12 @@ The functions carry the C entry points' names (see include/nvfp4.h):
                                                       (same, on the packed copy)
     nvfp4_mx_quantize / _dequantize / _quant_dequant / _pack / _qqmm / _qqmm_packed
                                                       (the mxfp4 / mxfp8 modes)
+    KVCache(...), kv_cache(pages, page_size, heads, dim, ...)
+                                                      (a paged key/value cache held in NVFP4)
+    nvfp4_kv_write(cache, k, v, slots)                (quantize tokens into their slots)
+    nvfp4_kv_read(cache, slots, dtype)                -> (k, v)
+    nvfp4_kv_attention(q, cache, page_table, context_lens, ...)
+                                                      -> out or (out, lse)
 Global scales are float32 device tensors with one element (per expert: e
 elements, any shape such as [e, 1, 1]), as the pages' validate_global_scale
 requires ("mlx 0.30.7.2 -> 0.30.7.6" diff, page 8).
@@ -39,6 +45,13 @@ _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lib = None
 
 
+class _KVCacheStruct(ctypes.Structure):
+    """nvfp4_kv_cache of include/nvfp4.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales",
+                                               "global_scale_k", "global_scale_v")] + \
+               [(n, ctypes.c_int64) for n in ("pages", "page_size", "heads", "dim")]
+
+
 class NVFP4Error(RuntimeError):
     def __init__(self, status, message):
         super().__init__(message)
@@ -54,6 +67,7 @@ def load_library():
         raise ImportError(f"libnvfp4.so not built at {LIB_PATH}; run nvfp4_block_scaled_amd/build.py")
     L = ctypes.CDLL(LIB_PATH)
     P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    C = ctypes.POINTER(_KVCacheStruct)
     sig = {
         "nvfp4_last_error": (ctypes.c_char_p, []),
         "nvfp4_version": (I, []),
@@ -94,6 +108,11 @@ def load_library():
         "nvfp4_mx_qqmm": (I, [P, I, I, P, P, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_qqmm_packed": (I, [P, I, I, P, P, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_gather_qmm": (I, [P, I, I, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
+        "nvfp4_kv_write": (I, [C, P, P, I, I64, I64, I64, I64, I64, P, P]),
+        "nvfp4_kv_read": (I, [C, P, I64, P, P, I, P]),
+        "nvfp4_kv_attention_workspace_size": (SZ, [C, I64, I64, I64, I64, I64, I64]),
+        "nvfp4_kv_attention": (I, [C, P, I, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, ctypes.c_float,
+                                   I, I64, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -731,6 +750,163 @@ def nvfp4_mx_qqmm_packed(x, w, out=None, workspace=None):
     return out
 
 
+# ------------------------------------------------------------------ key/value cache
+
+class KVCache:
+    """A paged key/value cache held in NVFP4: codes uint8 [pages, heads,
+    page_size, dim/2] and scales uint8 [pages, heads, page_size, dim/16] for
+    keys and for values, and the float32 device scalars of their global
+    scales (None: factor 1).  Slot = page * page_size + offset in the page."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, global_scale_k=None, global_scale_v=None):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page_size, dim/2]")
+        codes, scales = k_codes.shape, k_scales.shape
+        if v_codes.shape != codes or v_scales.shape != scales or scales[:-1] != codes[:-1] \
+                or scales[-1] * 8 != codes[-1]:
+            raise ValueError("the codes and scales of keys and values describe different shapes")
+        device = k_codes.device
+        for t in (k_codes, k_scales, v_codes, v_scales):
+            if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+                raise ValueError("codes and scales must be contiguous uint8 tensors of one device")
+        for g, name in ((global_scale_k, "global_scale_k"), (global_scale_v, "global_scale_v")):
+            _gscale(g, name)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.global_scale_k, self.global_scale_v = global_scale_k, global_scale_v
+        self.pages, self.heads, self.page_size, half = codes
+        self.dim = 2 * half
+        self._struct = _KVCacheStruct(
+            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+            None if global_scale_k is None else global_scale_k.data_ptr(),
+            None if global_scale_v is None else global_scale_v.data_ptr(),
+            self.pages, self.page_size, self.heads, self.dim)
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+
+def kv_cache(pages, page_size, heads, dim, global_scale_k=None, global_scale_v=None, device="cuda"):
+    """A new KVCache with zeroed codes and scales."""
+    if dim % 16:
+        raise ValueError("dim must be a multiple of 16")
+
+    def held(per):
+        return torch.zeros(pages, heads, page_size, dim // per, dtype=torch.uint8, device=device)
+
+    return KVCache(held(2), held(16), held(2), held(16), global_scale_k, global_scale_v)
+
+
+def _kv_rows(t, name, cache, heads):
+    """(token stride, head stride) of t [tokens, heads, dim]: its last dimension must be
+    contiguous, the others may have any stride."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {cache.dim}], not {tuple(t.shape)}")
+    if t.device != cache.k_codes.device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the cache's device")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return s[0], s[1]
+
+
+def _kv_index(t, name, cache, dtype, shape):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.device != cache.k_codes.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on the cache's device")
+
+
+def nvfp4_kv_write(cache, k, v, slots):
+    """Quantize the keys and values [tokens, heads, dim] of new tokens into
+    slots (int64 [tokens]; a slot outside the cache skips its token).  k and v
+    may be strided views with a contiguous last dimension."""
+    L = load_library()
+    kt, kh = _kv_rows(k, "k", cache, cache.heads)
+    vt, vh = _kv_rows(v, "v", cache, cache.heads)
+    tokens = k.shape[0]
+    if v.shape[0] != tokens or v.dtype != k.dtype:
+        raise ValueError("k and v must have one length and one dtype")
+    _kv_index(slots, "slots", cache, torch.int64, (tokens,))
+    _check(L.nvfp4_kv_write(cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"), tokens, kt, kh,
+                            vt, vh, slots.data_ptr(), _stream()))
+
+
+def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, out=None):
+    """(k, v), each [tokens, heads, dim] of dtype: what the cache holds in
+    slots (int64 [tokens]; zeros for a slot outside the cache).  out: the pair
+    of tensors to write."""
+    L = load_library()
+    if slots.dim() != 1:
+        raise ValueError("slots must be int64 [tokens]")
+    tokens = slots.shape[0]
+    _kv_index(slots, "slots", cache, torch.int64, (tokens,))
+    shape = (tokens, cache.heads, cache.dim)
+    if out is None:
+        k = torch.empty(shape, dtype=dtype, device=slots.device)
+        v = torch.empty(shape, dtype=dtype, device=slots.device)
+    else:
+        k, v = out
+        if k.shape != shape or v.shape != shape or k.dtype != v.dtype:
+            raise ValueError(f"out must be two tensors {shape} of one dtype")
+        _dev(k, "out")
+        _dev(v, "out")
+    _check(L.nvfp4_kv_read(cache._struct, slots.data_ptr(), tokens, k.data_ptr(), v.data_ptr(),
+                           _dtype_code(k, "out"), _stream()))
+    return k, v
+
+
+def kv_attention_workspace(cache, tokens, query_heads, seqs, max_queries, max_context, window=0):
+    """(workspace, bytes) for nvfp4_kv_attention calls of these sizes."""
+    nbytes = load_library().nvfp4_kv_attention_workspace_size(cache._struct, tokens, query_heads, seqs,
+                                                              max_queries, max_context, window)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device), nbytes
+
+
+def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, max_queries=1,
+                       max_context=None, scale=None, causal=True, window=0, return_lse=False, out=None,
+                       workspace=None):
+    """Attention of q [tokens, query_heads, dim] over the cached keys and
+    values of seqs sequences: page_table int32 [seqs, table_pages],
+    context_lens int32 [seqs] (cached tokens, the queries' own included),
+    query_starts int32 [seqs + 1] (None: one query a sequence).  max_queries
+    and max_context bound what is on the device; scale defaults to
+    1/sqrt(dim); window > 0 keeps the last `window` keys of each query.
+    Returns out [tokens, query_heads, dim], with return_lse also the float32
+    log-sum-exp [tokens, query_heads] of the scores."""
+    L = load_library()
+    tokens, query_heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+    qt, qh = _kv_rows(q, "q", cache, query_heads)
+    seqs, table_pages = page_table.shape
+    _kv_index(page_table, "page_table", cache, torch.int32, (seqs, table_pages))
+    _kv_index(context_lens, "context_lens", cache, torch.int32, (seqs,))
+    if query_starts is not None:
+        _kv_index(query_starts, "query_starts", cache, torch.int32, (seqs + 1,))
+    if max_context is None:
+        max_context = table_pages * cache.page_size
+    if scale is None:
+        scale = cache.dim ** -0.5
+    if out is None:
+        out = torch.empty((tokens, query_heads, cache.dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    else:
+        _dev(out, "out")
+    lse = torch.empty((tokens, query_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        nbytes = L.nvfp4_kv_attention_workspace_size(cache._struct, tokens, query_heads, seqs, max_queries,
+                                                     max_context, window)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(L.nvfp4_kv_attention(cache._struct, q.data_ptr(), _dtype_code(q, "q"), tokens, query_heads, qt, qh,
+                                page_table.data_ptr(), seqs, table_pages, context_lens.data_ptr(),
+                                _ptr(query_starts), max_queries, max_context, scale, int(bool(causal)), window,
+                                out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes, _stream()))
+    return (out, lse) if return_lse else out
+
+
 # ------------------------------------------------------------------ MLX-style names
 
 def _mode_check(group_size, bits, mode, global_scales=()):
@@ -829,5 +1005,6 @@ __all__ = [
     "MX_MODES", "MxPacked", "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_quant_dequant",
     "nvfp4_mx_pack", "mx_qqmm_workspace", "nvfp4_mx_qqmm", "nvfp4_mx_qqmm_packed",
     "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "nvfp4_gather_qmm_indexed",
-    "nvfp4_mx_gather_qmm",
+    "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "nvfp4_kv_read",
+    "kv_attention_workspace", "nvfp4_kv_attention",
 ]

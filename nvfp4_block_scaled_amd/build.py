@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libnvfp4.so")
 CEILING_LIB = os.path.join(HERE, "libnvfp4_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["codec.hip", "qmv.hip", "qmv_packed.hip", "gemm.hip", "smallm.hip", "mx_codec.hip", "mx_gemm.hip", "mx_qmv.hip", "gather_ex.hip", "capi.hip"]
+SOURCES = ["codec.hip", "qmv.hip", "qmv_packed.hip", "gemm.hip", "smallm.hip", "mx_codec.hip", "mx_gemm.hip", "mx_qmv.hip", "gather_ex.hip", "kv_cache.hip",
+           "kv_attention.hip", "capi.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [

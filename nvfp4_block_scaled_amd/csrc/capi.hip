@@ -1185,4 +1185,169 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
                                                     t * top_k, top_k, e, n, k, out, stream));
 }
 
+// ------------------------------------------------------------------ key/value cache
+
+static nvfp4_status check_kv(const char* op, const nvfp4_kv_cache* cache, nvfp4_dtype dt, int64_t tokens,
+                             nvfp4::KvCache* c) {
+  if (!dtype_ok(dt))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "[%s] Unsupported dtype code %d (float32, float16 and bfloat16 only).", op, (int)dt);
+  if (!cache) return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] cache must not be NULL.", op);
+  if (!cache->k_codes || !cache->k_scales || !cache->v_codes || !cache->v_scales)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] the cache's codes and scales must not be NULL.", op);
+  if (!aligned(cache->k_codes, 16) || !aligned(cache->k_scales, 16) || !aligned(cache->v_codes, 16) ||
+      !aligned(cache->v_scales, 16))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] the cache's codes and scales must be 16-byte aligned.", op);
+  if (cache->pages <= 0 || cache->page_size <= 0 || cache->heads <= 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] pages, page_size and heads must be positive.", op);
+  if (nvfp4_status st = check_k(op, cache->dim)) return st;
+  if (cache->dim > nvfp4::kKvMaxDim)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] dim (%lld) above %d.", op, (long long)cache->dim,
+                nvfp4::kKvMaxDim);
+  if (cache->pages > INT32_MAX || cache->page_size > INT32_MAX ||
+      cache->pages * cache->page_size > INT32_MAX || cache->heads > 32767)
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "[%s] pages * page_size must stay below 2^31 and heads below 32768.", op);
+  if (tokens < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tokens (%lld) must be >= 0.", op, (long long)tokens);
+  if (tokens > INT32_MAX || tokens * (cache->dim / 8) > INT32_MAX)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large (tokens * dim / 8 of 2^31 or more).", op);
+  *c = nvfp4::KvCache{cache->k_codes,        cache->k_scales,       cache->v_codes,     cache->v_scales,
+                      cache->global_scale_k, cache->global_scale_v, (int)cache->pages,  (int)cache->page_size,
+                      (int)cache->heads,     (int)cache->dim,       nvfp4::kv_make_div((uint32_t)cache->page_size)};
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
+                            int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                            hipStream_t stream) {
+  const char* op = "kv_write";
+  nvfp4::KvCache c;
+  if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
+  if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write] strides must be >= 0.");
+  if (tokens > 0) {
+    if (!k || !v || !slots)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write] k, v and slots must not be NULL.");
+    if (!aligned(k, dtype_size(dt)) || !aligned(v, dtype_size(dt)) || !aligned(slots, 8))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write] k, v and slots must be aligned to their elements.");
+  }
+  if (nvfp4_status st = check_device(op, stream)) return st;
+  if (tokens == 0) return ok();
+  return launched(op, nvfp4::launch_kv_write(c, k, v, dt, tokens, k_token_stride, k_head_stride,
+                                             v_token_stride, v_head_stride, slots, stream));
+}
+
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k,
+                           void* v, nvfp4_dtype dt, hipStream_t stream) {
+  const char* op = "kv_read";
+  nvfp4::KvCache c;
+  if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
+  if (tokens > 0) {
+    if (!k || !v || !slots)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_read] k, v and slots must not be NULL.");
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_read] k and v must be 16-byte, slots 8-byte aligned.");
+  }
+  if (nvfp4_status st = check_device(op, stream)) return st;
+  if (tokens == 0) return ok();
+  return launched(op, nvfp4::launch_kv_read(c, slots, tokens, k, v, dt, stream));
+}
+
+// The sizes of an attention call that its launch and its workspace go by.
+static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, int64_t tokens,
+                                       int64_t query_heads, int64_t seqs, int64_t max_queries,
+                                       int64_t max_context, int64_t window, nvfp4::KvAttention* a) {
+  if (seqs < 0 || query_heads <= 0 || max_queries <= 0 || max_context < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "[%s] query_heads and max_queries must be positive, seqs and max_context >= 0.", op);
+  if (query_heads % c.heads != 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] query_heads (%lld) must be a multiple of heads (%d).", op,
+                (long long)query_heads, c.heads);
+  if (window < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] window must be >= 0.", op);
+  if (query_heads > 65535 || seqs > 65535 || max_queries > INT32_MAX / query_heads || max_context > INT32_MAX ||
+      tokens > INT32_MAX / query_heads)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large.", op);
+  a->seqs = (int)seqs;
+  a->query_heads = (int)query_heads;
+  a->groups = (int)(query_heads / c.heads);
+  a->max_queries = (int)(max_queries < tokens ? max_queries : tokens);
+  a->max_keys = (int)max_context;
+  a->window = (int)(window > INT32_MAX ? 0 : window);
+  a->tokens = tokens;
+  return NVFP4_OK;
+}
+
+size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
+                                         int64_t seqs, int64_t max_queries, int64_t max_context,
+                                         int64_t window) {
+  const char* op = "kv_attention_workspace_size";
+  nvfp4::KvCache c;
+  nvfp4::KvAttention a{};
+  if (check_kv(op, cache, NVFP4_BF16, tokens, &c) ||
+      check_kv_attention(op, c, tokens, query_heads, seqs, max_queries, max_context, window, &a))
+    return 0;
+  return tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
+}
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
+                                int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
+                                const int32_t* page_table, int64_t seqs, int64_t table_pages,
+                                const int32_t* context_lens, const int32_t* query_starts,
+                                int64_t max_queries, int64_t max_context, float scale, int causal,
+                                int64_t window, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  const char* op = "kv_attention";
+  nvfp4::KvCache c;
+  nvfp4::KvAttention a{};
+  if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
+  if (nvfp4_status st =
+          check_kv_attention(op, c, tokens, query_heads, seqs, max_queries, max_context, window, &a))
+    return st;
+  if (!(scale > 0.0f) || scale > 3.0e38f)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] scale must be positive and finite.");
+  if (window > 0 && !causal)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] a window needs causal attention.");
+  if (q_token_stride < 0 || q_head_stride < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] strides must be >= 0.");
+  if (table_pages < 0 || table_pages > INT32_MAX || max_context > table_pages * c.page_size)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "[kv_attention] max_context (%lld) must be at most table_pages * page_size.",
+                (long long)max_context);
+  if (!query_starts && (tokens != seqs || max_queries != 1))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "[kv_attention] without query_starts every sequence has one query: tokens must equal seqs "
+                "and max_queries 1.");
+  const size_t need = tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
+  if (tokens > 0 && seqs > 0) {
+    if (!q || !out || !context_lens || (max_context > 0 && !page_table))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                  "[kv_attention] q, page_table, context_lens and out must not be NULL.");
+    if (!aligned(q, dtype_size(dt)) || !aligned(out, 16) || !aligned(page_table, 4) ||
+        !aligned(context_lens, 4) || !aligned(query_starts, 4) || !aligned(lse, 4))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                  "[kv_attention] out must be 16-byte aligned, the others to their elements.");
+    if (need > 0 && (!workspace || workspace_bytes < need))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] workspace of %zu bytes is smaller than %zu.",
+                  workspace ? workspace_bytes : (size_t)0, need);
+    if (need > 0 && !aligned(workspace, 256))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] workspace must be 256-byte aligned.");
+  }
+  if (nvfp4_status st = check_device(op, stream)) return st;
+  if (tokens == 0 || seqs == 0) return ok();
+  a.q = q;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.page_table = page_table;
+  a.context_lens = context_lens;
+  a.query_starts = query_starts;
+  a.out = out;
+  a.lse = lse;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.table_stride = table_pages;
+  return launched(op, nvfp4::launch_kv_attention(c, a, dt, workspace, stream));
+}
+
 }  // extern "C"
