@@ -46,6 +46,7 @@ constexpr float kLag = 3.0f, kBias = 12.0f;
 template <int SPLIT> struct KvSmall {
   static constexpr float kLimitLog2 = SPLIT == 2 ? -3.0f : -14.0f;
   static constexpr float kLimit = SPLIT == 2 ? 0x1p-3f : 0x1p-14f;
+  static constexpr float kShift = SPLIT == 2 ? 18.0f : 29.0f;
   static constexpr float kUp = SPLIT == 2 ? 0x1p18f : 0x1p29f, kDown = SPLIT == 2 ? 0x1p-18f : 0x1p-29f;
   static constexpr int kPasses = SPLIT == 2 ? 4 : 3;  // outputs stay below 2^44 2^58
 };
@@ -160,30 +161,66 @@ __device__ __forceinline__ f16x8 kv_read_transposed(const uint8_t* lo, const uin
 
 // ----------------------------------------------------------------- queries
 
-// `count` (a multiple of 8) elements of a query row from element d on, as
-// floats; elements from dim on are zeros.
-template <int COUNT>
-__device__ __forceinline__ void kv_load_query(const KvAttention& a, int dt, bool vec, int64_t at, int d, int dim,
-                                              bool live, float (&x)[COUNT]) {
+// 8 elements of a query row as they lie in memory.
+template <int SPLIT>
+struct KvRaw {
+  uint32_t w[4 * SPLIT];  // float32 for SPLIT 2, else 16-bit pairs
+};
+template <int SPLIT>
+__device__ __forceinline__ KvRaw<SPLIT> kv_load_query(const KvAttention& a, bool vec, int64_t e, bool live) {
+  KvRaw<SPLIT> r;
 #pragma unroll
-  for (int i = 0; i < COUNT / 8; ++i) {
-    float f[8] = {};
-    if (live && d + 8 * i < dim) {
-      const int64_t e = at + d + 8 * i;
-      if (vec) {
-        if (dt == kF32) load8x<kF32>(a.q, e >> 3, f);
-        else if (dt == kF16) load8x<kF16>(a.q, e >> 3, f);
-        else load8x<kBF16>(a.q, e >> 3, f);
-      } else {
+  for (int i = 0; i < 4 * SPLIT; ++i) r.w[i] = 0u;
+  if (live) {
+    if (vec) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          f[j] = dt == kF32 ? reinterpret_cast<const float*>(a.q)[e + j]
-                 : dt == kF16 ? (float)reinterpret_cast<const _Float16*>(a.q)[e + j]
-                              : (float)reinterpret_cast<const __bf16*>(a.q)[e + j];
+      for (int i = 0; i < SPLIT; ++i) {
+        const u32x4 x = reinterpret_cast<const u32x4*>(a.q)[SPLIT * (e >> 3) + i];
+        r.w[4 * i] = x.x; r.w[4 * i + 1] = x.y; r.w[4 * i + 2] = x.z; r.w[4 * i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * SPLIT; ++i) {
+        if constexpr (SPLIT == 2) {
+          r.w[i] = reinterpret_cast<const uint32_t*>(a.q)[e + i];
+        } else {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + e + 2 * i;
+          r.w[i] = p[0] | (uint32_t)p[1] << 16;
+        }
       }
     }
+  }
+  return r;
+}
+template <int SPLIT>
+__device__ __forceinline__ void kv_unpack_query(const KvRaw<SPLIT>& r, int dt, float (&x)[8]) {
+  if constexpr (SPLIT == 2) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[8 * i + j] = f[j];
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
+  } else {
+    const u32x4 w = {r.w[0], r.w[1], r.w[2], r.w[3]};
+    if (dt == kF16) unpack8<kF16>(w, x);
+    else unpack8<kBF16>(w, x);
+  }
+}
+template <int SPLIT>
+__device__ __forceinline__ float kv_query_top(const KvRaw<SPLIT>& r, int dt) {
+  float x[8], top = 0.0f;
+  kv_unpack_query<SPLIT>(r, dt, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(x[i]));
+  return top;
+}
+// Times `power` as one or two float16.
+template <int SPLIT>
+__device__ __forceinline__ void kv_query_halves(const KvRaw<SPLIT>& r, int dt, float power, f16x8& hi, f16x8& lo) {
+  float x[8];
+  kv_unpack_query<SPLIT>(r, dt, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = x[i] * power;
+    hi[i] = (_Float16)y;
+    if constexpr (SPLIT == 2) lo[i] = (_Float16)(y - (float)hi[i]);
   }
 }
 
@@ -215,11 +252,83 @@ __device__ __forceinline__ void kv_store4(int dt, void* out, int64_t e, const fl
   else kv_store4<kBF16>(out, e, v);
 }
 
+// ----------------------------------------------------------------- sharing out the keys
+//
+// Contexts differ in length and live on the device, so the workgroups share
+// the work out themselves.  The keys of every (sequence, kv head) pair are cut
+// into units of kFewStep keys, the pairs' units are counted through in order,
+// and each of the launch's workgroups takes an equal run of them: a part of one
+// pair, or the end of one and the beginning of the next ones.  The part of
+// pair p that workgroup g computes has the number g + p, which no other part
+// has.  A pair that one workgroup takes whole is written out by it; the parts
+// of the others are joined by a second launch.  (One workgroup per fixed
+// chunk of keys instead cost 3 us of start and end for each chunk, and left
+// compute units idle in the last round: 57 - 110 us against 46 us for 32
+// contexts of up to 8192, 8 heads.)
+constexpr int kFewWaves = 4;
+constexpr int kFewTile = 32;
+constexpr int kFewStep = kFewWaves * kFewTile;
+
+struct KvShare {
+  int groups;    // workgroups of the launch
+  int rows;      // rows of a part
+  float* sums;   // [parts][rows][dim], times 2^kBias
+  float* stats;  // [parts][rows][2]: maximum (log2), sum
+};
+
+// Lane `lane`'s (wave-uniform) values, in scalar registers.
+__device__ __forceinline__ int64_t kv_readlane(int64_t v, int lane) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+// Sequences 64 at a time, one per lane: their ranges and the units before them.
+struct KvScan {
+  KvRange range;   // of sequence base + lane
+  int units;       // of one pair of this sequence; 0 past the last one and without queries
+  int64_t first;   // units before this sequence
+  int64_t after;   // units up to the end of the block
+};
+__device__ __forceinline__ void kv_scan(const KvCache& c, const KvAttention& a, int rows, int base, int64_t before,
+                                        KvScan& s) {
+  const int lane = threadIdx.x & 63, b = base + lane;
+  s.units = 0;
+  s.range = KvRange{0, 0, 0, 0, 0};
+  if (b < a.seqs) {
+    s.range = kv_range(a, b, 0, rows);
+    // a sequence that sees nothing still has a unit: its rows are written as zeros
+    if (s.range.n > 0) s.units = max(1, (s.range.hi - s.range.lo + kFewStep - 1) / kFewStep);
+  }
+  int64_t sum = (int64_t)s.units * c.heads;
+  const int64_t own = sum;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t up = __shfl_up(sum, off, 64);
+    if (lane >= off) sum += up;
+  }
+  s.first = before + sum - own;
+  s.after = before + kv_readlane(sum, 63);
+}
+__device__ __forceinline__ KvRange kv_range_of(const KvScan& s, int lane) {
+  return KvRange{__builtin_amdgcn_readlane(s.range.first, lane), __builtin_amdgcn_readlane(s.range.n, lane),
+                 __builtin_amdgcn_readlane(s.range.context, lane), __builtin_amdgcn_readlane(s.range.lo, lane),
+                 __builtin_amdgcn_readlane(s.range.hi, lane)};
+}
+// Units of one workgroup.
+__device__ __forceinline__ int64_t kv_units_each(const KvCache& c, const KvAttention& a, const KvShare& sh) {
+  int64_t total = 0;
+  for (int base = 0; base < a.seqs; base += 64) {
+    KvScan s;
+    kv_scan(c, a, sh.rows, base, total, s);
+    total = s.after;
+  }
+  return (total + sh.groups - 1) / sh.groups;
+}
+
 // ----------------------------------------------------------------- few rows
 //
-// Up to 16 MT rows share a chunk of keys.  A workgroup of four waves takes one
-// (chunk, kv head, sequence); each wave walks its own tiles of 32 keys with
-// its own running maximum, and the four meet at the end.
+// Up to 16 MT rows of a pair share a run of its keys.  Each of a workgroup's
+// four waves walks its own tiles of 32 keys with its own running maximum, and
+// the four meet at the end of the run.
 //
 // Per tile a lane holds 64 NG / 4 values of key l % 16 (+ 16): it loads their
 // codes with one wide load and uses them in place as rows of the matrix
@@ -229,48 +338,61 @@ __device__ __forceinline__ void kv_store4(int dt, void* out, int64_t e, const fl
 // O^T = V^T P^T, so probabilities never leave their lane.  Values are decoded
 // the same way, written to the wave's own LDS as float16 and read back
 // transposed (ds_read_b64_tr_b16); nothing in the loop waits for another wave.
-// The next tile's codes are loaded before this tile's work.
-constexpr int kFewWaves = 4;
-constexpr int kFewTile = 32;
-constexpr int kFewStep = kFewWaves * kFewTile;
-
-struct KvSplit {
-  int chunk, splits;  // keys per chunk, chunks per row tile (1: the output is written directly)
-  float* sums;        // [rows of q * heads][splits][dim], times 2^kBias
-  float* stats;       // [rows of q * heads][splits][2]: maximum (log2), sum
-};
 
 constexpr int few_row_bytes(int NG) { return 128 * NG + 32; }  // a key's values in LDS: +32 spreads the banks
+constexpr int kFewPages = 1024;  // page numbers staged at a time
+
+// Waves per SIMD (and workgroups per CU) that the registers of an instance
+// allow without spills.
+constexpr int few_occupancy(int NG, int MT, int SPLIT) {
+  const int size = NG * MT * SPLIT;
+  return size == 1 ? 4 : size == 2 ? 3 : size <= 4 && MT == 1 ? 2 : 1;
+}
 
 template <int NG, int MT, int SPLIT, bool EXACT>
-__global__ void __launch_bounds__(256, (NG * MT * SPLIT > 4 ? 1 : NG * MT * SPLIT > 2 ? 2 : 4))
-kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
+__global__ void __launch_bounds__(256, few_occupancy(NG, MT, SPLIT))
+kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   constexpr int DP = 64 * NG, STEPS = 2 * NG, DB = DP / 16, RB = few_row_bytes(NG);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ float stat_m[kFewWaves][16 * MT], stat_l[kFewWaves][16 * MT];
+  int* page_of = reinterpret_cast<int*>(lds + kFewWaves * kFewTile * RB);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, quarter = lane >> 4;
-  const int b = blockIdx.y;
-  const int split = blockIdx.x % sp.splits, tile_head = blockIdx.x / sp.splits;
-  const int head = tile_head % c.heads;
-  const int row0 = tile_head / c.heads * 16 * MT;
+  uint8_t* mine = lds + wave * kFewTile * RB;
+  const int g0 = NG * quarter;
+  const float value_factor = global_decode(c.global_v);
+  const float key_factor = a.scale * kLog2e * global_decode(c.global_k);
 
-  const KvRange rg = kv_range(a, b, row0, 16 * MT);
-  const int rows = rg.n * a.groups;
-  if (row0 >= rows) return;
-  const int begin = rg.lo + split * sp.chunk, end = min(rg.hi, begin + sp.chunk);
-  if (begin >= end && split > 0) return;  // the first chunk's workgroup answers for rows that see nothing
-
-  // page numbers of the chunk, -1 where there is no such page
-  int* page_of = reinterpret_cast<int*>(lds + kFewWaves * kFewTile * RB);
-  const int p0 = kv_div(begin, c.page_div);
-  if (begin < end) {
-    const int count = (int)kv_div(end - 1, c.page_div) - p0 + 1;
-    for (int i = threadIdx.x; i < count; i += 256) {
-      const int p = a.page_table[b * a.table_stride + p0 + i];
-      page_of[i] = p >= 0 && p < c.pages ? p : -1;
-    }
+  const int64_t each = kv_units_each(c, a, sh);
+  int64_t unit = blockIdx.x * each;
+  const int64_t last_unit = unit + each;
+  int base = 0;
+  int64_t before = 0;
+  bool first_run = true;
+  while (unit < last_unit) {
+  // the sequence that holds this unit (scanned anew for each run: kept, the
+  // scan would cost the loop a dozen registers)
+  KvScan scan;
+  for (kv_scan(c, a, sh.rows, base, before, scan); unit >= scan.after; kv_scan(c, a, sh.rows, base, before, scan)) {
+    base += 64;
+    before = scan.after;
+    if (base >= a.seqs) return;  // past the last unit
   }
+  const int at_lane = 63 - __builtin_clzll(__ballot(scan.units > 0 && scan.first <= unit));
+  const int b = base + at_lane;
+  const KvRange rg = kv_range_of(scan, at_lane);
+  const int pair_units = __builtin_amdgcn_readlane(scan.units, at_lane);
+  const int64_t inside = unit - kv_readlane(scan.first, at_lane);
+  const int head = (int)(inside / pair_units);
+  const int off = (int)(inside - (int64_t)head * pair_units);
+  const int take = (int)min((int64_t)(pair_units - off), last_unit - unit);
+  unit += take;
+  const bool whole = take == pair_units;
+  const int begin = rg.lo + off * kFewStep, end = min(rg.hi, begin + take * kFewStep);
+  const int rows = rg.n * a.groups;
+  constexpr int row0 = 0;
+  if (!first_run) __syncthreads();  // the last run's sums and page numbers have been read
+  first_run = false;
 
   // queries: row `col` of each row tile, values 16 NG quarter ..
   f16x8 q[MT][SPLIT][STEPS];
@@ -282,24 +404,21 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
     const bool live = r < rows;
     const int qi = r / a.groups;
     const int64_t at = (int64_t)(rg.first + qi) * a.q_token + (head * a.groups + (r - qi * a.groups)) * a.q_head;
-    float x[16 * NG];
-    kv_load_query<16 * NG>(a, dt, q_vec, at, 16 * NG * quarter, c.dim, live, x);
+    KvRaw<SPLIT> raw[STEPS];
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16 * NG; ++i) top = fmaxf(top, __builtin_fabsf(x[i]));
+    for (int t = 0; t < STEPS; ++t) {
+      const int d = 16 * NG * quarter + 8 * t;
+      raw[t] = kv_load_query<SPLIT>(a, q_vec, at + d, live && d < c.dim);
+      top = fmaxf(top, kv_query_top<SPLIT>(raw[t], dt));
+    }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     float back;
     const float power = kv_row_power(top, back);
-    factor[m] = a.scale * kLog2e * global_decode(c.global_k) * back;
+    factor[m] = key_factor * back;
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float y = x[8 * t + j] * power;
-        q[m][0][t][j] = (_Float16)y;
-        if constexpr (SPLIT == 2) q[m][SPLIT - 1][t][j] = (_Float16)(y - (float)(_Float16)y);
-      }
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, power, q[m][0][t], q[m][SPLIT - 1][t]);
     const int pos = rg.context - rg.n + qi;
     see_hi[m] = !live ? 0 : a.causal ? min(rg.hi, pos + 1) : rg.hi;
     see_lo[m] = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
@@ -311,7 +430,6 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
     if (a.window > 0)
       all_lo = max(0, rg.context - rg.n + min(rg.n - 1, (row0 + 16 * MT - 1) / a.groups) - a.window + 1);
   }
-  __syncthreads();
 
   f32x4 acc[MT][DB];
   float m_run[MT], sub[MT], l_run[MT];
@@ -324,42 +442,60 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
     for (int d = 0; d < DB; ++d) acc[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  uint8_t* mine = lds + wave * kFewTile * RB;
-  const int g0 = NG * quarter;
-  KvGroups<NG> kn[2], vn[2];  // the next tile
-  uint32_t live_n = 0;        // which of its 32 keys exist
-  auto fetch = [&](int tile) {
-    uint32_t bits = 0;
+  // runs whose page numbers do not fit are staged in several goes
+  const int span = (int)min((int64_t)(end - begin), (int64_t)(kFewPages - 2) * c.page_size / kFewStep * kFewStep);
+  for (int from = begin; from < end; from += span) {
+  const int to = min(end, from + span);
+  const int p0 = kv_div(from, c.page_div);
+  {
+    const int count = (int)kv_div(to - 1, c.page_div) - p0 + 1;
+    if (from > begin) __syncthreads();
+    for (int i = threadIdx.x; i < count; i += 256) {  // -1 where there is no such page
+      const int p = a.page_table[b * a.table_stride + p0 + i];
+      page_of[i] = p >= 0 && p < c.pages ? p : -1;
+    }
+    __syncthreads();
+  }
+  // A tile's keys are loaded once the last tile's are used up, its values
+  // likewise: two thirds of a tile's time ahead, in the same registers.
+  KvGroups<NG> kt[2], vt[2];
+  int64_t row[2];        // this lane's rows of the tile that is being loaded
+  uint32_t exists = 0u;  // which of its 32 keys do
+  auto locate = [&](int at) {
+    exists = 0u;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int j = tile + 16 * u + col;
-      bool live = j < end;
-      int64_t row = 0;
-      if (live) {
+      const int j = at + 16 * u + col;
+      row[u] = -1;
+      if (j < to) {
         const int pi = kv_div(j, c.page_div);
         const int page = page_of[pi - p0];
-        live = page >= 0;
-        row = kv_row(c, max(page, 0), head, j - pi * c.page_size);
+        if (page >= 0) row[u] = kv_row(c, page, head, j - pi * c.page_size);
       }
-      bits |= (uint32_t)(__ballot(live) & 0xFFFFu) << (16 * u);
-      kn[u] = kv_load<NG, EXACT>(c.k_codes, c.k_scales, row, c.dim, g0, live);
-      vn[u] = kv_load<NG, EXACT>(c.v_codes, c.v_scales, row, c.dim, g0, live);
+      exists |= (uint32_t)(__ballot(row[u] >= 0) & 0xFFFFu) << (16 * u);
     }
-    live_n = bits;
   };
-  int tile = begin + wave * kFewTile;
-  if (tile < end) fetch(tile);
-  for (; tile < end; tile += kFewStep) {
-    const KvGroups<NG> k0 = kn[0], k1 = kn[1], v0 = vn[0], v1 = vn[1];
-    const uint32_t live = live_n;
-    if (tile + kFewStep < end) fetch(tile + kFewStep);
+  auto load = [&](const uint8_t* codes, const uint8_t* scales, KvGroups<NG>(&x)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) x[u] = kv_load<NG, EXACT>(codes, scales, max(row[u], (int64_t)0), c.dim, g0, row[u] >= 0);
+  };
+  int tile = from + wave * kFewTile;
+  if (tile < to) {
+    locate(tile);
+    load(c.k_codes, c.k_scales, kt);
+    load(c.v_codes, c.v_scales, vt);
+  }
+  for (; tile < to; tile += kFewStep) {
+    const uint32_t live = exists;
+    const bool more = tile + kFewStep < to;
+    if (more) locate(tile + kFewStep);
 
     // scores
     f32x4 s[MT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f16x8 kf[STEPS];
-      kv_values<NG>(u == 0 ? k0 : k1, kf);
+      kv_values<NG>(kt[u], kf);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -371,15 +507,17 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
         s[m][u] = x;
       }
     }
+    if (more) load(c.k_codes, c.k_scales, kt);
     // values into LDS
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f16x8 vf[STEPS];
-      kv_values<NG>(u == 0 ? v0 : v1, vf);
+      kv_values<NG>(vt[u], vf);
 #pragma unroll
       for (int t = 0; t < STEPS; ++t)
         *reinterpret_cast<f16x8*>(mine + (16 * u + col) * RB + 32 * NG * quarter + 16 * t) = vf[t];
     }
+    if (more) load(c.v_codes, c.v_scales, vt);
     // probabilities
     const bool masked = live != 0xFFFFFFFFu || tile < all_lo || tile + kFewTile > all_hi;
     float w[MT][8];
@@ -451,12 +589,12 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         const uint8_t* at = mine + (4 * quarter + (col >> 2)) * RB + 32 * d + 8 * (col & 3);
-        const f16x8 vt = kv_read_transposed(at, at + 16 * RB);
+        const f16x8 vf = kv_read_transposed(at, at + 16 * RB);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int e = SPLIT - 1; e >= 0; --e)
-            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, p[m][e], acc[m][d], 0, 0, 0);
+            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[m][e], acc[m][d], 0, 0, 0);
       }
       if (!again) {
         if (pass > 1) {
@@ -482,6 +620,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
       }
     }
   }
+  }
 
   // the four waves meet
 #pragma unroll
@@ -494,7 +633,6 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
       stat_l[wave][16 * m + col] = l;
     }
   }
-  const float value_factor = global_decode(c.global_v);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (m > 0) __syncthreads();
@@ -522,90 +660,469 @@ kv_few_kernel(KvCache c, KvAttention a, KvSplit sp, int dt, bool q_vec) {
       }
       const int qi = r / a.groups;
       const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + head * a.groups + (r - qi * a.groups);
-      if (sp.splits == 1) {
+      if (whole) {
         const float by = l == 0.0f ? 0.0f : value_factor / l;  // a NaN stays one
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= by;
         kv_store4(dt, a.out, row * c.dim + d, v);
         if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? kNone : (mt - kBias + __builtin_log2f(l)) * kLn2;
       } else {
-        const int64_t at = row * sp.splits + split;
-        kv_store4<kF32>(sp.sums, at * c.dim + d, v);
-        if (d == 0) *reinterpret_cast<f32x2*>(sp.stats + 2 * at) = f32x2{mt, l};
+        const int64_t at = ((int64_t)blockIdx.x + (int64_t)b * c.heads + head) * sh.rows + r;
+        kv_store4<kF32>(sh.sums, at * c.dim + d, v);
+        if (d == 0) *reinterpret_cast<f32x2*>(sh.stats + 2 * at) = f32x2{mt, l};
       }
     }
   }
+  }
 }
 
-// ----------------------------------------------------------------- joining the chunks
+// ----------------------------------------------------------------- many rows
+//
+// 128 rows of a (sequence, kv head) per workgroup, 32 per wave, against tiles
+// of keys and values that the workgroup decodes once into LDS as float16 for
+// all of them: S^T = K Q^T and O^T = V^T P^T on 32 x 32 x 16 products, the
+// probabilities again staying in the lane that computed their scores.  Two
+// buffers: while a tile is multiplied the next one's codes (loaded a tile
+// earlier) are decoded into the other, and the loads of the one after it are
+// under way; one barrier a tile.  Rows of LDS are padded so that the 16-byte
+// reads of K and the transposing reads of V touch every bank once.
+//
+// Too few workgroups for the GPU split the keys further (KvChunks).
+constexpr int kManyRows = 128;
+constexpr int many_tile(int NG) { return NG <= 2 ? 64 : 32; }
+constexpr int many_k_row(int NG) { return 128 * NG + 16; }
+constexpr int many_v_row(int NG) { return 128 * NG + 64; }
+constexpr int many_lds(int NG) { return 2 * many_tile(NG) * (many_k_row(NG) + many_v_row(NG)); }
 
-// One wave per query and query head: the maximum over its chunks, then their
-// sums in chunk order (the same bits on every run).
-__global__ void __launch_bounds__(256) kv_join_kernel(KvCache c, KvAttention a, KvSplit sp, int tile_rows, int dt) {
-  const int lane = threadIdx.x & 63, b = blockIdx.y;
-  const int r0 = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int qi = r0 / a.query_heads, qh = r0 - qi * a.query_heads;
-  const int r = qi * a.groups + qh % a.groups;  // its row among those of its kv head
-  const KvRange rg = kv_range(a, b, r / tile_rows * tile_rows, tile_rows);
-  if (qi >= rg.n) return;
-  const int used = rg.hi > rg.lo ? (rg.hi - rg.lo + sp.chunk - 1) / sp.chunk : 1;
+struct KvChunks {
+  int chunk, splits;  // keys per chunk (a multiple of 64), chunks per tile of rows
+  int row_tiles;      // of a sequence and kv head
+  float* sums;        // [tokens][query_heads][splits][dim], times 2^kBias
+  float* stats;       // [tokens][query_heads][splits][2]: maximum (log2), sum
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+template <int NG, int SPLIT, bool EXACT>
+__global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1))
+kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
+  constexpr int DP = 64 * NG, TILE = many_tile(NG), SUB = TILE / 32, STEPS = DP / 16, DB = DP / 32;
+  constexpr int KROW = many_k_row(NG), VROW = many_v_row(NG), BUF = TILE * (KROW + VROW);
+  constexpr bool BOTH = TILE == 64;  // every thread decodes keys and values; else half of them each
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ uint64_t exists[2][4];  // four lanes a key: which keys of a buffer exist
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 31, half = lane >> 5;
+  const int b = blockIdx.y;
+  int x = blockIdx.x;
+  const int split = x % sp.splits;
+  x /= sp.splits;
+  const int head = x % c.heads;
+  const int row0 = (sp.row_tiles - 1 - x / c.heads) * kManyRows;  // the longest ranges first
+  const KvRange rg = kv_range(a, b, row0, kManyRows);
+  const int rows = rg.n * a.groups;
+  if (row0 >= rows) return;
+  const int begin = rg.lo + split * sp.chunk, end = min(rg.hi, begin + sp.chunk);
+  if (begin >= end && split > 0) return;  // the first chunk's workgroup answers for rows that see nothing
+
+  // what this thread decodes: NG groups of one key (and of its value)
+  const int key_of = BOTH ? threadIdx.x >> 2 : (threadIdx.x & 127) >> 2;
+  const bool second = !BOTH && threadIdx.x >= 128;
+  const int g0 = NG * (threadIdx.x & 3);
+  auto lookup = [&](int tile) {  // the page of this thread's key, -1 where there is none
+    const int j = tile + key_of;
+    if (j >= end) return -1;
+    const int page = a.page_table[b * a.table_stride + kv_div(j, c.page_div)];
+    return page < c.pages ? page : -1;
+  };
+  KvGroups<NG> kt, vt;
+  int live = 0;
+  auto load = [&](int tile, int page) {
+    const int j = tile + key_of;
+    live = (page >= 0) | (j >= end);  // past the end every row's mask holds
+    const int64_t row = page >= 0 ? kv_row(c, page, head, j - (int)kv_div(j, c.page_div) * c.page_size) : 0;
+    if constexpr (BOTH) {
+      kt = kv_load<NG, EXACT>(c.k_codes, c.k_scales, row, c.dim, g0, page >= 0);
+      vt = kv_load<NG, EXACT>(c.v_codes, c.v_scales, row, c.dim, g0, page >= 0);
+    } else {
+      kt = kv_load<NG, EXACT>(second ? c.v_codes : c.k_codes, second ? c.v_scales : c.k_scales, row, c.dim, g0, page >= 0);
+    }
+  };
+  auto store = [&](int buf) {
+    uint8_t* to = lds + buf * BUF;
+    const uint64_t bits = __ballot(live != 0);
+    if (lane == 0) exists[buf][wave] = bits;
+    f16x8 v[2 * NG];
+    kv_values<NG>(kt, v);
+    uint8_t* at = to + (second ? TILE * KROW + key_of * VROW : key_of * KROW) + 32 * g0;
+#pragma unroll
+    for (int i = 0; i < 2 * NG; ++i) *reinterpret_cast<f16x8*>(at + 16 * i) = v[i];
+    if constexpr (BOTH) {
+      kv_values<NG>(vt, v);
+      at = to + TILE * KROW + key_of * VROW + 32 * g0;
+#pragma unroll
+      for (int i = 0; i < 2 * NG; ++i) *reinterpret_cast<f16x8*>(at + 16 * i) = v[i];
+    }
+  };
+  int page = lookup(begin);
+  int page2 = lookup(begin + TILE);
+
+  // queries: row `col` of this wave's 32
+  const int r = row0 + 32 * wave + col;
+  const bool row_live = r < rows;
+  const int qi = r / a.groups, qh = head * a.groups + r - qi * a.groups;
+  f16x8 q[SPLIT][STEPS];
+  float factor;
+  {
+    const int64_t at = (int64_t)(rg.first + qi) * a.q_token + qh * a.q_head;
+    KvRaw<SPLIT> raw[STEPS];
+    float top = 0.0f;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int d = 16 * t + 8 * half;
+      raw[t] = kv_load_query<SPLIT>(a, q_vec, at + d, row_live && d < c.dim);
+      top = fmaxf(top, kv_query_top<SPLIT>(raw[t], dt));
+    }
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    float back;
+    const float power = kv_row_power(top, back);
+    factor = a.scale * kLog2e * global_decode(c.global_k) * back;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, power, q[0][t], q[SPLIT - 1][t]);
+  }
+  const int pos = rg.context - rg.n + qi;
+  const int see_hi = !row_live ? 0 : a.causal ? min(end, pos + 1) : end;
+  const int see_lo = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  // keys that any, and that every row of this wave sees
+  int any_lo = 0, any_hi = end, all_lo = 0, all_hi = end;
+  {
+    const int w0 = row0 + 32 * wave;
+    if (w0 >= rows) any_hi = 0;
+    else if (a.causal) {
+      const int q0 = w0 / a.groups, q1 = min(w0 + 31, rows - 1) / a.groups, base = rg.context - rg.n;
+      any_hi = min(end, base + q1 + 1);
+      all_hi = min(end, base + q0 + 1);
+      if (a.window > 0) {
+        any_lo = max(0, base + q0 - a.window + 1);
+        all_lo = max(0, base + q1 - a.window + 1);
+      }
+    }
+  }
+
+  f32x16 acc[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+  float m_run = kNone, sub = -kBias, l_run = 0.0f;
+
+  if (begin < end) {
+    load(begin, page);
+    page = page2;
+    page2 = lookup(begin + 2 * TILE);
+    store(0);
+    if (begin + TILE < end) load(begin + TILE, page);
+    page = page2;
+    page2 = lookup(begin + 3 * TILE);
+    lds_barrier();
+  }
+  int buf = 0;
+  for (int tile = begin; tile < end; tile += TILE, buf ^= 1) {
+    const uint8_t* kb = lds + buf * BUF;
+    const uint8_t* vb = kb + TILE * KROW;
+    const bool busy = tile < any_hi && tile + TILE > any_lo;  // wave-uniform
+    f32x16 s[SUB];
+    if (busy) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+          const f16x8 kf = *reinterpret_cast<const f16x8*>(kb + (32 * u + col) * KROW + 32 * t + 16 * half);
+#pragma unroll
+          for (int e = SPLIT - 1; e >= 0; --e)
+            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[e][t], s[u], 0, 0, 0);
+        }
+      }
+    }
+    if (tile + TILE < end) {
+      store(buf ^ 1);
+      if (tile + 2 * TILE < end) load(tile + 2 * TILE, page);
+      page = page2;
+      page2 = lookup(tile + 4 * TILE);
+    }
+    if (busy) {
+      if (tile < all_lo || tile + TILE > all_hi) {
+        const int lo = see_lo - tile - 4 * half, hi = see_hi - tile - 4 * half;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = 32 * u + 8 * (i >> 2) + (i & 3);
+            s[u][i] = ((key >= lo) & (key < hi)) ? s[u][i] : kNone;
+          }
+      }
+      uint64_t have = ~0ull;
+#pragma unroll
+      for (int i = 0; i < 2 * SUB; ++i) have &= exists[buf][i];
+      if (have != ~0ull) {  // pages that are not there
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = 8 * (i >> 2) + 4 * half + (i & 3);  // of this half tile
+            if (!(exists[buf][2 * u + (i >> 3)] >> (4 * (key & 15)) & 1)) s[u][i] = kNone;
+          }
+      }
+      float top = s[0][0], low = s[0][0];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          top = max3(top, s[u][i], s[u][i + 1]);
+          low = min3(low, s[u][i], s[u][i + 1]);
+        }
+      top *= factor;  // the factor is positive
+      low *= factor;
+      if (__any(top > m_run + kLag)) {
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float next = fmaxf(m_run, top);
+        const float keep = m_run == kNone ? 0.0f : __builtin_amdgcn_exp2f(m_run - next);
+        m_run = next;
+        sub = next == kNone ? -kBias : next - kBias;
+        l_run *= keep;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] *= keep;
+      }
+      int small = __builtin_amdgcn_readfirstlane(__any(low - sub < KvSmall<SPLIT>::kLimitLog2));
+      float shift = 0.0f, down = 1.0f;  // of the present band of small weights
+      for (int pass = 1;; ++pass) {
+        asm("" : "+s"(small));  // one copy of the products below for both kinds of tile
+        f16x8 p[SUB][2][SPLIT];
+        bool again = false;
+        if (!small) {
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], factor, -sub));
+              l_run += w;
+              p[u][i >> 3][0][i & 7] = (_Float16)w;
+              if constexpr (SPLIT == 2) p[u][i >> 3][SPLIT - 1][i & 7] = (_Float16)(w - (float)(_Float16)w);
+            }
+        } else {  // one pass per band of weights (KvSmall)
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float t = __builtin_fmaf(s[u][i], factor, -sub) + shift;
+              const bool below = (t < KvSmall<SPLIT>::kLimitLog2) & (pass < KvSmall<SPLIT>::kPasses);
+              const bool above = (pass > 1) & (t >= KvSmall<SPLIT>::kLimitLog2 + KvSmall<SPLIT>::kShift);
+              const float w = (below | above) ? 0.0f : __builtin_amdgcn_exp2f(t);
+              l_run += w * down;
+              again |= below & (t > kNone);
+              p[u][i >> 3][0][i & 7] = (_Float16)w;
+              if constexpr (SPLIT == 2) p[u][i >> 3][SPLIT - 1][i & 7] = (_Float16)(w - (float)(_Float16)w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              const uint8_t* at = vb + (32 * u + 16 * t + 4 * half + ((lane & 15) >> 2)) * VROW + 64 * d +
+                                  32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+              const f16x8 vf = kv_read_transposed(at, at + 8 * VROW);
+#pragma unroll
+              for (int e = SPLIT - 1; e >= 0; --e)
+                acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[u][t][e], acc[d], 0, 0, 0);
+            }
+        if (!small) break;
+        const bool last = !__any(again);
+        const float by = last ? down : KvSmall<SPLIT>::kUp;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] *= by;
+        if (last) break;
+        shift += KvSmall<SPLIT>::kShift;
+        down *= KvSmall<SPLIT>::kDown;
+      }
+    }
+    lds_barrier();
+  }
+
+  l_run += __shfl_xor(l_run, 32, 64);
+  if (!row_live) return;
   const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + qh;
-  const float* stats = sp.stats + 2 * row * sp.splits;
+  if (sp.splits == 1) {
+    const float by = l_run == 0.0f ? 0.0f : global_decode(c.global_v) / l_run;  // a NaN stays one
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = 32 * d + 8 * i + 4 * half;
+        const float v[4] = {acc[d][4 * i] * by, acc[d][4 * i + 1] * by, acc[d][4 * i + 2] * by, acc[d][4 * i + 3] * by};
+        if (at < c.dim) kv_store4(dt, a.out, row * c.dim + at, v);
+      }
+    if (a.lse && half == 0) a.lse[row] = l_run == 0.0f ? kNone : (m_run - kBias + __builtin_log2f(l_run)) * kLn2;
+  } else {
+    const int64_t part = row * sp.splits + split;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = 32 * d + 8 * i + 4 * half;
+        const float v[4] = {acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        if (at < c.dim) kv_store4<kF32>(sp.sums, part * c.dim + at, v);
+      }
+    if (half == 0) *reinterpret_cast<f32x2*>(sp.stats + 2 * part) = f32x2{m_run, l_run};
+  }
+}
+
+// ----------------------------------------------------------------- joining the parts
+
+// Row `row` of the output from its parts at, at + stride, ..: one workgroup.  Each wave sums some of the parts,
+// several at a time (dim / 4 lanes a part), and the four add theirs in a fixed
+// order, so every run gives the same bits.
+__device__ __forceinline__ void kv_join(const KvCache& c, const KvAttention& a, int dt, const float* sums,
+                                        const float* stats, int64_t at, int64_t stride, int parts, int64_t row) {
+  __shared__ __attribute__((aligned(16))) float part[kFewWaves][kKvMaxDim];
+  __shared__ float part_l[kFewWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float top = kNone;
-  for (int i = lane; i < used; i += 64) top = fmaxf(top, stats[2 * i]);
+  for (int i = lane; i < parts; i += 64) top = fmaxf(top, stats[2 * (at + i * stride)]);
   top = wave_max(top);
-  const float* sums = sp.sums + row * sp.splits * c.dim;
+  const int wide = c.dim / 4, each_wave = 64 / wide;  // lanes of a part, parts side by side
+  const int side = lane / wide, d = 4 * (lane - side * wide);
   float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const bool on = 4 * lane < c.dim;
+  if (side < each_wave) {
 #pragma unroll 4
-  for (int i = 0; i < used; ++i) {
-    const f32x2 st = *reinterpret_cast<const f32x2*>(stats + 2 * i);
-    const float by = st.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
-    l += by * st.y;
-    if (on) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(sums + (int64_t)i * c.dim + 4 * lane);
+    for (int i = wave * each_wave + side; i < parts; i += kFewWaves * each_wave) {
+      const int64_t e = at + i * stride;
+      const f32x2 st = *reinterpret_cast<const f32x2*>(stats + 2 * e);
+      const f32x4 o = *reinterpret_cast<const f32x4*>(sums + e * c.dim + d);
+      const float by = st.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
+      l += by * st.y;
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += by * o[j];
     }
   }
+  for (int s = 1; s < each_wave; ++s) {  // the parts side by side, onto the first
+    const float l2 = __shfl(l, lane + s * wide, 64);
+    float v2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v2[j] = __shfl(v[j], lane + s * wide, 64);
+    if (side == 0) {
+      l += l2;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += v2[j];
+    }
+  }
+  if (side == 0) *reinterpret_cast<f32x4*>(&part[wave][d]) = f32x4{v[0], v[1], v[2], v[3]};
+  if (lane == 0) part_l[wave] = l;
+  __syncthreads();
+  if (wave > 0 || side > 0) return;
+#pragma unroll
+  for (int w = 1; w < kFewWaves; ++w) {
+    l += part_l[w];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += part[w][d + j];
+  }
+  l = __shfl(l, 0, 64);
   const float by = l == 0.0f ? 0.0f : global_decode(c.global_v) / l;
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] *= by;
-  if (on) kv_store4(dt, a.out, row * c.dim + 4 * lane, v);
+  kv_store4(dt, a.out, row * c.dim + d, v);
   if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? kNone : (top - kBias + __builtin_log2f(l)) * kLn2;
+}
+
+__global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt) {
+  const int b = blockIdx.y;
+  const int qi = blockIdx.x / a.query_heads, qh = blockIdx.x - qi * a.query_heads;
+  const int head = qh / a.groups, r = qi * a.groups + qh - head * a.groups;
+  const int64_t each = kv_units_each(c, a, sh);
+  KvScan scan;
+  int base = 0;
+  for (kv_scan(c, a, sh.rows, 0, 0, scan); b >= base + 64;) {
+    base += 64;
+    kv_scan(c, a, sh.rows, base, scan.after, scan);
+  }
+  const KvRange rg = kv_range_of(scan, b - base);
+  if (qi >= rg.n) return;
+  const int units = __builtin_amdgcn_readlane(scan.units, b - base);
+  const int64_t u0 = kv_readlane(scan.first, b - base) + (int64_t)head * units;
+  const int64_t g0 = u0 / each, g1 = (u0 + units - 1) / each;
+  if (g0 == g1) return;  // one workgroup had it all
+  const int parts = (int)(g1 - g0) + 1;
+  const int64_t at = (g0 + (int64_t)b * c.heads + head) * sh.rows + r;
+  kv_join(c, a, dt, sh.sums, sh.stats, at, sh.rows, parts, (int64_t)(rg.first + qi) * a.query_heads + qh);
+}
+
+__global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt) {
+  const int qi = blockIdx.x / a.query_heads, qh = blockIdx.x - qi * a.query_heads;
+  const int r = qi * a.groups + qh % a.groups;  // its row among those of its kv head
+  const KvRange rg = kv_range(a, blockIdx.y, r / kManyRows * kManyRows, kManyRows);
+  if (qi >= rg.n) return;
+  const int parts = rg.hi > rg.lo ? (rg.hi - rg.lo + sp.chunk - 1) / sp.chunk : 1;
+  const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + qh;
+  kv_join(c, a, dt, sp.sums, sp.stats, row * sp.splits, 1, parts, row);
 }
 
 // ----------------------------------------------------------------- launches
 
 struct KvPlan {
-  int row_tiles, tile_rows;  // rows a workgroup takes, and how many such tiles a sequence and kv head has
-  int chunk, splits;
+  bool few;
+  int mt, groups;                 // few rows: row tiles of 16, workgroups
+  int row_tiles, chunk, splits;   // many rows
   size_t sums_bytes, bytes;
 };
 
-KvPlan kv_plan(const KvCache& c, const KvAttention& a) {
-  KvPlan p;
+constexpr int few_groups(int dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : dim <= 192 ? 3 : 4; }
+
+// Up to 32 rows a (sequence, kv head) the keys are streamed once past all of
+// them, which the few-rows kernel does at the speed of memory; more rows are
+// matrix work.
+KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
+  KvPlan p{};
   const int64_t rows = (int64_t)a.max_queries * a.groups;
-  p.tile_rows = rows <= 16 ? 16 : 32;
-  p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   int64_t keys = a.max_keys;
-  if (a.window > 0) keys = keys < (int64_t)a.window + a.max_queries ? keys : (int64_t)a.window + a.max_queries;
-  const int64_t items = (int64_t)a.seqs * c.heads * p.row_tiles;
-  const int64_t want = 8 * device_cu_count();
-  int64_t splits = (want + items - 1) / items;
-  const int64_t most = (keys + kFewStep - 1) / kFewStep;
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
-  int64_t chunk = (keys + splits - 1) / splits;
-  chunk = (chunk + kFewStep - 1) / kFewStep * kFewStep;
-  if (chunk > 2048) chunk = 2048;
-  if (chunk < kFewStep) chunk = kFewStep;
-  splits = keys > 0 ? (keys + chunk - 1) / chunk : 1;
-  p.chunk = (int)chunk;
-  p.splits = (int)splits;
-  const int64_t parts = a.tokens * a.query_heads * splits;
-  p.sums_bytes = splits > 1 ? ((size_t)parts * c.dim * 4 + 255) / 256 * 256 : 0;
-  p.bytes = splits > 1 ? p.sums_bytes + ((size_t)parts * 8 + 255) / 256 * 256 : 0;
+  if (a.window > 0 && keys > (int64_t)a.window + a.max_queries) keys = (int64_t)a.window + a.max_queries;
+  const int64_t pairs = (int64_t)a.seqs * c.heads;
+  size_t parts;
+  p.few = rows <= 32;
+  if (p.few) {
+    p.mt = rows <= 16 ? 1 : 2;
+    // as many workgroups as run at once, but no more than there can be units
+    const int64_t units = pairs * (keys > kFewStep ? (keys + kFewStep - 1) / kFewStep : 1);
+    const int64_t most = (int64_t)device_cu_count() * few_occupancy(few_groups(c.dim), p.mt, split);
+    p.groups = (int)(units < most ? units : most);
+    parts = units > pairs ? (size_t)(p.groups + pairs) * 16 * p.mt : 0;  // one unit a pair: nothing to join
+  } else {
+    p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
+    int64_t splits = 2 * device_cu_count() / (pairs * p.row_tiles);
+    const int64_t most = keys / 256;
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    p.chunk = (int)((keys / splits + 64) / 64 * 64);
+    p.splits = keys > 0 ? (int)((keys + p.chunk - 1) / p.chunk) : 1;
+    parts = p.splits > 1 ? (size_t)a.tokens * a.query_heads * p.splits : 0;
+  }
+  p.sums_bytes = (parts * c.dim * 4 + 255) / 256 * 256;
+  p.bytes = p.sums_bytes + (parts * 8 + 255) / 256 * 256;
   return p;
 }
 
@@ -624,17 +1141,16 @@ hipError_t allow_lds(K* kernel, bool (&set)[64]) {
 }
 
 template <int NG, bool EXACT>
-hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvSplit& sp, const KvPlan& p, int dt, bool q_vec,
+hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvShare& sh, const KvPlan& p, int dt, bool q_vec,
                       hipStream_t s) {
-  const dim3 grid((unsigned)(p.splits * c.heads * p.row_tiles), a.seqs);
-  const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 4 * (p.chunk / c.page_size + 2);
+  const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 4 * kFewPages;
 #define KV_FEW(MT, SPLIT)                                                                         \
   do {                                                                                            \
     static bool set[64];                                                                          \
     if (hipError_t e = allow_lds(&kv_few_kernel<NG, MT, SPLIT, EXACT>, set)) return e;            \
-    kv_few_kernel<NG, MT, SPLIT, EXACT><<<grid, 256, lds, s>>>(c, a, sp, dt, q_vec);              \
+    kv_few_kernel<NG, MT, SPLIT, EXACT><<<p.groups, 256, lds, s>>>(c, a, sh, dt, q_vec);          \
   } while (0)
-  if (p.tile_rows == 16) {
+  if (p.mt == 1) {
     if (dt == kF32) KV_FEW(1, 2); else KV_FEW(1, 1);
   } else {
     if (dt == kF32) KV_FEW(2, 2); else KV_FEW(2, 1);
@@ -643,27 +1159,59 @@ hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvSplit& sp,
   return hipGetLastError();
 }
 
+template <int NG, bool EXACT>
+hipError_t launch_many(const KvCache& c, const KvAttention& a, const KvChunks& sp, int dt, bool q_vec, hipStream_t s) {
+  const dim3 grid((unsigned)(sp.row_tiles * c.heads * sp.splits), a.seqs);
+#define KV_MANY(SPLIT)                                                                            \
+  do {                                                                                            \
+    static bool set[64];                                                                          \
+    if (hipError_t e = allow_lds(&kv_many_kernel<NG, SPLIT, EXACT>, set)) return e;               \
+    kv_many_kernel<NG, SPLIT, EXACT><<<grid, 256, many_lds(NG), s>>>(c, a, sp, dt, q_vec);        \
+  } while (0)
+  if (dt == kF32) KV_MANY(2); else KV_MANY(1);
+#undef KV_MANY
+  return hipGetLastError();
+}
+
+template <int NG, bool EXACT>
+hipError_t launch(const KvCache& c, const KvAttention& a, const KvPlan& p, int dt, float* sums, float* stats,
+                  bool q_vec, hipStream_t s) {
+  const dim3 rows((unsigned)(a.max_queries * a.query_heads), a.seqs);
+  if (p.few) {
+    const KvShare sh{p.groups, 16 * p.mt, sums, stats};
+    const hipError_t e = launch_few<NG, EXACT>(c, a, sh, p, dt, q_vec, s);
+    if (e != hipSuccess || p.bytes == 0) return e;
+    kv_join_few_kernel<<<rows, 256, 0, s>>>(c, a, sh, dt);
+  } else {
+    const KvChunks sp{p.chunk, p.splits, p.row_tiles, sums, stats};
+    const hipError_t e = launch_many<NG, EXACT>(c, a, sp, dt, q_vec, s);
+    if (e != hipSuccess || p.bytes == 0) return e;
+    kv_join_many_kernel<<<rows, 256, 0, s>>>(c, a, sp, dt);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t kv_attention_workspace(const KvCache& c, const KvAttention& a) { return kv_plan(c, a).bytes; }
+size_t kv_attention_workspace(const KvCache& c, const KvAttention& a) {
+  const size_t one = kv_plan(c, a, 1).bytes, two = kv_plan(c, a, 2).bytes;
+  return one > two ? one : two;
+}
 
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s) {
-  const KvPlan p = kv_plan(c, a);
-  KvSplit sp{p.chunk, p.splits, reinterpret_cast<float*>(workspace),
-             reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + p.sums_bytes)};
+  const KvPlan p = kv_plan(c, a, dt == kF32 ? 2 : 1);
+  float* sums = reinterpret_cast<float*>(workspace);
+  float* stats = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + p.sums_bytes);
   const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && (a.q_token | a.q_head) % 8 == 0;
-  hipError_t e;
-  if (c.dim == 64) e = launch_few<1, true>(c, a, sp, p, dt, q_vec, s);
-  else if (c.dim == 128) e = launch_few<2, true>(c, a, sp, p, dt, q_vec, s);
-  else if (c.dim == 256) e = launch_few<4, true>(c, a, sp, p, dt, q_vec, s);
-  else if (c.dim < 64) e = launch_few<1, false>(c, a, sp, p, dt, q_vec, s);
-  else if (c.dim < 128) e = launch_few<2, false>(c, a, sp, p, dt, q_vec, s);
-  else if (c.dim <= 192) e = launch_few<3, false>(c, a, sp, p, dt, q_vec, s);
-  else e = launch_few<4, false>(c, a, sp, p, dt, q_vec, s);
-  if (e != hipSuccess || p.splits == 1) return e;
-  const dim3 grid((unsigned)(((int64_t)a.max_queries * a.query_heads + 3) / 4), a.seqs);
-  kv_join_kernel<<<grid, 256, 0, s>>>(c, a, sp, p.tile_rows, dt);
-  return hipGetLastError();
+  switch (c.dim) {
+    case 64: return launch<1, true>(c, a, p, dt, sums, stats, q_vec, s);
+    case 128: return launch<2, true>(c, a, p, dt, sums, stats, q_vec, s);
+    case 256: return launch<4, true>(c, a, p, dt, sums, stats, q_vec, s);
+  }
+  if (c.dim < 64) return launch<1, false>(c, a, p, dt, sums, stats, q_vec, s);
+  if (c.dim < 128) return launch<2, false>(c, a, p, dt, sums, stats, q_vec, s);
+  if (c.dim <= 192) return launch<3, false>(c, a, p, dt, sums, stats, q_vec, s);
+  return launch<4, false>(c, a, p, dt, sums, stats, q_vec, s);
 }
 
 }  // namespace nvfp4
