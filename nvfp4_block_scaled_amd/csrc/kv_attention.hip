@@ -37,18 +37,17 @@ constexpr float kNone = -__builtin_huge_valf();
 //
 // Small weights.  Below 2^-14 a float16 loses bits, and in a 4-bit cache an
 // output may consist of small weights alone (the keys with large weights
-// hold an exact 0 there).  So weights below KvSmall::kLimit, 2^-26 of the
+// hold an exact 0 there).  So weights below KvSmall::kLimitLog2, 2^-26 of the
 // largest (float32 queries, whose second float16 is 2^-11 smaller: 2^-15),
-// enter the product in a further pass, times 2^kShift with the output scaled
-// along, and so keep their bits.  Tiles without such weights, nearly all
-// unless a row's scores spread over more than 18 nats, take one pass.
+// enter the product apart, in bands of 2^kShift with the output scaled along,
+// and so keep their bits.  Tiles without such weights, nearly all unless a
+// row's scores spread over more than 18 nats, skip this.
 constexpr float kLag = 3.0f, kBias = 12.0f;
 template <int SPLIT> struct KvSmall {
   static constexpr float kLimitLog2 = SPLIT == 2 ? -3.0f : -14.0f;
-  static constexpr float kLimit = SPLIT == 2 ? 0x1p-3f : 0x1p-14f;
   static constexpr float kShift = SPLIT == 2 ? 18.0f : 29.0f;
   static constexpr float kUp = SPLIT == 2 ? 0x1p18f : 0x1p29f, kDown = SPLIT == 2 ? 0x1p-18f : 0x1p-29f;
-  static constexpr int kPasses = SPLIT == 2 ? 4 : 3;  // outputs stay below 2^44 2^58
+  static constexpr int kBands = SPLIT == 2 ? 4 : 3;  // outputs stay below 2^44 2^58
 };
 
 // ----------------------------------------------------------------- ranges
@@ -159,6 +158,28 @@ __device__ __forceinline__ f16x8 kv_read_transposed(const uint8_t* lo, const uin
   return __builtin_bit_cast(f16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// The same value, computed where it stands: keeps what a rare path derives from
+// it out of the registers of the loop around that path.
+__device__ __forceinline__ int opaque(int v) {
+  asm("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ float opaque(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedDsRead = 0x100;  // groups of sched_group_barrier
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // ----------------------------------------------------------------- queries
 
 // 8 elements of a query row as they lie in memory.
@@ -204,11 +225,14 @@ __device__ __forceinline__ void kv_unpack_query(const KvRaw<SPLIT>& r, int dt, f
   }
 }
 template <int SPLIT>
-__device__ __forceinline__ float kv_query_top(const KvRaw<SPLIT>& r, int dt) {
+__device__ __forceinline__ float kv_query_top(KvRaw<SPLIT>& r, int dt) {
   float x[8], top = 0.0f;
   kv_unpack_query<SPLIT>(r, dt, x);
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(x[i]));
+  // unpacked again when they are converted, rather than kept as floats
+#pragma unroll
+  for (int i = 0; i < 4 * SPLIT; ++i) r.w[i] = opaque((int)r.w[i]);
   return top;
 }
 // Times `power` as one or two float16.
@@ -520,27 +544,24 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     if (more) load(c.v_codes, c.v_scales, vt);
     // probabilities
     const bool masked = live != 0xFFFFFFFFu || tile < all_lo || tile + kFewTile > all_hi;
-    float w[MT][8];
-    bool small = false;
+    float x[MT][8], low = 0.0f;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = s[m][i >> 2][i & 3] * factor[m];
+      for (int i = 0; i < 8; ++i) x[m][i] = s[m][i >> 2][i & 3] * factor[m];
       if (masked) {
+        const int h = 4 * opaque(quarter);
+        const int lo = see_lo[m] - tile - h, hi = see_hi[m] - tile - h;
+        const uint32_t have = live >> h;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int key = 16 * (i >> 2) + 4 * quarter + (i & 3);
-          const bool see = ((live >> key) & 1u) && tile + key >= see_lo[m] && tile + key < see_hi[m];
-          x[i] = see ? x[i] : kNone;
+          const int key = 16 * (i >> 2) + (i & 3);
+          x[m][i] = (((have >> key) & 1u) & (key >= lo) & (key < hi)) ? x[m][i] : kNone;
         }
       }
-      float top = x[0], low = x[0];
+      float top = fmaxf(x[m][0], x[m][1]);
 #pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        top = fmaxf(top, x[i]);
-        low = fminf(low, x[i]);
-      }
+      for (int i = 2; i < 8; i += 2) top = max3(top, x[m][i], x[m][i + 1]);
       if (__any(top > m_run[m] + kLag)) {  // rare once a row has met its large scores
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -554,38 +575,18 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[m][d][i] *= keep;
       }
-      small |= low - sub[m] < KvSmall<SPLIT>::kLimitLog2;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[m][i] = __builtin_amdgcn_exp2f(x[i] - sub[m]);
-        l_run[m] += w[m][i];
-      }
+      for (int i = 0; i < 8; ++i) x[m][i] -= sub[m];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) low = min3(low, x[m][i], x[m][i + 1]);
     }
     // output: 16 values (rows) of V^T at a time, keys 4 quarter + 16 u + (0 .. 3) a lane
-    bool again = __any(small);
-    for (int pass = 1;; ++pass) {
-      float rest[MT][8];
-      if (again) {
-        bool any = false;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bool tiny = w[m][i] < KvSmall<SPLIT>::kLimit;
-            rest[m][i] = tiny ? w[m][i] * KvSmall<SPLIT>::kUp : 0.0f;
-            any |= rest[m][i] > 0.0f;
-            if (tiny) w[m][i] = 0.0f;
-          }
-        again = __any(any) && pass < KvSmall<SPLIT>::kPasses;
-      }
-      f16x8 p[MT][SPLIT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[m][0][i] = (_Float16)w[m][i];
-          if constexpr (SPLIT == 2) p[m][SPLIT - 1][i] = (_Float16)(w[m][i] - (float)(_Float16)w[m][i]);
-        }
+    f16x8 p[MT][SPLIT];
+    auto weight = [&](int m, int i, float w) {
+      p[m][0][i] = (_Float16)w;
+      if constexpr (SPLIT == 2) p[m][SPLIT - 1][i] = (_Float16)(w - (float)(_Float16)w);
+    };
+    auto multiply = [&]() {
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         const uint8_t* at = mine + (4 * quarter + (col >> 2)) * RB + 32 * d + 8 * (col & 3);
@@ -596,29 +597,59 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
           for (int e = SPLIT - 1; e >= 0; --e)
             acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[m][e], acc[m][d], 0, 0, 0);
       }
-      if (!again) {
-        if (pass > 1) {
-          float down = KvSmall<SPLIT>::kDown;
-          for (int i = 2; i < pass; ++i) down *= KvSmall<SPLIT>::kDown;
+    };
+    if (__any(low < KvSmall<SPLIT>::kLimitLog2)) {  // KvSmall: the bands of small weights, then the rest
+      float shift = KvSmall<SPLIT>::kShift, up = KvSmall<SPLIT>::kUp, down = KvSmall<SPLIT>::kDown;
+      bool any = false;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+        for (int i = 0; i < 8; ++i) any |= (x[m][i] < KvSmall<SPLIT>::kLimitLog2) & (x[m][i] > kNone);
+      for (int band = 1; band < KvSmall<SPLIT>::kBands && __any(any); ++band) {
+        any = false;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[m][d][i] *= down;
-        }
-        break;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float t = x[m][i] + shift;
+            const bool lower = (t < KvSmall<SPLIT>::kLimitLog2) & (band < KvSmall<SPLIT>::kBands - 1);
+            const bool in = (t < KvSmall<SPLIT>::kLimitLog2 + KvSmall<SPLIT>::kShift) & !lower;
+            const float w = in ? __builtin_amdgcn_exp2f(t) : 0.0f;
+            l_run[m] += w * down;
+            any |= lower & (t > kNone);
+            weight(m, i, w);
+          }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][d][i] *= up;
+        multiply();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][d][i] *= down;
+        shift += KvSmall<SPLIT>::kShift;
+        up *= KvSmall<SPLIT>::kUp;
+        down *= KvSmall<SPLIT>::kDown;
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][d][i] *= KvSmall<SPLIT>::kUp;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[m][i] = rest[m][i];
-      }
+        for (int i = 0; i < 8; ++i) x[m][i] = x[m][i] < KvSmall<SPLIT>::kLimitLog2 ? kNone : x[m][i];
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __builtin_amdgcn_exp2f(x[m][i]);
+        l_run[m] += w;
+        weight(m, i, w);
+      }
+    multiply();
   }
   }
 
@@ -701,17 +732,6 @@ struct KvChunks {
   float* stats;       // [tokens][query_heads][splits][2]: maximum (log2), sum
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
-
 template <int NG, int SPLIT, bool EXACT>
 __global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1))
 kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
@@ -738,23 +758,24 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   const int key_of = BOTH ? threadIdx.x >> 2 : (threadIdx.x & 127) >> 2;
   const bool second = !BOTH && threadIdx.x >= 128;
   const int g0 = NG * (threadIdx.x & 3);
-  auto lookup = [&](int tile) {  // the page of this thread's key, -1 where there is none
-    const int j = tile + key_of;
-    if (j >= end) return -1;
-    const int page = a.page_table[b * a.table_stride + kv_div(j, c.page_div)];
-    return page < c.pages ? page : -1;
+  // The page number of this thread's key, as it stands in the table (checked
+  // when it is used, a tile later: nothing may wait for it here).  Past the
+  // end the last key's.
+  auto lookup = [&](int tile) {
+    return a.page_table[b * a.table_stride + kv_div(min(tile + key_of, end - 1), c.page_div)];
   };
   KvGroups<NG> kt, vt;
   int live = 0;
   auto load = [&](int tile, int page) {
     const int j = tile + key_of;
-    live = (page >= 0) | (j >= end);  // past the end every row's mask holds
-    const int64_t row = page >= 0 ? kv_row(c, page, head, j - (int)kv_div(j, c.page_div) * c.page_size) : 0;
+    const bool there = (page >= 0) & (page < c.pages) & (j < end);
+    live = there | (j >= end);  // past the end every row's mask holds
+    const int64_t row = there ? kv_row(c, page, head, j - (int)kv_div(j, c.page_div) * c.page_size) : 0;
     if constexpr (BOTH) {
-      kt = kv_load<NG, EXACT>(c.k_codes, c.k_scales, row, c.dim, g0, page >= 0);
-      vt = kv_load<NG, EXACT>(c.v_codes, c.v_scales, row, c.dim, g0, page >= 0);
+      kt = kv_load<NG, EXACT>(c.k_codes, c.k_scales, row, c.dim, g0, there);
+      vt = kv_load<NG, EXACT>(c.v_codes, c.v_scales, row, c.dim, g0, there);
     } else {
-      kt = kv_load<NG, EXACT>(second ? c.v_codes : c.k_codes, second ? c.v_scales : c.k_scales, row, c.dim, g0, page >= 0);
+      kt = kv_load<NG, EXACT>(second ? c.v_codes : c.k_codes, second ? c.v_scales : c.k_scales, row, c.dim, g0, there);
     }
   };
   auto store = [&](int buf) {
@@ -773,8 +794,11 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
       for (int i = 0; i < 2 * NG; ++i) *reinterpret_cast<f16x8*>(at + 16 * i) = v[i];
     }
   };
-  int page = lookup(begin);
-  int page2 = lookup(begin + TILE);
+  int page = 0, page2 = 0;
+  if (begin < end) {
+    page = lookup(begin);
+    page2 = lookup(begin + TILE);
+  }
 
   // queries: row `col` of this wave's 32
   const int r = row0 + 32 * wave + col;
@@ -802,20 +826,12 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   const int pos = rg.context - rg.n + qi;
   const int see_hi = !row_live ? 0 : a.causal ? min(end, pos + 1) : end;
   const int see_lo = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  // keys that any, and that every row of this wave sees
-  int any_lo = 0, any_hi = end, all_lo = 0, all_hi = end;
-  {
-    const int w0 = row0 + 32 * wave;
-    if (w0 >= rows) any_hi = 0;
-    else if (a.causal) {
-      const int q0 = w0 / a.groups, q1 = min(w0 + 31, rows - 1) / a.groups, base = rg.context - rg.n;
-      any_hi = min(end, base + q1 + 1);
-      all_hi = min(end, base + q0 + 1);
-      if (a.window > 0) {
-        any_lo = max(0, base + q0 - a.window + 1);
-        all_lo = max(0, base + q1 - a.window + 1);
-      }
-    }
+  // keys that every row of this wave sees
+  int all_lo = 0, all_hi = end;
+  if (a.causal) {
+    const int w0 = min(row0 + 32 * wave, rows - 1), base = rg.context - rg.n;
+    all_hi = min(end, base + w0 / a.groups + 1);
+    if (a.window > 0) all_lo = max(0, base + min(w0 + 31, rows - 1) / a.groups - a.window + 1);
   }
 
   f32x16 acc[DB];
@@ -839,31 +855,37 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   for (int tile = begin; tile < end; tile += TILE, buf ^= 1) {
     const uint8_t* kb = lds + buf * BUF;
     const uint8_t* vb = kb + TILE * KROW;
-    const bool busy = tile < any_hi && tile + TILE > any_lo;  // wave-uniform
     f32x16 s[SUB];
-    if (busy) {
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
+    for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+      for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-          const f16x8 kf = *reinterpret_cast<const f16x8*>(kb + (32 * u + col) * KROW + 32 * t + 16 * half);
+      for (int t = 0; t < STEPS; ++t) {
+        const f16x8 kf = *reinterpret_cast<const f16x8*>(kb + (32 * u + col) * KROW + 32 * t + 16 * half);
 #pragma unroll
-          for (int e = SPLIT - 1; e >= 0; --e)
-            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[e][t], s[u], 0, 0, 0);
-        }
+        for (int e = SPLIT - 1; e >= 0; --e)
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[e][t], s[u], 0, 0, 0);
       }
     }
-    if (tile + TILE < end) {
-      store(buf ^ 1);
-      if (tile + 2 * TILE < end) load(tile + 2 * TILE, page);
-      page = page2;
-      page2 = lookup(tile + 4 * TILE);
+    store(buf ^ 1);  // (after the last tile: what lies there is not read)
+    if constexpr (SPLIT == 1 && BOTH) {
+      // K fragments two products ahead, the decoding of the next tile between the products
+      __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 3, 0);
+#pragma unroll
+      for (int i = 0; i < SUB * STEPS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedValu, 6, 0);
+      }
     }
-    if (busy) {
+    if (tile + 2 * TILE < end) load(tile + 2 * TILE, page);
+    page = page2;
+    page2 = lookup(tile + 4 * TILE);
+    {
       if (tile < all_lo || tile + TILE > all_hi) {
-        const int lo = see_lo - tile - 4 * half, hi = see_hi - tile - 4 * half;
+        const int h = opaque(half);
+        const int lo = see_lo - tile - 4 * h, hi = see_hi - tile - 4 * h;
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -876,11 +898,12 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 #pragma unroll
       for (int i = 0; i < 2 * SUB; ++i) have &= exists[buf][i];
       if (have != ~0ull) {  // pages that are not there
+        const int h = opaque(half);
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int key = 8 * (i >> 2) + 4 * half + (i & 3);  // of this half tile
+            const int key = 8 * (i >> 2) + 4 * h + (i & 3);  // of this half tile
             if (!(exists[buf][2 * u + (i >> 3)] >> (4 * (key & 15)) & 1)) s[u][i] = kNone;
           }
       }
@@ -906,37 +929,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[d][i] *= keep;
       }
-      int small = __builtin_amdgcn_readfirstlane(__any(low - sub < KvSmall<SPLIT>::kLimitLog2));
-      float shift = 0.0f, down = 1.0f;  // of the present band of small weights
-      for (int pass = 1;; ++pass) {
-        asm("" : "+s"(small));  // one copy of the products below for both kinds of tile
-        f16x8 p[SUB][2][SPLIT];
-        bool again = false;
-        if (!small) {
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], factor, -sub));
-              l_run += w;
-              p[u][i >> 3][0][i & 7] = (_Float16)w;
-              if constexpr (SPLIT == 2) p[u][i >> 3][SPLIT - 1][i & 7] = (_Float16)(w - (float)(_Float16)w);
-            }
-        } else {  // one pass per band of weights (KvSmall)
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float t = __builtin_fmaf(s[u][i], factor, -sub) + shift;
-              const bool below = (t < KvSmall<SPLIT>::kLimitLog2) & (pass < KvSmall<SPLIT>::kPasses);
-              const bool above = (pass > 1) & (t >= KvSmall<SPLIT>::kLimitLog2 + KvSmall<SPLIT>::kShift);
-              const float w = (below | above) ? 0.0f : __builtin_amdgcn_exp2f(t);
-              l_run += w * down;
-              again |= below & (t > kNone);
-              p[u][i >> 3][0][i & 7] = (_Float16)w;
-              if constexpr (SPLIT == 2) p[u][i >> 3][SPLIT - 1][i & 7] = (_Float16)(w - (float)(_Float16)w);
-            }
-        }
+      auto multiply = [&](const f16x8(&p)[SUB][2][SPLIT]) {
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -950,16 +943,75 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
               for (int e = SPLIT - 1; e >= 0; --e)
                 acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[u][t][e], acc[d], 0, 0, 0);
             }
-        if (!small) break;
-        const bool last = !__any(again);
-        const float by = last ? down : KvSmall<SPLIT>::kUp;
+      };
+      f16x8 p[SUB][2][SPLIT];
+      auto weight = [&](int u, int i, float w) {
+        p[u][i >> 3][0][i & 7] = (_Float16)w;
+        if constexpr (SPLIT == 2) p[u][i >> 3][SPLIT - 1][i & 7] = (_Float16)(w - (float)(_Float16)w);
+      };
+      if (__any(low - sub < KvSmall<SPLIT>::kLimitLog2)) {  // KvSmall: the bands of small weights, then the rest
+        const float f = opaque(factor), below = opaque(sub);
+        float shift = KvSmall<SPLIT>::kShift, up = KvSmall<SPLIT>::kUp, down = KvSmall<SPLIT>::kDown;
+        bool any = false;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[d][i] *= by;
-        if (last) break;
-        shift += KvSmall<SPLIT>::kShift;
-        down *= KvSmall<SPLIT>::kDown;
+          for (int i = 0; i < 16; ++i) {
+            const float t = __builtin_fmaf(s[u][i], f, -below);
+            any |= (t < KvSmall<SPLIT>::kLimitLog2) & (t > kNone);
+          }
+        for (int band = 1; band < KvSmall<SPLIT>::kBands && __any(any); ++band) {
+          any = false;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float t = __builtin_fmaf(s[u][i], f, -below) + shift;
+              const bool lower = (t < KvSmall<SPLIT>::kLimitLog2) & (band < KvSmall<SPLIT>::kBands - 1);
+              const bool in = (t < KvSmall<SPLIT>::kLimitLog2 + KvSmall<SPLIT>::kShift) & !lower;
+              const float w = in ? __builtin_amdgcn_exp2f(t) : 0.0f;
+              l_run += w * down;
+              any |= lower & (t > kNone);
+              weight(u, i, w);
+            }
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] *= up;
+          multiply(p);
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] *= down;
+          shift += KvSmall<SPLIT>::kShift;
+          up *= KvSmall<SPLIT>::kUp;
+          down *= KvSmall<SPLIT>::kDown;
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[u][i] = __builtin_fmaf(s[u][i], f, -below) < KvSmall<SPLIT>::kLimitLog2 ? kNone : s[u][i];
+      }
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], factor, -sub));
+          l_run += w;
+          weight(u, i, w);
+        }
+      multiply(p);
+      if constexpr (SPLIT == 1 && BOTH) {
+        // the first keys' probabilities, then products among the computation of the others'
+        __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * SUB * DB; ++i) {
+          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(kSchedValu, 7, 0);
+        }
       }
     }
     lds_barrier();
