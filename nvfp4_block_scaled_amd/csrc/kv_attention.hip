@@ -168,7 +168,6 @@ __device__ __forceinline__ float opaque(float v) {
   asm("" : "+v"(v));
   return v;
 }
-constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedDsRead = 0x100;  // groups of sched_group_barrier
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -778,21 +777,19 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
       kt = kv_load<NG, EXACT>(second ? c.v_codes : c.k_codes, second ? c.v_scales : c.k_scales, row, c.dim, g0, there);
     }
   };
-  auto store = [&](int buf) {
-    uint8_t* to = lds + buf * BUF;
+  // Decodes piece i (8 values) of what was loaded and writes it to buffer `buf`.
+  constexpr int PIECES = (BOTH ? 4 : 2) * NG;
+  auto store_piece = [&](int buf, int i) {
+    const bool of_v = BOTH ? i >= 2 * NG : second;
+    const KvGroups<NG>& x = BOTH && i >= 2 * NG ? vt : kt;
+    const int w = BOTH && i >= 2 * NG ? i - 2 * NG : i;
+    const f16x2 sc = kv_scale2(w < 4 ? x.s : x.s >> 16);
+    uint8_t* at = lds + buf * BUF + (of_v ? TILE * KROW + key_of * VROW : key_of * KROW) + 32 * g0 + 16 * w;
+    *reinterpret_cast<f16x8*>(at) = kv_decode8(x.w[w], w & 2 ? sc.y : sc.x);
+  };
+  auto store_flags = [&](int buf) {
     const uint64_t bits = __ballot(live != 0);
     if (lane == 0) exists[buf][wave] = bits;
-    f16x8 v[2 * NG];
-    kv_values<NG>(kt, v);
-    uint8_t* at = to + (second ? TILE * KROW + key_of * VROW : key_of * KROW) + 32 * g0;
-#pragma unroll
-    for (int i = 0; i < 2 * NG; ++i) *reinterpret_cast<f16x8*>(at + 16 * i) = v[i];
-    if constexpr (BOTH) {
-      kv_values<NG>(vt, v);
-      at = to + TILE * KROW + key_of * VROW + 32 * g0;
-#pragma unroll
-      for (int i = 0; i < 2 * NG; ++i) *reinterpret_cast<f16x8*>(at + 16 * i) = v[i];
-    }
   };
   int page = 0, page2 = 0;
   if (begin < end) {
@@ -845,7 +842,9 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
     load(begin, page);
     page = page2;
     page2 = lookup(begin + 2 * TILE);
-    store(0);
+    store_flags(0);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) store_piece(0, i);
     if (begin + TILE < end) load(begin + TILE, page);
     page = page2;
     page2 = lookup(begin + 3 * TILE);
@@ -855,28 +854,33 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   for (int tile = begin; tile < end; tile += TILE, buf ^= 1) {
     const uint8_t* kb = lds + buf * BUF;
     const uint8_t* vb = kb + TILE * KROW;
+    // Scores.  The order is fixed by hand: K fragments kAhead products ahead,
+    // and the decoding of the next tile between the products.
     f32x16 s[SUB];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
+    for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+    store_flags(buf ^ 1);
+    {
+      constexpr int N = SUB * STEPS, kAhead = 3;
+      f16x8 kf[kAhead + 1];
+      auto fetch = [&](int n) {
+        kf[n % (kAhead + 1)] = *reinterpret_cast<const f16x8*>(kb + (32 * (n / STEPS) + col) * KROW +
+                                                               32 * (n % STEPS) + 16 * half);
+      };
 #pragma unroll
-      for (int t = 0; t < STEPS; ++t) {
-        const f16x8 kf = *reinterpret_cast<const f16x8*>(kb + (32 * u + col) * KROW + 32 * t + 16 * half);
+      for (int n = 0; n < kAhead; ++n) fetch(n);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (n + kAhead < N) fetch(n + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = SPLIT - 1; e >= 0; --e)
-          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[e][t], s[u], 0, 0, 0);
-      }
-    }
-    store(buf ^ 1);  // (after the last tile: what lies there is not read)
-    if constexpr (SPLIT == 1 && BOTH) {
-      // K fragments two products ahead, the decoding of the next tile between the products
-      __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 3, 0);
-#pragma unroll
-      for (int i = 0; i < SUB * STEPS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedValu, 6, 0);
+          s[n / STEPS] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[n % (kAhead + 1)], q[e][n % STEPS], s[n / STEPS], 0, 0, 0);
+        // (after the last tile: what is decoded then is not read)
+        if (n * PIECES / N != (n + 1) * PIECES / N) store_piece(buf ^ 1, n * PIECES / N);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (tile + 2 * TILE < end) load(tile + 2 * TILE, page);
@@ -929,20 +933,11 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[d][i] *= keep;
       }
-      auto multiply = [&](const f16x8(&p)[SUB][2][SPLIT]) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              const uint8_t* at = vb + (32 * u + 16 * t + 4 * half + ((lane & 15) >> 2)) * VROW + 64 * d +
-                                  32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-              const f16x8 vf = kv_read_transposed(at, at + 8 * VROW);
-#pragma unroll
-              for (int e = SPLIT - 1; e >= 0; --e)
-                acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[u][t][e], acc[d], 0, 0, 0);
-            }
+      // values 32 d .. of the 16 keys of group g, transposed
+      auto values_of = [&](int g, int d) {
+        const uint8_t* at = vb + (16 * g + 4 * half + ((lane & 15) >> 2)) * VROW + 64 * d +
+                            32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+        return kv_read_transposed(at, at + 8 * VROW);
       };
       f16x8 p[SUB][2][SPLIT];
       auto weight = [&](int u, int i, float w) {
@@ -978,7 +973,13 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
           for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[d][i] *= up;
-          multiply(p);
+#pragma unroll
+          for (int n = 0; n < 2 * SUB * DB; ++n) {
+            const f16x8 vf = values_of(n / DB, n % DB);
+#pragma unroll
+            for (int e = SPLIT - 1; e >= 0; --e)
+              acc[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[n / DB >> 1][n / DB & 1][e], acc[n % DB], 0, 0, 0);
+          }
 #pragma unroll
           for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -993,24 +994,36 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
           for (int i = 0; i < 16; ++i)
             s[u][i] = __builtin_fmaf(s[u][i], f, -below) < KvSmall<SPLIT>::kLimitLog2 ? kNone : s[u][i];
       }
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
+      // Output, in a fixed order too: V fragments kAhead products ahead, and the
+      // probabilities of the next 16 keys between the products of these.
+      {
+        constexpr int G = 2 * SUB, N = G * DB, kAhead = 3;
+        f16x8 vf[kAhead + 1];
+        auto fetch = [&](int n) { vf[n % (kAhead + 1)] = values_of(n / DB, n % DB); };
+        auto probability = [&](int g, int j) {
+          const int u = g >> 1, i = 8 * (g & 1) + j;
           const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], factor, -sub));
           l_run += w;
           weight(u, i, w);
-        }
-      multiply(p);
-      if constexpr (SPLIT == 1 && BOTH) {
-        // the first keys' probabilities, then products among the computation of the others'
-        __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 4, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 0);
+        };
 #pragma unroll
-        for (int i = 0; i < 2 * SUB * DB; ++i) {
-          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 2, 0);
-          __builtin_amdgcn_sched_group_barrier(kSchedValu, 7, 0);
+        for (int n = 0; n < kAhead; ++n) fetch(n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) probability(0, j);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int g = n / DB, d = n % DB;
+          if (n + kAhead < N) fetch(n + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int e = SPLIT - 1; e >= 0; --e)
+            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n % (kAhead + 1)], p[g >> 1][g & 1][e], acc[d], 0, 0, 0);
+          if (g + 1 < G) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j * DB / 8 == d) probability(g + 1, j);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
