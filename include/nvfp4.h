@@ -618,7 +618,7 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
  *   k_codes, v_codes    device uint8 [pages, heads, page_size, dim/2], 16-byte aligned
  *   k_scales, v_scales  device uint8 [pages, heads, page_size, dim/16], 16-byte aligned
  * page_size >= 1, dim a multiple of 16 and at most 256, pages * page_size <
- * 2^31.  The struct is read during the call only; the memory is the caller's.
+ * 2^31, heads < 2^15, the codes of one page below 4 GiB.  The struct is read during the call only; the memory is the caller's.
  * Slots that were never written may hold any bytes: no call reads a token
  * outside the slots or contexts that it is given.
  */

@@ -1208,6 +1208,8 @@ static nvfp4_status check_kv(const char* op, const nvfp4_kv_cache* cache, nvfp4_
       cache->pages * cache->page_size > INT32_MAX || cache->heads > 32767)
     return fail(NVFP4_ERR_UNSUPPORTED,
                 "[%s] pages * page_size must stay below 2^31 and heads below 32768.", op);
+  if (cache->heads * cache->page_size >= ((int64_t)1 << 32) / (cache->dim / 2))
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] a page's codes must stay below 4 GiB.", op);
   if (tokens < 0)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tokens (%lld) must be >= 0.", op, (long long)tokens);
   if (tokens > INT32_MAX || tokens * (cache->dim / 8) > INT32_MAX)

@@ -42,7 +42,7 @@ constexpr float kNone = -__builtin_huge_valf();
 // enter the product apart, in bands of 2^kShift with the output scaled along,
 // and so keep their bits.  Tiles without such weights, nearly all unless a
 // row's scores spread over more than 18 nats, skip this.
-constexpr float kLag = 3.0f, kBias = 12.0f;
+constexpr float kLag = 0.9f, kBias = 15.0f;
 template <int SPLIT> struct KvSmall {
   static constexpr float kLimitLog2 = SPLIT == 2 ? -3.0f : -14.0f;
   static constexpr float kShift = SPLIT == 2 ? 18.0f : 29.0f;
@@ -95,27 +95,49 @@ struct KvGroups {
   uint32_t w[2 * NG];
   uint32_t s;  // scale bytes
 };
-// EXACT: dim = 64 NG, so a lane's NG groups exist and lie on an 8 NG byte
-// boundary; otherwise groups from `groups` on are zeros.  live: the row exists.
-template <int NG, bool EXACT>
+// Where a head's codes start, counted from the start of the codes, by page:
+// byte page * page_bytes + head_bytes + offset * dim/2; its scales at an
+// eighth of that.  (page_bytes < 2^32: one multiply-add for the page.)
+struct KvPlace {
+  uint32_t page_bytes, row_bytes;
+  uint64_t head_bytes;
+};
+__device__ __forceinline__ KvPlace kv_place(const KvCache& c, int head) {
+  return KvPlace{(uint32_t)(c.heads * c.page_size) * (uint32_t)(c.dim / 2), (uint32_t)(c.dim / 2),
+                 (uint64_t)head * c.page_size * (c.dim / 2)};
+}
+__device__ __forceinline__ uint64_t kv_offset(const KvPlace& p, int page, int off) {
+  return (uint64_t)(uint32_t)page * p.page_bytes + (p.head_bytes + (uint64_t)(uint32_t)off * p.row_bytes);
+}
+
+template <bool ONCE, typename T>
+__device__ __forceinline__ T kv_fetch(const T* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+// Groups g0 .. g0 + NG - 1 of the row at `at` (kv_offset).  EXACT: dim = 64 NG,
+// so they exist and lie on an 8 NG byte boundary; otherwise groups from
+// dim / 16 on are zeros, as is a row that is not `live`.  ONCE: the row is
+// read by this workgroup only.
+template <int NG, bool EXACT, bool ONCE>
 __device__ __forceinline__ KvGroups<NG> kv_load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                int64_t row, int dim, int g0, bool live) {
+                                                uint64_t at, int dim, int g0, bool live) {
   KvGroups<NG> r;
 #pragma unroll
   for (int i = 0; i < 2 * NG; ++i) r.w[i] = 0u;
   r.s = 0u;
-  const uint8_t* c = codes + row * (dim / 2) + 8 * g0;
-  const uint8_t* s = scales + row * (dim / 16) + g0;
+  const uint8_t* c = codes + at + 8 * g0;
+  const uint8_t* s = scales + (at >> 3) + g0;
   if constexpr (EXACT) {
     if (live) {
       if constexpr (NG == 1) {
-        const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(c));
+        const u32x2 x = kv_fetch<ONCE>(reinterpret_cast<const u32x2*>(c));
         r.w[0] = x.x; r.w[1] = x.y;
         r.s = *s;
       } else {
 #pragma unroll
         for (int i = 0; i < NG / 2; ++i) {
-          const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c) + i);
+          const u32x4 x = kv_fetch<ONCE>(reinterpret_cast<const u32x4*>(c) + i);
           r.w[4 * i] = x.x; r.w[4 * i + 1] = x.y; r.w[4 * i + 2] = x.z; r.w[4 * i + 3] = x.w;
         }
         if constexpr (NG == 2) r.s = *reinterpret_cast<const uint16_t*>(s);
@@ -127,7 +149,7 @@ __device__ __forceinline__ KvGroups<NG> kv_load(const uint8_t* __restrict__ code
 #pragma unroll
     for (int i = 0; i < NG; ++i)
       if (live && i < have) {
-        const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(c) + i);
+        const u32x2 x = kv_fetch<ONCE>(reinterpret_cast<const u32x2*>(c) + i);
         r.w[2 * i] = x.x; r.w[2 * i + 1] = x.y;
         r.s |= (uint32_t)s[i] << (8 * i);
       }
@@ -413,6 +435,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   const bool whole = take == pair_units;
   const int begin = rg.lo + off * kFewStep, end = min(rg.hi, begin + take * kFewStep);
   const int rows = rg.n * a.groups;
+  const KvPlace place = kv_place(c, head);
   constexpr int row0 = 0;
   if (!first_run) __syncthreads();  // the last run's sums and page numbers have been read
   first_run = false;
@@ -482,25 +505,24 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   // A tile's keys are loaded once the last tile's are used up, its values
   // likewise: two thirds of a tile's time ahead, in the same registers.
   KvGroups<NG> kt[2], vt[2];
-  int64_t row[2];        // this lane's rows of the tile that is being loaded
+  uint64_t row[2];       // this lane's rows of the tile that is being loaded
+  bool there[2];
   uint32_t exists = 0u;  // which of its 32 keys do
   auto locate = [&](int at) {
     exists = 0u;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int j = at + 16 * u + col;
-      row[u] = -1;
-      if (j < to) {
-        const int pi = kv_div(j, c.page_div);
-        const int page = page_of[pi - p0];
-        if (page >= 0) row[u] = kv_row(c, page, head, j - pi * c.page_size);
-      }
-      exists |= (uint32_t)(__ballot(row[u] >= 0) & 0xFFFFu) << (16 * u);
+      const int j = min(at + 16 * u + col, to - 1);
+      const int pi = kv_div(j, c.page_div);
+      const int page = page_of[pi - p0];
+      there[u] = (page >= 0) & (at + 16 * u + col < to);
+      row[u] = kv_offset(place, page, j - pi * c.page_size);
+      exists |= (uint32_t)(__ballot(there[u]) & 0xFFFFu) << (16 * u);
     }
   };
   auto load = [&](const uint8_t* codes, const uint8_t* scales, KvGroups<NG>(&x)[2]) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) x[u] = kv_load<NG, EXACT>(codes, scales, max(row[u], (int64_t)0), c.dim, g0, row[u] >= 0);
+    for (int u = 0; u < 2; ++u) x[u] = kv_load<NG, EXACT, true>(codes, scales, row[u], c.dim, g0, there[u]);
   };
   int tile = from + wave * kFewTile;
   if (tile < to) {
@@ -721,7 +743,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 constexpr int kManyRows = 128;
 constexpr int many_tile(int NG) { return NG <= 2 ? 64 : 32; }
 constexpr int many_k_row(int NG) { return 128 * NG + 16; }
-constexpr int many_v_row(int NG) { return 128 * NG + 64; }
+constexpr int many_v_row(int NG) { return 128 * NG + 32; }
 constexpr int many_lds(int NG) { return 2 * many_tile(NG) * (many_k_row(NG) + many_v_row(NG)); }
 
 struct KvChunks {
@@ -765,16 +787,18 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   };
   KvGroups<NG> kt, vt;
   int live = 0;
+  const KvPlace place = kv_place(c, head);
   auto load = [&](int tile, int page) {
     const int j = tile + key_of;
     const bool there = (page >= 0) & (page < c.pages) & (j < end);
     live = there | (j >= end);  // past the end every row's mask holds
-    const int64_t row = there ? kv_row(c, page, head, j - (int)kv_div(j, c.page_div) * c.page_size) : 0;
+    const uint64_t row = kv_offset(place, page, j - (int)kv_div(j, c.page_div) * c.page_size);
     if constexpr (BOTH) {
-      kt = kv_load<NG, EXACT>(c.k_codes, c.k_scales, row, c.dim, g0, there);
-      vt = kv_load<NG, EXACT>(c.v_codes, c.v_scales, row, c.dim, g0, there);
+      kt = kv_load<NG, EXACT, false>(c.k_codes, c.k_scales, row, c.dim, g0, there);
+      vt = kv_load<NG, EXACT, false>(c.v_codes, c.v_scales, row, c.dim, g0, there);
     } else {
-      kt = kv_load<NG, EXACT>(second ? c.v_codes : c.k_codes, second ? c.v_scales : c.k_scales, row, c.dim, g0, there);
+      kt = kv_load<NG, EXACT, false>(second ? c.v_codes : c.k_codes, second ? c.v_scales : c.k_scales, row, c.dim, g0,
+                                     there);
     }
   };
   // Decodes piece i (8 values) of what was loaded and writes it to buffer `buf`.
@@ -861,7 +885,18 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+    uint64_t have = ~0ull;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) have &= exists[buf][i];
     store_flags(buf ^ 1);
+    // largest and smallest scores, in four chains; those of the first 32 keys
+    // while the others' products run
+    float top4[4], low4[4];
+    auto extremes = [&](int u, int k, bool begin_chain) {
+      const float a0 = s[u][4 * k], a1 = s[u][4 * k + 1], a2 = s[u][4 * k + 2], a3 = s[u][4 * k + 3];
+      top4[k] = max3(begin_chain ? fmaxf(a0, a1) : max3(top4[k], a0, a1), a2, a3);
+      low4[k] = min3(begin_chain ? fminf(a0, a1) : min3(low4[k], a0, a1), a2, a3);
+    };
     {
       constexpr int N = SUB * STEPS, kAhead = 3;
       f16x8 kf[kAhead + 1];
@@ -880,6 +915,10 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
           s[n / STEPS] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[n % (kAhead + 1)], q[e][n % STEPS], s[n / STEPS], 0, 0, 0);
         // (after the last tile: what is decoded then is not read)
         if (n * PIECES / N != (n + 1) * PIECES / N) store_piece(buf ^ 1, n * PIECES / N);
+        if (SUB == 2 && n >= STEPS + 2 && n < STEPS + 4) {
+          extremes(0, 2 * (n - STEPS - 2), true);
+          extremes(0, 2 * (n - STEPS - 2) + 1, true);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -887,7 +926,8 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
     page = page2;
     page2 = lookup(tile + 4 * TILE);
     {
-      if (tile < all_lo || tile + TILE > all_hi) {
+      const bool edge = tile < all_lo || tile + TILE > all_hi, holes = have != ~0ull;
+      if (edge) {
         const int h = opaque(half);
         const int lo = see_lo - tile - 4 * h, hi = see_hi - tile - 4 * h;
 #pragma unroll
@@ -898,10 +938,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
             s[u][i] = ((key >= lo) & (key < hi)) ? s[u][i] : kNone;
           }
       }
-      uint64_t have = ~0ull;
-#pragma unroll
-      for (int i = 0; i < 2 * SUB; ++i) have &= exists[buf][i];
-      if (have != ~0ull) {  // pages that are not there
+      if (holes) {  // pages that are not there
         const int h = opaque(half);
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
@@ -911,16 +948,17 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
             if (!(exists[buf][2 * u + (i >> 3)] >> (4 * (key & 15)) & 1)) s[u][i] = kNone;
           }
       }
-      float top = s[0][0], low = s[0][0];
+      if (SUB == 1 || edge || holes) {
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+        for (int k = 0; k < 4; ++k) extremes(0, k, true);
+      }
+      if constexpr (SUB == 2) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          top = max3(top, s[u][i], s[u][i + 1]);
-          low = min3(low, s[u][i], s[u][i + 1]);
-        }
-      top *= factor;  // the factor is positive
-      low *= factor;
+        for (int k = 0; k < 4; ++k) extremes(SUB - 1, k, false);
+      }
+      // (the factor is positive)
+      float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]) * factor;
+      const float low = min3(fminf(low4[0], low4[1]), low4[2], low4[3]) * factor;
       if (__any(top > m_run + kLag)) {
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float next = fmaxf(m_run, top);
