@@ -1269,11 +1269,12 @@ static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, 
                 (long long)query_heads, c.heads);
   if (window < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] window must be >= 0.", op);
   if (query_heads > 65535 || seqs > 65535 || max_queries > INT32_MAX / query_heads || max_context > INT32_MAX ||
-      tokens > INT32_MAX / query_heads)
+      tokens > INT32_MAX / query_heads || seqs * c.heads > (((int64_t)1 << 30) / (max_context / 128 + 1)))
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large.", op);
   a->seqs = (int)seqs;
   a->query_heads = (int)query_heads;
   a->groups = (int)(query_heads / c.heads);
+  a->group_div = nvfp4::kv_make_div((uint32_t)a->groups);
   a->max_queries = (int)(max_queries < tokens ? max_queries : tokens);
   a->max_keys = (int)max_context;
   a->window = (int)(window > INT32_MAX ? 0 : window);

@@ -68,7 +68,7 @@ __device__ __forceinline__ KvRange kv_range(const KvAttention& a, int b, int row
   r.lo = 0;
   r.hi = min(r.context, a.max_keys);
   if (a.causal) {
-    const int q0 = row0 / a.groups, q1 = min((row0 + rows - 1) / a.groups, r.n - 1);
+    const int q0 = kv_div(row0, a.group_div), q1 = min((int)kv_div(row0 + rows - 1, a.group_div), r.n - 1);
     r.hi = min(r.hi, r.context - r.n + q1 + 1);
     if (a.window > 0) r.lo = max(0, r.context - r.n + q0 - a.window + 1);
   }
@@ -317,23 +317,18 @@ constexpr int kFewStep = kFewWaves * kFewTile;
 struct KvShare {
   int groups;    // workgroups of the launch
   int rows;      // rows of a part
-  float* sums;   // [parts][rows][dim], times 2^kBias
+  float* sums;   // [parts][rows][dim], times 2^kBias; null: workgroup g takes pair g whole
   float* stats;  // [parts][rows][2]: maximum (log2), sum
 };
 
-// Lane `lane`'s (wave-uniform) values, in scalar registers.
-__device__ __forceinline__ int64_t kv_readlane(int64_t v, int lane) {
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
-}
 // Sequences 64 at a time, one per lane: their ranges and the units before them.
 struct KvScan {
-  KvRange range;   // of sequence base + lane
-  int units;       // of one pair of this sequence; 0 past the last one and without queries
-  int64_t first;   // units before this sequence
-  int64_t after;   // units up to the end of the block
+  KvRange range;  // of sequence base + lane
+  int units;      // of one pair of this sequence; 0 past the last one and without queries
+  int first;      // units before this sequence
+  int after;      // units up to the end of the block
 };
-__device__ __forceinline__ void kv_scan(const KvCache& c, const KvAttention& a, int rows, int base, int64_t before,
+__device__ __forceinline__ void kv_scan(const KvCache& c, const KvAttention& a, int rows, int base, int before,
                                         KvScan& s) {
   const int lane = threadIdx.x & 63, b = base + lane;
   s.units = 0;
@@ -343,26 +338,27 @@ __device__ __forceinline__ void kv_scan(const KvCache& c, const KvAttention& a, 
     // a sequence that sees nothing still has a unit: its rows are written as zeros
     if (s.range.n > 0) s.units = max(1, (s.range.hi - s.range.lo + kFewStep - 1) / kFewStep);
   }
-  int64_t sum = (int64_t)s.units * c.heads;
-  const int64_t own = sum;
+  int sum = s.units * c.heads;  // all units together stay below 2^30
+  const int own = sum;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int64_t up = __shfl_up(sum, off, 64);
+    const int up = __shfl_up(sum, off, 64);
     if (lane >= off) sum += up;
   }
   s.first = before + sum - own;
-  s.after = before + kv_readlane(sum, 63);
+  s.after = before + __builtin_amdgcn_readlane(sum, 63);
 }
+// Lane `lane`'s (wave-uniform) range, in scalar registers.
 __device__ __forceinline__ KvRange kv_range_of(const KvScan& s, int lane) {
   return KvRange{__builtin_amdgcn_readlane(s.range.first, lane), __builtin_amdgcn_readlane(s.range.n, lane),
                  __builtin_amdgcn_readlane(s.range.context, lane), __builtin_amdgcn_readlane(s.range.lo, lane),
                  __builtin_amdgcn_readlane(s.range.hi, lane)};
 }
-// Units of one workgroup.
-__device__ __forceinline__ int64_t kv_units_each(const KvCache& c, const KvAttention& a, const KvShare& sh) {
-  int64_t total = 0;
+// Units of one workgroup.  Leaves the scan at the last 64 sequences (with up
+// to 64 of them: at all).
+__device__ __forceinline__ int kv_units_each(const KvCache& c, const KvAttention& a, const KvShare& sh, KvScan& s) {
+  int total = 0;
   for (int base = 0; base < a.seqs; base += 64) {
-    KvScan s;
     kv_scan(c, a, sh.rows, base, total, s);
     total = s.after;
   }
@@ -408,100 +404,72 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   const float value_factor = global_decode(c.global_v);
   const float key_factor = a.scale * kLog2e * global_decode(c.global_k);
 
-  const int64_t each = kv_units_each(c, a, sh);
-  int64_t unit = blockIdx.x * each;
-  const int64_t last_unit = unit + each;
-  int base = 0;
-  int64_t before = 0;
-  bool first_run = true;
-  while (unit < last_unit) {
-  // the sequence that holds this unit (scanned anew for each run: kept, the
-  // scan would cost the loop a dozen registers)
+  const bool alone = sh.sums == nullptr;  // one workgroup a pair
   KvScan scan;
-  for (kv_scan(c, a, sh.rows, base, before, scan); unit >= scan.after; kv_scan(c, a, sh.rows, base, before, scan)) {
-    base += 64;
-    before = scan.after;
-    if (base >= a.seqs) return;  // past the last unit
+  const int each = alone ? 1 : kv_units_each(c, a, sh, scan);
+  int unit = (int)blockIdx.x * each;
+  const int last_unit = unit + each;
+  int base = 0, before = 0;
+  bool scanned = a.seqs <= 64, first_run = true;
+  while (unit < last_unit) {
+  int b, head, begin, end;
+  bool whole = true;
+  KvRange rg;
+  if (alone) {
+    b = blockIdx.x / c.heads;
+    head = blockIdx.x - b * c.heads;
+    rg = kv_range(a, b, 0, sh.rows);
+    if (rg.n == 0) return;
+    begin = rg.lo;
+    end = rg.hi;
+    ++unit;
+  } else {
+    // the sequence that holds this unit (scanned anew for each run: kept, the
+    // scan would cost the loop a dozen registers)
+    if (!scanned) kv_scan(c, a, sh.rows, base, before, scan);
+    scanned = false;
+    while (unit >= scan.after) {
+      base += 64;
+      before = scan.after;
+      if (base >= a.seqs) return;  // past the last unit
+      kv_scan(c, a, sh.rows, base, before, scan);
+    }
+    const int at_lane = 63 - __builtin_clzll(__ballot(scan.units > 0 && scan.first <= unit));
+    b = base + at_lane;
+    rg = kv_range_of(scan, at_lane);
+    const int pair_units = __builtin_amdgcn_readlane(scan.units, at_lane);
+    const int inside = unit - __builtin_amdgcn_readlane(scan.first, at_lane);
+    head = inside / pair_units;
+    const int off = inside - head * pair_units;
+    const int take = min(pair_units - off, last_unit - unit);
+    unit += take;
+    whole = take == pair_units;
+    begin = rg.lo + off * kFewStep;
+    end = min(rg.hi, begin + take * kFewStep);
   }
-  const int at_lane = 63 - __builtin_clzll(__ballot(scan.units > 0 && scan.first <= unit));
-  const int b = base + at_lane;
-  const KvRange rg = kv_range_of(scan, at_lane);
-  const int pair_units = __builtin_amdgcn_readlane(scan.units, at_lane);
-  const int64_t inside = unit - kv_readlane(scan.first, at_lane);
-  const int head = (int)(inside / pair_units);
-  const int off = (int)(inside - (int64_t)head * pair_units);
-  const int take = (int)min((int64_t)(pair_units - off), last_unit - unit);
-  unit += take;
-  const bool whole = take == pair_units;
-  const int begin = rg.lo + off * kFewStep, end = min(rg.hi, begin + take * kFewStep);
   const int rows = rg.n * a.groups;
   const KvPlace place = kv_place(c, head);
-  constexpr int row0 = 0;
-  if (!first_run) __syncthreads();  // the last run's sums and page numbers have been read
+  if (!first_run) lds_barrier();  // the last run's sums and page numbers have been read
   first_run = false;
 
-  // queries: row `col` of each row tile, values 16 NG quarter ..
-  f16x8 q[MT][SPLIT][STEPS];
-  float factor[MT];
-  int see_lo[MT], see_hi[MT];  // keys that row `col` sees
+  // Loads first, in the order of their use: queries, page numbers, the first
+  // tile; the queries are converted while it is on its way.
+  KvRaw<SPLIT> raw[MT][STEPS];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int r = row0 + 16 * m + col;
-    const bool live = r < rows;
-    const int qi = r / a.groups;
+    const int r = 16 * m + col;  // this lane's row
+    const int qi = kv_div(r, a.group_div);
     const int64_t at = (int64_t)(rg.first + qi) * a.q_token + (head * a.groups + (r - qi * a.groups)) * a.q_head;
-    KvRaw<SPLIT> raw[STEPS];
-    float top = 0.0f;
 #pragma unroll
     for (int t = 0; t < STEPS; ++t) {
       const int d = 16 * NG * quarter + 8 * t;
-      raw[t] = kv_load_query<SPLIT>(a, q_vec, at + d, live && d < c.dim);
-      top = fmaxf(top, kv_query_top<SPLIT>(raw[t], dt));
+      raw[m][t] = kv_load_query<SPLIT>(a, q_vec, at + d, r < rows && d < c.dim);
     }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    float back;
-    const float power = kv_row_power(top, back);
-    factor[m] = key_factor * back;
-#pragma unroll
-    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, power, q[m][0][t], q[m][SPLIT - 1][t]);
-    const int pos = rg.context - rg.n + qi;
-    see_hi[m] = !live ? 0 : a.causal ? min(rg.hi, pos + 1) : rg.hi;
-    see_lo[m] = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  }
-  // keys that every row sees: [all_lo, all_hi)
-  int all_hi = rg.hi, all_lo = 0;
-  if (a.causal) {
-    all_hi = min(rg.hi, rg.context - rg.n + row0 / a.groups + 1);
-    if (a.window > 0)
-      all_lo = max(0, rg.context - rg.n + min(rg.n - 1, (row0 + 16 * MT - 1) / a.groups) - a.window + 1);
   }
 
-  f32x4 acc[MT][DB];
-  float m_run[MT], sub[MT], l_run[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    m_run[m] = kNone;
-    sub[m] = -kBias;
-    l_run[m] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DB; ++d) acc[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  // runs whose page numbers do not fit are staged in several goes
+  // Runs whose page numbers do not fit are staged in several goes of `span` keys.
   const int span = (int)min((int64_t)(end - begin), (int64_t)(kFewPages - 2) * c.page_size / kFewStep * kFewStep);
-  for (int from = begin; from < end; from += span) {
-  const int to = min(end, from + span);
-  const int p0 = kv_div(from, c.page_div);
-  {
-    const int count = (int)kv_div(to - 1, c.page_div) - p0 + 1;
-    if (from > begin) __syncthreads();
-    for (int i = threadIdx.x; i < count; i += 256) {  // -1 where there is no such page
-      const int p = a.page_table[b * a.table_stride + p0 + i];
-      page_of[i] = p >= 0 && p < c.pages ? p : -1;
-    }
-    __syncthreads();
-  }
+  int to = begin, p0 = 0;
   // A tile's keys are loaded once the last tile's are used up, its values
   // likewise: two thirds of a tile's time ahead, in the same registers.
   KvGroups<NG> kt[2], vt[2];
@@ -524,13 +492,64 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) x[u] = kv_load<NG, EXACT, true>(codes, scales, row[u], c.dim, g0, there[u]);
   };
-  int tile = from + wave * kFewTile;
-  if (tile < to) {
-    locate(tile);
-    load(c.k_codes, c.k_scales, kt);
-    load(c.v_codes, c.v_scales, vt);
+  auto stage = [&](int from) {  // page numbers of the keys from `from` on, then this wave's first tile of them
+    to = min(end, from + span);
+    p0 = kv_div(from, c.page_div);
+    const int count = (int)kv_div(to - 1, c.page_div) - p0 + 1;
+    for (int i = threadIdx.x; i < count; i += 256) {  // -1 where there is no such page
+      const int p = a.page_table[b * a.table_stride + p0 + i];
+      page_of[i] = p >= 0 && p < c.pages ? p : -1;
+    }
+    lds_barrier();
+    if (from + wave * kFewTile < to) {
+      locate(from + wave * kFewTile);
+      load(c.k_codes, c.k_scales, kt);
+      load(c.v_codes, c.v_scales, vt);
+    }
+  };
+  if (begin < end) stage(begin);
+
+  // row `col` of each row tile, values 16 NG quarter ..
+  f16x8 q[MT][SPLIT][STEPS];
+  float factor[MT];
+  int see_lo[MT], see_hi[MT];  // keys that row `col` sees
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float top = 0.0f;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) top = fmaxf(top, kv_query_top<SPLIT>(raw[m][t], dt));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    float back;
+    const float power = kv_row_power(top, back);
+    factor[m] = key_factor * back;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[m][t], dt, power, q[m][0][t], q[m][SPLIT - 1][t]);
+    const int r = 16 * m + col;
+    const int pos = rg.context - rg.n + (int)kv_div(r, a.group_div);
+    see_hi[m] = r >= rows ? 0 : a.causal ? min(rg.hi, pos + 1) : rg.hi;
+    see_lo[m] = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
   }
-  for (; tile < to; tile += kFewStep) {
+  // keys that every row sees: [all_lo, all_hi)
+  int all_hi = rg.hi, all_lo = 0;
+  if (a.causal) {
+    all_hi = min(rg.hi, rg.context - rg.n + 1);
+    if (a.window > 0) all_lo = max(0, rg.context - a.window);
+  }
+
+  f32x4 acc[MT][DB];
+  float m_run[MT], sub[MT], l_run[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    m_run[m] = kNone;
+    sub[m] = -kBias;
+    l_run[m] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) acc[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  for (int from = begin; from < end;) {
+  for (int tile = from + wave * kFewTile; tile < to; tile += kFewStep) {
     const uint32_t live = exists;
     const bool more = tile + kFewStep < to;
     if (more) locate(tile + kFewStep);
@@ -672,6 +691,11 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       }
     multiply();
   }
+  from = to;
+  if (from < end) {
+    lds_barrier();
+    stage(from);
+  }
   }
 
   // the four waves meet
@@ -687,14 +711,14 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (m > 0) __syncthreads();
+    if (m > 0) lds_barrier();
     float* own = reinterpret_cast<float*>(mine) + col * (DP + 4);
 #pragma unroll
     for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4*>(own + 16 * d + 4 * quarter) = acc[m][d];
-    __syncthreads();
+    lds_barrier();
     for (int i = threadIdx.x; i < 16 * (DP / 4); i += 256) {
       const int rr = i / (DP / 4), d = 4 * (i - rr * (DP / 4));
-      const int r = row0 + 16 * m + rr;
+      const int r = 16 * m + rr;
       if (r >= rows || d >= c.dim) continue;
       float mt = stat_m[0][16 * m + rr];
 #pragma unroll
@@ -710,7 +734,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += by * o[j];
       }
-      const int qi = r / a.groups;
+      const int qi = kv_div(r, a.group_div);
       const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + head * a.groups + (r - qi * a.groups);
       if (whole) {
         const float by = l == 0.0f ? 0.0f : value_factor / l;  // a NaN stays one
@@ -719,7 +743,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
         kv_store4(dt, a.out, row * c.dim + d, v);
         if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? kNone : (mt - kBias + __builtin_log2f(l)) * kLn2;
       } else {
-        const int64_t at = ((int64_t)blockIdx.x + (int64_t)b * c.heads + head) * sh.rows + r;
+        const int64_t at = ((int64_t)blockIdx.x + b * c.heads + head) * sh.rows + r;
         kv_store4<kF32>(sh.sums, at * c.dim + d, v);
         if (d == 0) *reinterpret_cast<f32x2*>(sh.stats + 2 * at) = f32x2{mt, l};
       }
@@ -824,7 +848,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   // queries: row `col` of this wave's 32
   const int r = row0 + 32 * wave + col;
   const bool row_live = r < rows;
-  const int qi = r / a.groups, qh = head * a.groups + r - qi * a.groups;
+  const int qi = kv_div(r, a.group_div), qh = head * a.groups + r - qi * a.groups;
   f16x8 q[SPLIT][STEPS];
   float factor;
   {
@@ -851,8 +875,8 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   int all_lo = 0, all_hi = end;
   if (a.causal) {
     const int w0 = min(row0 + 32 * wave, rows - 1), base = rg.context - rg.n;
-    all_hi = min(end, base + w0 / a.groups + 1);
-    if (a.window > 0) all_lo = max(0, base + min(w0 + 31, rows - 1) / a.groups - a.window + 1);
+    all_hi = min(end, base + (int)kv_div(w0, a.group_div) + 1);
+    if (a.window > 0) all_lo = max(0, base + (int)kv_div(min(w0 + 31, rows - 1), a.group_div) - a.window + 1);
   }
 
   f32x16 acc[DB];
@@ -1157,21 +1181,24 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention
   const int b = blockIdx.y;
   const int qi = blockIdx.x / a.query_heads, qh = blockIdx.x - qi * a.query_heads;
   const int head = qh / a.groups, r = qi * a.groups + qh - head * a.groups;
-  const int64_t each = kv_units_each(c, a, sh);
   KvScan scan;
+  const int each = kv_units_each(c, a, sh, scan);
   int base = 0;
-  for (kv_scan(c, a, sh.rows, 0, 0, scan); b >= base + 64;) {
-    base += 64;
-    kv_scan(c, a, sh.rows, base, scan.after, scan);
+  if (a.seqs > 64) {
+    kv_scan(c, a, sh.rows, 0, 0, scan);
+    while (b >= base + 64) {
+      base += 64;
+      kv_scan(c, a, sh.rows, base, scan.after, scan);
+    }
   }
   const KvRange rg = kv_range_of(scan, b - base);
   if (qi >= rg.n) return;
   const int units = __builtin_amdgcn_readlane(scan.units, b - base);
-  const int64_t u0 = kv_readlane(scan.first, b - base) + (int64_t)head * units;
-  const int64_t g0 = u0 / each, g1 = (u0 + units - 1) / each;
+  const int u0 = __builtin_amdgcn_readlane(scan.first, b - base) + head * units;
+  const int g0 = u0 / each, g1 = (u0 + units - 1) / each;
   if (g0 == g1) return;  // one workgroup had it all
-  const int parts = (int)(g1 - g0) + 1;
-  const int64_t at = (g0 + (int64_t)b * c.heads + head) * sh.rows + r;
+  const int parts = g1 - g0 + 1;
+  const int64_t at = ((int64_t)g0 + b * c.heads + head) * sh.rows + r;
   kv_join(c, a, dt, sh.sums, sh.stats, at, sh.rows, parts, (int64_t)(rg.first + qi) * a.query_heads + qh);
 }
 
@@ -1186,6 +1213,10 @@ __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttentio
 }
 
 // ----------------------------------------------------------------- launches
+
+// Contexts of up to so many keys are left to one workgroup a pair: no parts, no
+// second launch.
+constexpr int kFewAlone = 1024;
 
 struct KvPlan {
   bool few;
@@ -1212,8 +1243,8 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
     // as many workgroups as run at once, but no more than there can be units
     const int64_t units = pairs * (keys > kFewStep ? (keys + kFewStep - 1) / kFewStep : 1);
     const int64_t most = (int64_t)device_cu_count() * few_occupancy(few_groups(c.dim), p.mt, split);
-    p.groups = (int)(units < most ? units : most);
-    parts = units > pairs ? (size_t)(p.groups + pairs) * 16 * p.mt : 0;  // one unit a pair: nothing to join
+    p.groups = (int)(keys <= kFewAlone ? pairs : units < most ? units : most);
+    parts = keys > kFewAlone ? (size_t)(p.groups + pairs) * 16 * p.mt : 0;
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
     int64_t splits = 2 * device_cu_count() / (pairs * p.row_tiles);
@@ -1281,7 +1312,7 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const KvPlan& p, int d
                   bool q_vec, hipStream_t s) {
   const dim3 rows((unsigned)(a.max_queries * a.query_heads), a.seqs);
   if (p.few) {
-    const KvShare sh{p.groups, 16 * p.mt, sums, stats};
+    const KvShare sh{p.groups, 16 * p.mt, p.bytes ? sums : nullptr, stats};
     const hipError_t e = launch_few<NG, EXACT>(c, a, sh, p, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
     kv_join_few_kernel<<<rows, 256, 0, s>>>(c, a, sh, dt);

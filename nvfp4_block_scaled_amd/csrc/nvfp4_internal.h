@@ -172,6 +172,7 @@ struct KvAttention {
   float* lse;                   // [tokens, query_heads] or null
   float scale;
   int seqs, query_heads, groups, max_queries, max_keys, causal, window;
+  KvDiv group_div;              // by groups
   int64_t table_stride, tokens;
 };
 size_t kv_attention_workspace(const KvCache& c, const KvAttention& a);
