@@ -32,6 +32,7 @@ elements, any shape such as [e, 1, 1]), as the pages' validate_global_scale
 requires ("mlx 0.30.7.2 -> 0.30.7.6" diff, page 8).
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -759,31 +760,28 @@ class KVCache:
     scales (None: factor 1).  Slot = page * page_size + offset in the page."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, global_scale_k=None, global_scale_v=None):
-        if k_codes.dim() != 4:
+        codes, scales, device = k_codes.shape, k_scales.shape, k_codes.device
+        if len(codes) != 4:
             raise ValueError("k_codes must be [pages, heads, page_size, dim/2]")
-        codes, scales = k_codes.shape, k_scales.shape
-        if v_codes.shape != codes or v_scales.shape != scales or scales[:-1] != codes[:-1] \
-                or scales[-1] * 8 != codes[-1]:
+        if v_codes.shape != codes or v_scales.shape != scales or scales[:3] != codes[:3] \
+                or scales[3] * 8 != codes[3]:
             raise ValueError("the codes and scales of keys and values describe different shapes")
-        device = k_codes.device
         for t in (k_codes, k_scales, v_codes, v_scales):
-            if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+            if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous():
                 raise ValueError("codes and scales must be contiguous uint8 tensors of one device")
+        pointers = []
         for g, name in ((global_scale_k, "global_scale_k"), (global_scale_v, "global_scale_v")):
-            _gscale(g, name)
+            if g is not None and (g.numel() != 1 or g.dtype is not torch.float32 or g.device != device):
+                raise ValueError(f"{name} must be a float32 scalar on the cache's device")
+            pointers.append(None if g is None else g.data_ptr())
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.global_scale_k, self.global_scale_v = global_scale_k, global_scale_v
         self.pages, self.heads, self.page_size, half = codes
         self.dim = 2 * half
-        self._struct = _KVCacheStruct(
-            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-            None if global_scale_k is None else global_scale_k.data_ptr(),
-            None if global_scale_v is None else global_scale_v.data_ptr(),
-            self.pages, self.page_size, self.heads, self.dim)
-
-    @property
-    def device(self):
-        return self.k_codes.device
+        self.device = device
+        self._struct = _KVCacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                      v_scales.data_ptr(), *pointers, self.pages, self.page_size, self.heads,
+                                      self.dim)
 
 
 def kv_cache(pages, page_size, heads, dim, global_scale_k=None, global_scale_v=None, device="cuda"):
@@ -797,12 +795,19 @@ def kv_cache(pages, page_size, heads, dim, global_scale_k=None, global_scale_v=N
     return KVCache(held(2), held(16), held(2), held(16), global_scale_k, global_scale_v)
 
 
-def _kv_rows(t, name, cache, heads):
+def _kv_stream(cache):
+    """The current stream of the cache's device, as an integer."""
+    if cache.device.type != "cuda":
+        raise ValueError("the cache must be on a GPU")
+    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+
+
+def _kv_rows(t, name, cache, shape):
     """(token stride, head stride) of t [tokens, heads, dim]: its last dimension must be
     contiguous, the others may have any stride."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {cache.dim}], not {tuple(t.shape)}")
-    if t.device != cache.k_codes.device or not t.is_cuda:
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != cache.device:
         raise ValueError(f"{name} must be on the cache's device")
     s = t.stride()
     if s[2] != 1:
@@ -811,9 +816,9 @@ def _kv_rows(t, name, cache, heads):
 
 
 def _kv_index(t, name, cache, dtype, shape):
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    if t.device != cache.k_codes.device or not t.is_contiguous():
+    if t.device != cache.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on the cache's device")
 
 
@@ -822,14 +827,17 @@ def nvfp4_kv_write(cache, k, v, slots):
     slots (int64 [tokens]; a slot outside the cache skips its token).  k and v
     may be strided views with a contiguous last dimension."""
     L = load_library()
-    kt, kh = _kv_rows(k, "k", cache, cache.heads)
-    vt, vh = _kv_rows(v, "v", cache, cache.heads)
-    tokens = k.shape[0]
-    if v.shape[0] != tokens or v.dtype != k.dtype:
-        raise ValueError("k and v must have one length and one dtype")
-    _kv_index(slots, "slots", cache, torch.int64, (tokens,))
-    _check(L.nvfp4_kv_write(cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"), tokens, kt, kh,
-                            vt, vh, slots.data_ptr(), _stream()))
+    stream = _kv_stream(cache)
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != cache.heads or shape[2] != cache.dim:
+        raise ValueError(f"k must be [tokens, {cache.heads}, {cache.dim}], not {tuple(shape)}")
+    kt, kh = _kv_rows(k, "k", cache, shape)
+    vt, vh = _kv_rows(v, "v", cache, shape)
+    if v.dtype is not k.dtype:
+        raise ValueError("k and v must have one dtype")
+    _kv_index(slots, "slots", cache, torch.int64, shape[:1])
+    _check(L.nvfp4_kv_write(cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"), shape[0], kt, kh,
+                            vt, vh, slots.data_ptr(), stream))
 
 
 def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, out=None):
@@ -837,29 +845,36 @@ def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, out=None):
     slots (int64 [tokens]; zeros for a slot outside the cache).  out: the pair
     of tensors to write."""
     L = load_library()
+    stream = _kv_stream(cache)
     if slots.dim() != 1:
         raise ValueError("slots must be int64 [tokens]")
     tokens = slots.shape[0]
     _kv_index(slots, "slots", cache, torch.int64, (tokens,))
     shape = (tokens, cache.heads, cache.dim)
     if out is None:
-        k = torch.empty(shape, dtype=dtype, device=slots.device)
-        v = torch.empty(shape, dtype=dtype, device=slots.device)
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
     else:
         k, v = out
-        if k.shape != shape or v.shape != shape or k.dtype != v.dtype:
-            raise ValueError(f"out must be two tensors {shape} of one dtype")
-        _dev(k, "out")
-        _dev(v, "out")
+        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.device != cache.device \
+                or v.device != cache.device or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError(f"out must be two contiguous tensors {shape} of one dtype on the cache's device")
     _check(L.nvfp4_kv_read(cache._struct, slots.data_ptr(), tokens, k.data_ptr(), v.data_ptr(),
-                           _dtype_code(k, "out"), _stream()))
+                           _dtype_code(k, "out"), stream))
     return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv_attention_bytes(pages, page_size, heads, dim, *sizes):
+    """Bytes of workspace: a function of the sizes alone."""
+    s = _KVCacheStruct(256, 256, 256, 256, None, None, pages, page_size, heads, dim)
+    return load_library().nvfp4_kv_attention_workspace_size(s, *sizes)
 
 
 def kv_attention_workspace(cache, tokens, query_heads, seqs, max_queries, max_context, window=0):
     """(workspace, bytes) for nvfp4_kv_attention calls of these sizes."""
-    nbytes = load_library().nvfp4_kv_attention_workspace_size(cache._struct, tokens, query_heads, seqs,
-                                                              max_queries, max_context, window)
+    nbytes = _kv_attention_bytes(cache.pages, cache.page_size, cache.heads, cache.dim, tokens, query_heads, seqs,
+                                 max_queries, max_context, window)
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device), nbytes
 
 
@@ -875,35 +890,45 @@ def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, ma
     Returns out [tokens, query_heads, dim], with return_lse also the float32
     log-sum-exp [tokens, query_heads] of the scores."""
     L = load_library()
-    tokens, query_heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    qt, qh = _kv_rows(q, "q", cache, query_heads)
-    seqs, table_pages = page_table.shape
-    _kv_index(page_table, "page_table", cache, torch.int32, (seqs, table_pages))
-    _kv_index(context_lens, "context_lens", cache, torch.int32, (seqs,))
+    stream = _kv_stream(cache)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"q must be [tokens, query_heads, {cache.dim}], not {tuple(shape)}")
+    tokens, query_heads, _ = shape
+    qt, qh = _kv_rows(q, "q", cache, shape)
+    table_shape = page_table.shape
+    if len(table_shape) != 2:
+        raise ValueError("page_table must be int32 [seqs, table_pages]")
+    seqs, table_pages = table_shape
+    _kv_index(page_table, "page_table", cache, torch.int32, table_shape)
+    _kv_index(context_lens, "context_lens", cache, torch.int32, table_shape[:1])
+    starts = None
     if query_starts is not None:
         _kv_index(query_starts, "query_starts", cache, torch.int32, (seqs + 1,))
+        starts = query_starts.data_ptr()
     if max_context is None:
         max_context = table_pages * cache.page_size
     if scale is None:
         scale = cache.dim ** -0.5
     if out is None:
-        out = torch.empty((tokens, query_heads, cache.dim), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and dtype")
-    else:
-        _dev(out, "out")
-    lse = torch.empty((tokens, query_heads), dtype=torch.float32, device=q.device) if return_lse else None
+        out = torch.empty(shape, dtype=q.dtype, device=cache.device)
+    elif out.shape != shape or out.dtype is not q.dtype or out.device != cache.device or not out.is_contiguous():
+        raise ValueError("out must be contiguous and have q's shape, dtype and device")
+    lse = torch.empty((tokens, query_heads), dtype=torch.float32, device=cache.device) if return_lse else None
     if workspace is None:
-        nbytes = L.nvfp4_kv_attention_workspace_size(cache._struct, tokens, query_heads, seqs, max_queries,
-                                                     max_context, window)
+        nbytes = _kv_attention_bytes(cache.pages, cache.page_size, cache.heads, cache.dim, tokens, query_heads,
+                                     seqs, max_queries, max_context, window)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     else:
         nbytes = workspace.numel() * workspace.element_size()
+        if workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
     _check(L.nvfp4_kv_attention(cache._struct, q.data_ptr(), _dtype_code(q, "q"), tokens, query_heads, qt, qh,
-                                page_table.data_ptr(), seqs, table_pages, context_lens.data_ptr(),
-                                _ptr(query_starts), max_queries, max_context, scale, int(bool(causal)), window,
-                                out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes, _stream()))
+                                page_table.data_ptr(), seqs, table_pages, context_lens.data_ptr(), starts,
+                                max_queries, max_context, scale, 1 if causal else 0, window, out.data_ptr(),
+                                lse.data_ptr() if return_lse else None,
+                                workspace.data_ptr() if nbytes else None, nbytes, stream))
     return (out, lse) if return_lse else out
 
 

@@ -90,10 +90,10 @@ __device__ __forceinline__ f16x2 kv_scale2(uint32_t w) {
 }
 
 // The codes and scales of NG groups of 16 of one cached row, from group `g0`.
-template <int NG>
+template <int NG, bool EXACT>
 struct KvGroups {
   uint32_t w[2 * NG];
-  uint32_t s;  // scale bytes
+  uint32_t s[EXACT ? 1 : NG];  // scale bytes: of all groups in one, or one each (joining them would wait for the loads)
 };
 // Where a head's codes start, counted from the start of the codes, by page:
 // byte page * page_bytes + head_bytes + offset * dim/2; its scales at an
@@ -120,12 +120,13 @@ __device__ __forceinline__ T kv_fetch(const T* p) {
 // dim / 16 on are zeros, as is a row that is not `live`.  ONCE: the row is
 // read by this workgroup only.
 template <int NG, bool EXACT, bool ONCE>
-__device__ __forceinline__ KvGroups<NG> kv_load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+__device__ __forceinline__ KvGroups<NG, EXACT> kv_load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                 uint64_t at, int dim, int g0, bool live) {
-  KvGroups<NG> r;
+  KvGroups<NG, EXACT> r;
 #pragma unroll
   for (int i = 0; i < 2 * NG; ++i) r.w[i] = 0u;
-  r.s = 0u;
+#pragma unroll
+  for (int i = 0; i < (EXACT ? 1 : NG); ++i) r.s[i] = 0u;
   const uint8_t* c = codes + at + 8 * g0;
   const uint8_t* s = scales + (at >> 3) + g0;
   if constexpr (EXACT) {
@@ -133,15 +134,15 @@ __device__ __forceinline__ KvGroups<NG> kv_load(const uint8_t* __restrict__ code
       if constexpr (NG == 1) {
         const u32x2 x = kv_fetch<ONCE>(reinterpret_cast<const u32x2*>(c));
         r.w[0] = x.x; r.w[1] = x.y;
-        r.s = *s;
+        r.s[0] = *s;
       } else {
 #pragma unroll
         for (int i = 0; i < NG / 2; ++i) {
           const u32x4 x = kv_fetch<ONCE>(reinterpret_cast<const u32x4*>(c) + i);
           r.w[4 * i] = x.x; r.w[4 * i + 1] = x.y; r.w[4 * i + 2] = x.z; r.w[4 * i + 3] = x.w;
         }
-        if constexpr (NG == 2) r.s = *reinterpret_cast<const uint16_t*>(s);
-        else r.s = *reinterpret_cast<const uint32_t*>(s);
+        if constexpr (NG == 2) r.s[0] = *reinterpret_cast<const uint16_t*>(s);
+        else r.s[0] = *reinterpret_cast<const uint32_t*>(s);
       }
     }
   } else {
@@ -151,20 +152,24 @@ __device__ __forceinline__ KvGroups<NG> kv_load(const uint8_t* __restrict__ code
       if (live && i < have) {
         const u32x2 x = kv_fetch<ONCE>(reinterpret_cast<const u32x2*>(c) + i);
         r.w[2 * i] = x.x; r.w[2 * i + 1] = x.y;
-        r.s |= (uint32_t)s[i] << (8 * i);
+        r.s[i] = s[i];
       }
   }
   return r;
 }
+// The block scale of group g.
+template <int NG, bool EXACT>
+__device__ __forceinline__ _Float16 kv_scale_of(const KvGroups<NG, EXACT>& r, int g) {
+  if constexpr (!EXACT) return kv_scale2(r.s[g]).x;
+  const f16x2 two = kv_scale2(g < 2 ? r.s[0] : r.s[0] >> 16);
+  return g & 1 ? two.y : two.x;
+}
 // Dwords 2g, 2g + 1 (group g) as 16 float16.
-template <int NG>
-__device__ __forceinline__ void kv_values(const KvGroups<NG>& r, f16x8 (&v)[2 * NG]) {
-  const f16x2 s01 = kv_scale2(r.s);
-  f16x2 s23 = s01;
-  if constexpr (NG > 2) s23 = kv_scale2(r.s >> 16);
+template <int NG, bool EXACT>
+__device__ __forceinline__ void kv_values(const KvGroups<NG, EXACT>& r, f16x8 (&v)[2 * NG]) {
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const _Float16 s = g == 0 ? s01.x : g == 1 ? s01.y : g == 2 ? s23.x : s23.y;
+    const _Float16 s = kv_scale_of(r, g);
     v[2 * g] = kv_decode8(r.w[2 * g], s);
     v[2 * g + 1] = kv_decode8(r.w[2 * g + 1], s);
   }
@@ -472,7 +477,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   int to = begin, p0 = 0;
   // A tile's keys are loaded once the last tile's are used up, its values
   // likewise: two thirds of a tile's time ahead, in the same registers.
-  KvGroups<NG> kt[2], vt[2];
+  KvGroups<NG, EXACT> kt[2], vt[2];
   uint64_t row[2];       // this lane's rows of the tile that is being loaded
   bool there[2];
   uint32_t exists = 0u;  // which of its 32 keys do
@@ -488,7 +493,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       exists |= (uint32_t)(__ballot(there[u]) & 0xFFFFu) << (16 * u);
     }
   };
-  auto load = [&](const uint8_t* codes, const uint8_t* scales, KvGroups<NG>(&x)[2]) {
+  auto load = [&](const uint8_t* codes, const uint8_t* scales, KvGroups<NG, EXACT>(&x)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) x[u] = kv_load<NG, EXACT, true>(codes, scales, row[u], c.dim, g0, there[u]);
   };
@@ -559,7 +564,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f16x8 kf[STEPS];
-      kv_values<NG>(kt[u], kf);
+      kv_values<NG, EXACT>(kt[u], kf);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -576,7 +581,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f16x8 vf[STEPS];
-      kv_values<NG>(vt[u], vf);
+      kv_values<NG, EXACT>(vt[u], vf);
 #pragma unroll
       for (int t = 0; t < STEPS; ++t)
         *reinterpret_cast<f16x8*>(mine + (16 * u + col) * RB + 32 * NG * quarter + 16 * t) = vf[t];
@@ -809,7 +814,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   auto lookup = [&](int tile) {
     return a.page_table[b * a.table_stride + kv_div(min(tile + key_of, end - 1), c.page_div)];
   };
-  KvGroups<NG> kt, vt;
+  KvGroups<NG, EXACT> kt, vt;
   int live = 0;
   const KvPlace place = kv_place(c, head);
   auto load = [&](int tile, int page) {
@@ -829,11 +834,10 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   constexpr int PIECES = (BOTH ? 4 : 2) * NG;
   auto store_piece = [&](int buf, int i) {
     const bool of_v = BOTH ? i >= 2 * NG : second;
-    const KvGroups<NG>& x = BOTH && i >= 2 * NG ? vt : kt;
+    const KvGroups<NG, EXACT>& x = BOTH && i >= 2 * NG ? vt : kt;
     const int w = BOTH && i >= 2 * NG ? i - 2 * NG : i;
-    const f16x2 sc = kv_scale2(w < 4 ? x.s : x.s >> 16);
     uint8_t* at = lds + buf * BUF + (of_v ? TILE * KROW + key_of * VROW : key_of * KROW) + 32 * g0 + 16 * w;
-    *reinterpret_cast<f16x8*>(at) = kv_decode8(x.w[w], w & 2 ? sc.y : sc.x);
+    *reinterpret_cast<f16x8*>(at) = kv_decode8(x.w[w], kv_scale_of(x, w >> 1));
   };
   auto store_flags = [&](int buf) {
     const uint64_t bits = __ballot(live != 0);
@@ -1122,14 +1126,14 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 
 // ----------------------------------------------------------------- joining the parts
 
-// Row `row` of the output from its parts at, at + stride, ..: one workgroup.  Each wave sums some of the parts,
-// several at a time (dim / 4 lanes a part), and the four add theirs in a fixed
-// order, so every run gives the same bits.
+// Row `row` of the output from its parts at, at + stride, ..: by one workgroup
+// (WAVES 4: many parts) or one wave (WAVES 1: many rows of a few parts).  Each
+// wave sums some of the parts, several side by side (dim / 4 lanes a part),
+// and everything is added in a fixed order, so every run gives the same bits.
+template <int WAVES>
 __device__ __forceinline__ void kv_join(const KvCache& c, const KvAttention& a, int dt, const float* sums,
                                         const float* stats, int64_t at, int64_t stride, int parts, int64_t row) {
-  __shared__ __attribute__((aligned(16))) float part[kFewWaves][kKvMaxDim];
-  __shared__ float part_l[kFewWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
   float top = kNone;
   for (int i = lane; i < parts; i += 64) top = fmaxf(top, stats[2 * (at + i * stride)]);
   top = wave_max(top);
@@ -1138,7 +1142,7 @@ __device__ __forceinline__ void kv_join(const KvCache& c, const KvAttention& a, 
   float l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (side < each_wave) {
 #pragma unroll 4
-    for (int i = wave * each_wave + side; i < parts; i += kFewWaves * each_wave) {
+    for (int i = wave * each_wave + side; i < parts; i += WAVES * each_wave) {
       const int64_t e = at + i * stride;
       const f32x2 st = *reinterpret_cast<const f32x2*>(stats + 2 * e);
       const f32x4 o = *reinterpret_cast<const f32x4*>(sums + e * c.dim + d);
@@ -1159,17 +1163,22 @@ __device__ __forceinline__ void kv_join(const KvCache& c, const KvAttention& a, 
       for (int j = 0; j < 4; ++j) v[j] += v2[j];
     }
   }
-  if (side == 0) *reinterpret_cast<f32x4*>(&part[wave][d]) = f32x4{v[0], v[1], v[2], v[3]};
-  if (lane == 0) part_l[wave] = l;
-  __syncthreads();
-  if (wave > 0 || side > 0) return;
+  if constexpr (WAVES > 1) {
+    __shared__ __attribute__((aligned(16))) float part[WAVES][kKvMaxDim];
+    __shared__ float part_l[WAVES];
+    if (side == 0) *reinterpret_cast<f32x4*>(&part[wave][d]) = f32x4{v[0], v[1], v[2], v[3]};
+    if (lane == 0) part_l[wave] = l;
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
-  for (int w = 1; w < kFewWaves; ++w) {
-    l += part_l[w];
+    for (int w = 1; w < WAVES; ++w) {
+      l += part_l[w];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += part[w][d + j];
+      for (int j = 0; j < 4; ++j) v[j] += side == 0 ? part[w][d + j] : 0.0f;
+    }
   }
   l = __shfl(l, 0, 64);
+  if (side > 0) return;
   const float by = l == 0.0f ? 0.0f : global_decode(c.global_v) / l;
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] *= by;
@@ -1199,17 +1208,18 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention
   if (g0 == g1) return;  // one workgroup had it all
   const int parts = g1 - g0 + 1;
   const int64_t at = ((int64_t)g0 + b * c.heads + head) * sh.rows + r;
-  kv_join(c, a, dt, sh.sums, sh.stats, at, sh.rows, parts, (int64_t)(rg.first + qi) * a.query_heads + qh);
+  kv_join<kFewWaves>(c, a, dt, sh.sums, sh.stats, at, sh.rows, parts, (int64_t)(rg.first + qi) * a.query_heads + qh);
 }
 
 __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt) {
-  const int qi = blockIdx.x / a.query_heads, qh = blockIdx.x - qi * a.query_heads;
+  const int row_of = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int qi = row_of / a.query_heads, qh = row_of - qi * a.query_heads;
   const int r = qi * a.groups + qh % a.groups;  // its row among those of its kv head
   const KvRange rg = kv_range(a, blockIdx.y, r / kManyRows * kManyRows, kManyRows);
   if (qi >= rg.n) return;
   const int parts = rg.hi > rg.lo ? (rg.hi - rg.lo + sp.chunk - 1) / sp.chunk : 1;
   const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + qh;
-  kv_join(c, a, dt, sp.sums, sp.stats, row * sp.splits, 1, parts, row);
+  kv_join<1>(c, a, dt, sp.sums, sp.stats, row * sp.splits, 1, parts, row);
 }
 
 // ----------------------------------------------------------------- launches
@@ -1247,7 +1257,9 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
     parts = keys > kFewAlone ? (size_t)(p.groups + pairs) * 16 * p.mt : 0;
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
-    int64_t splits = 2 * device_cu_count() / (pairs * p.row_tiles);
+    const int64_t tiles = pairs * p.row_tiles;
+    // short contexts are not worth a second launch for less than a whole factor of two
+    int64_t splits = (2 * device_cu_count() + (keys >= 4096 ? tiles / 2 : 0)) / tiles;
     const int64_t most = keys / 256;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
@@ -1320,7 +1332,7 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const KvPlan& p, int d
     const KvChunks sp{p.chunk, p.splits, p.row_tiles, sums, stats};
     const hipError_t e = launch_many<NG, EXACT>(c, a, sp, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
-    kv_join_many_kernel<<<rows, 256, 0, s>>>(c, a, sp, dt);
+    kv_join_many_kernel<<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sp, dt);
   }
   return hipGetLastError();
 }
