@@ -401,7 +401,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   constexpr int DP = 64 * NG, STEPS = 2 * NG, DB = DP / 16, RB = few_row_bytes(NG);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ float stat_m[kFewWaves][16 * MT], stat_l[kFewWaves][16 * MT];
-  int* page_of = reinterpret_cast<int*>(lds + kFewWaves * kFewTile * RB);
+  int* page_of = reinterpret_cast<int*>(lds + kFewWaves * kFewTile * RB);  // of this run and of the next one
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, quarter = lane >> 4;
   uint8_t* mine = lds + wave * kFewTile * RB;
@@ -409,85 +409,103 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   const float value_factor = global_decode(c.global_v);
   const float key_factor = a.scale * kLog2e * global_decode(c.global_k);
 
-  const bool alone = sh.sums == nullptr;  // one workgroup a pair
+  // A run: some of the keys of one pair.
+  struct Run {
+    KvRange rg;
+    int b, head, begin, end, pages;  // pages: staged page numbers
+    bool whole;
+  };
+  // Keys whose page numbers are staged at a time.
+  const int span = (int)min((int64_t)1 << 30, (int64_t)(kFewPages - 2) * c.page_size / kFewStep * kFewStep);
+  auto pages_of = [&](int from, int end) {
+    return from < end ? (int)kv_div(min(end, from + span) - 1, c.page_div) - (int)kv_div(from, c.page_div) + 1 : 0;
+  };
   KvScan scan;
-  const int each = alone ? 1 : kv_units_each(c, a, sh, scan);
-  int unit = (int)blockIdx.x * each;
-  const int last_unit = unit + each;
-  int base = 0, before = 0;
-  bool scanned = a.seqs <= 64, first_run = true;
-  while (unit < last_unit) {
-  int b, head, begin, end;
-  bool whole = true;
-  KvRange rg;
-  if (alone) {
-    b = blockIdx.x / c.heads;
-    head = blockIdx.x - b * c.heads;
-    rg = kv_range(a, b, 0, sh.rows);
-    if (rg.n == 0) return;
-    begin = rg.lo;
-    end = rg.hi;
-    ++unit;
-  } else {
-    // the sequence that holds this unit (scanned anew for each run: kept, the
-    // scan would cost the loop a dozen registers)
-    if (!scanned) kv_scan(c, a, sh.rows, base, before, scan);
-    scanned = false;
+  int unit = 0, last_unit = 0, base = 0, before = 0;
+  // The run that begins with `unit`; `scan` holds the 64 sequences from `base`.
+  auto next_run = [&](KvScan& scan, Run& r) {
+    if (unit >= last_unit) return false;
     while (unit >= scan.after) {
       base += 64;
       before = scan.after;
-      if (base >= a.seqs) return;  // past the last unit
+      if (base >= a.seqs) {  // past the last unit
+        last_unit = unit;
+        return false;
+      }
       kv_scan(c, a, sh.rows, base, before, scan);
     }
-    const int at_lane = 63 - __builtin_clzll(__ballot(scan.units > 0 && scan.first <= unit));
-    b = base + at_lane;
-    rg = kv_range_of(scan, at_lane);
+    const int at_lane = __builtin_amdgcn_readfirstlane(63 - __builtin_clzll(__ballot(scan.units > 0 && scan.first <= unit)));
+    r.b = base + at_lane;
+    r.rg = kv_range_of(scan, at_lane);
     const int pair_units = __builtin_amdgcn_readlane(scan.units, at_lane);
     const int inside = unit - __builtin_amdgcn_readlane(scan.first, at_lane);
-    head = inside / pair_units;
-    const int off = inside - head * pair_units;
+    r.head = __builtin_amdgcn_readfirstlane(inside / pair_units);
+    const int off = inside - r.head * pair_units;
     const int take = min(pair_units - off, last_unit - unit);
     unit += take;
-    whole = take == pair_units;
-    begin = rg.lo + off * kFewStep;
-    end = min(rg.hi, begin + take * kFewStep);
+    r.whole = take == pair_units;
+    r.begin = r.rg.lo + off * kFewStep;
+    r.end = min(r.rg.hi, r.begin + take * kFewStep);
+    r.pages = __builtin_amdgcn_readfirstlane(pages_of(r.begin, r.end));
+    return true;
+  };
+  Run now, next;
+  next.pages = next.begin = 0;
+  bool more_runs = false;
+  if (sh.sums == nullptr) {  // one workgroup a pair
+    now.b = __builtin_amdgcn_readfirstlane(blockIdx.x / c.heads);
+    now.head = blockIdx.x - now.b * c.heads;
+    now.rg = kv_range(a, now.b, 0, sh.rows);
+    now.whole = true;
+    now.begin = now.rg.lo;
+    now.end = now.rg.hi;
+    now.pages = pages_of(now.begin, now.end);
+    if (now.rg.n == 0) return;
+  } else {
+    const int each = kv_units_each(c, a, sh, scan);
+    if (a.seqs > 64) kv_scan(c, a, sh.rows, 0, 0, scan);
+    unit = __builtin_amdgcn_readfirstlane((int)blockIdx.x * each);
+    last_unit = unit + __builtin_amdgcn_readfirstlane(each);
+    if (!next_run(scan, now)) return;
+    more_runs = next_run(scan, next);
   }
-  const int rows = rg.n * a.groups;
-  const KvPlace place = kv_place(c, head);
-  if (!first_run) lds_barrier();  // the last run's sums and page numbers have been read
-  first_run = false;
 
-  // Loads first, in the order of their use: queries, page numbers, the first
-  // tile; the queries are converted while it is on its way.
   KvRaw<SPLIT> raw[MT][STEPS];
+  auto load_queries = [&](const Run& r) {
+    const int rows = r.rg.n * a.groups;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = 16 * m + col;  // this lane's row
-    const int qi = kv_div(r, a.group_div);
-    const int64_t at = (int64_t)(rg.first + qi) * a.q_token + (head * a.groups + (r - qi * a.groups)) * a.q_head;
+    for (int m = 0; m < MT; ++m) {
+      const int i = 16 * m + col;  // this lane's row
+      const int qi = kv_div(i, a.group_div);
+      const int64_t at = (int64_t)(r.rg.first + qi) * a.q_token + (r.head * a.groups + (i - qi * a.groups)) * a.q_head;
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) {
-      const int d = 16 * NG * quarter + 8 * t;
-      raw[m][t] = kv_load_query<SPLIT>(a, q_vec, at + d, r < rows && d < c.dim);
+      for (int t = 0; t < STEPS; ++t) {
+        const int d = 16 * NG * quarter + 8 * t;
+        raw[m][t] = kv_load_query<SPLIT>(a, q_vec, at + d, i < rows && d < c.dim);
+      }
     }
-  }
+  };
+  // The page numbers of `count` pages from that of key `from` on; -1 where there is no such page.
+  auto page_at = [&](int b, int from, int i) {
+    const int p = a.page_table[b * a.table_stride + kv_div(from, c.page_div) + i];
+    return p >= 0 && p < c.pages ? p : -1;
+  };
 
-  // Runs whose page numbers do not fit are staged in several goes of `span` keys.
-  const int span = (int)min((int64_t)(end - begin), (int64_t)(kFewPages - 2) * c.page_size / kFewStep * kFewStep);
-  int to = begin, p0 = 0;
   // A tile's keys are loaded once the last tile's are used up, its values
   // likewise: two thirds of a tile's time ahead, in the same registers.
   KvGroups<NG, EXACT> kt[2], vt[2];
   uint64_t row[2];       // this lane's rows of the tile that is being loaded
   bool there[2];
   uint32_t exists = 0u;  // which of its 32 keys do
+  int buf = 0, to = 0, p0 = 0;
+  KvPlace place;
   auto locate = [&](int at) {
     exists = 0u;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int j = min(at + 16 * u + col, to - 1);
       const int pi = kv_div(j, c.page_div);
-      const int page = page_of[pi - p0];
+      const int page = page_of[buf * kFewPages + pi - p0];
       there[u] = (page >= 0) & (at + 16 * u + col < to);
       row[u] = kv_offset(place, page, j - pi * c.page_size);
       exists |= (uint32_t)(__ballot(there[u]) & 0xFFFFu) << (16 * u);
@@ -497,22 +515,34 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) x[u] = kv_load<NG, EXACT, true>(codes, scales, row[u], c.dim, g0, there[u]);
   };
-  auto stage = [&](int from) {  // page numbers of the keys from `from` on, then this wave's first tile of them
-    to = min(end, from + span);
-    p0 = kv_div(from, c.page_div);
-    const int count = (int)kv_div(to - 1, c.page_div) - p0 + 1;
-    for (int i = threadIdx.x; i < count; i += 256) {  // -1 where there is no such page
-      const int p = a.page_table[b * a.table_stride + p0 + i];
-      page_of[i] = p >= 0 && p < c.pages ? p : -1;
-    }
-    lds_barrier();
+  // This wave's first tile of the keys from `from` on, whose page numbers are staged.
+  auto begin_span = [&](const Run& r, int from) {
+    to = min(r.end, from + span);
+    p0 = __builtin_amdgcn_readfirstlane(kv_div(from, c.page_div));
+    place = kv_place(c, r.head);
     if (from + wave * kFewTile < to) {
       locate(from + wave * kFewTile);
       load(c.k_codes, c.k_scales, kt);
       load(c.v_codes, c.v_scales, vt);
     }
   };
-  if (begin < end) stage(begin);
+
+  // Loads in the order of their use, and all that the next run needs before
+  // this one's keys: a run that follows another begins with its first tile on
+  // the way while the last one's sums are still being put together.
+  load_queries(now);
+  for (int i = threadIdx.x; i < now.pages + next.pages; i += 256) {
+    const bool second = i >= now.pages;
+    page_of[second ? kFewPages + i - now.pages : i] =
+        second ? page_at(next.b, next.begin, i - now.pages) : page_at(now.b, now.begin, i);
+  }
+  lds_barrier();
+  begin_span(now, now.begin);
+
+  for (;;) {
+  const KvRange rg = now.rg;
+  const int head = now.head, begin = now.begin, end = now.end;
+  const int rows = rg.n * a.groups;
 
   // row `col` of each row tile, values 16 NG quarter ..
   f16x8 q[MT][SPLIT][STEPS];
@@ -699,8 +729,14 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   from = to;
   if (from < end) {
     lds_barrier();
-    stage(from);
+    for (int i = threadIdx.x; i < pages_of(from, end); i += 256) page_of[buf * kFewPages + i] = page_at(now.b, from, i);
+    lds_barrier();
+    begin_span(now, from);
   }
+  }
+  if (more_runs) {  // the next run's first tile
+    buf ^= 1;
+    begin_span(next, next.begin);
   }
 
   // the four waves meet
@@ -741,19 +777,32 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       }
       const int qi = kv_div(r, a.group_div);
       const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + head * a.groups + (r - qi * a.groups);
-      if (whole) {
+      if (now.whole) {
         const float by = l == 0.0f ? 0.0f : value_factor / l;  // a NaN stays one
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= by;
         kv_store4(dt, a.out, row * c.dim + d, v);
         if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? kNone : (mt - kBias + __builtin_log2f(l)) * kLn2;
       } else {
-        const int64_t at = ((int64_t)blockIdx.x + b * c.heads + head) * sh.rows + r;
+        const int64_t at = ((int64_t)blockIdx.x + now.b * c.heads + head) * sh.rows + r;
         kv_store4<kF32>(sh.sums, at * c.dim + d, v);
         if (d == 0) *reinterpret_cast<f32x2*>(sh.stats + 2 * at) = f32x2{mt, l};
       }
     }
   }
+  if (!more_runs) return;
+  now = next;
+  load_queries(now);
+  // (scanned anew: kept, the scan would cost the loop a dozen registers)
+  more_runs = unit < last_unit;
+  if (more_runs) {
+    KvScan again;
+    kv_scan(c, a, sh.rows, base, before, again);
+    more_runs = next_run(again, next);
+    if (more_runs)
+      for (int i = threadIdx.x; i < next.pages; i += 256) page_of[(buf ^ 1) * kFewPages + i] = page_at(next.b, next.begin, i);
+  }
+  lds_barrier();  // the sums have been read and the next page numbers are there
   }
 }
 
@@ -1289,7 +1338,7 @@ hipError_t allow_lds(K* kernel, bool (&set)[64]) {
 template <int NG, bool EXACT>
 hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvShare& sh, const KvPlan& p, int dt, bool q_vec,
                       hipStream_t s) {
-  const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 4 * kFewPages;
+  const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 2 * 4 * kFewPages;
 #define KV_FEW(MT, SPLIT)                                                                         \
   do {                                                                                            \
     static bool set[64];                                                                          \
