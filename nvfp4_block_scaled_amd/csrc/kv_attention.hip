@@ -95,19 +95,39 @@ struct KvGroups {
   uint32_t w[2 * NG];
   uint32_t s[EXACT ? 1 : NG];  // scale bytes: of all groups in one, or one each (joining them would wait for the loads)
 };
-// Where a head's codes start, counted from the start of the codes, by page:
-// byte page * page_bytes + head_bytes + offset * dim/2; its scales at an
-// eighth of that.  (page_bytes < 2^32: one multiply-add for the page.)
+// The codes of a row begin at byte page * page_bytes + head_bytes + offset *
+// dim/2, its scales at an eighth of that.  (page_bytes < 2^32: one
+// multiply-add for the page.)
 struct KvPlace {
-  uint32_t page_bytes, row_bytes;
+  uint32_t page_bytes;
   uint64_t head_bytes;
 };
 __device__ __forceinline__ KvPlace kv_place(const KvCache& c, int head) {
-  return KvPlace{(uint32_t)(c.heads * c.page_size) * (uint32_t)(c.dim / 2), (uint32_t)(c.dim / 2),
+  return KvPlace{(uint32_t)(c.heads * c.page_size) * (uint32_t)(c.dim / 2),
                  (uint64_t)head * c.page_size * (c.dim / 2)};
 }
-__device__ __forceinline__ uint64_t kv_offset(const KvPlace& p, int page, int off) {
-  return (uint64_t)(uint32_t)page * p.page_bytes + (p.head_bytes + (uint64_t)(uint32_t)off * p.row_bytes);
+__device__ __forceinline__ uint64_t kv_page_start(const KvPlace& p, int page) {
+  return (uint64_t)(uint32_t)page * p.page_bytes + p.head_bytes;
+}
+template <int NG, bool EXACT>
+__device__ __forceinline__ uint32_t kv_row_start(int off, int dim) {
+  return (uint32_t)off * (EXACT ? 32u * NG : (uint32_t)dim / 2);
+}
+
+// A key's page (counted from the run's first) and its offset there, moved on
+// by a fixed number of keys without a division.
+struct KvStep {
+  int pages, rest;  // keys = pages * page_size + rest
+};
+__device__ __forceinline__ KvStep kv_step(const KvCache& c, int keys) {
+  const int q = __builtin_amdgcn_readfirstlane(kv_div(keys, c.page_div));
+  return KvStep{q, keys - q * c.page_size};
+}
+__device__ __forceinline__ void kv_advance(const KvStep& s, int page_size, int& page, int& off) {
+  off += s.rest;
+  const bool over = off >= page_size;
+  page += s.pages + (over ? 1 : 0);
+  off -= over ? page_size : 0;
 }
 
 template <bool ONCE, typename T>
@@ -386,7 +406,8 @@ __device__ __forceinline__ int kv_units_each(const KvCache& c, const KvAttention
 // transposed (ds_read_b64_tr_b16); nothing in the loop waits for another wave.
 
 constexpr int few_row_bytes(int NG) { return 128 * NG + 32; }  // a key's values in LDS: +32 spreads the banks
-constexpr int kFewPages = 1024;  // page numbers staged at a time
+constexpr int kFewPages = 512;  // pages staged at a time
+constexpr uint64_t kNoPage = ~0ull;
 
 // Waves per SIMD (and workgroups per CU) that the registers of an instance
 // allow without spills.
@@ -401,7 +422,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   constexpr int DP = 64 * NG, STEPS = 2 * NG, DB = DP / 16, RB = few_row_bytes(NG);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ float stat_m[kFewWaves][16 * MT], stat_l[kFewWaves][16 * MT];
-  int* page_of = reinterpret_cast<int*>(lds + kFewWaves * kFewTile * RB);  // of this run and of the next one
+  uint64_t* page_of = reinterpret_cast<uint64_t*>(lds + kFewWaves * kFewTile * RB);  // of this run and of the next one
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, quarter = lane >> 4;
   uint8_t* mine = lds + wave * kFewTile * RB;
@@ -485,10 +506,10 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       }
     }
   };
-  // The page numbers of `count` pages from that of key `from` on; -1 where there is no such page.
-  auto page_at = [&](int b, int from, int i) {
-    const int p = a.page_table[b * a.table_stride + kv_div(from, c.page_div) + i];
-    return p >= 0 && p < c.pages ? p : -1;
+  // Where this head's codes start in the i-th page from that of key `from` on.
+  auto page_at = [&](const Run& r, int from, int i) {
+    const int p = a.page_table[r.b * a.table_stride + kv_div(from, c.page_div) + i];
+    return p >= 0 && p < c.pages ? kv_page_start(kv_place(c, r.head), p) : kNoPage;
   };
 
   // A tile's keys are loaded once the last tile's are used up, its values
@@ -497,18 +518,18 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   uint64_t row[2];       // this lane's rows of the tile that is being loaded
   bool there[2];
   uint32_t exists = 0u;  // which of its 32 keys do
-  int buf = 0, to = 0, p0 = 0;
-  KvPlace place;
+  int buf = 0, to = 0, staged = 0;
+  int page[2], off[2];   // of this lane's keys, from the span's first page
+  const KvStep step = kv_step(c, kFewStep);
   auto locate = [&](int at) {
     exists = 0u;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int j = min(at + 16 * u + col, to - 1);
-      const int pi = kv_div(j, c.page_div);
-      const int page = page_of[buf * kFewPages + pi - p0];
-      there[u] = (page >= 0) & (at + 16 * u + col < to);
-      row[u] = kv_offset(place, page, j - pi * c.page_size);
+      const uint64_t start = page_of[buf * kFewPages + min(page[u], staged - 1)];
+      there[u] = (start != kNoPage) & (at + 16 * u + col < to);
+      row[u] = start + kv_row_start<NG, EXACT>(off[u], c.dim);
       exists |= (uint32_t)(__ballot(there[u]) & 0xFFFFu) << (16 * u);
+      kv_advance(step, c.page_size, page[u], off[u]);
     }
   };
   auto load = [&](const uint8_t* codes, const uint8_t* scales, KvGroups<NG, EXACT>(&x)[2]) {
@@ -518,10 +539,18 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   // This wave's first tile of the keys from `from` on, whose page numbers are staged.
   auto begin_span = [&](const Run& r, int from) {
     to = min(r.end, from + span);
-    p0 = __builtin_amdgcn_readfirstlane(kv_div(from, c.page_div));
-    place = kv_place(c, r.head);
-    if (from + wave * kFewTile < to) {
-      locate(from + wave * kFewTile);
+    staged = pages_of(from, r.end);
+    const int first = from + wave * kFewTile;
+    if (first < to) {
+      const int p0 = kv_div(from, c.page_div);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int j = first + 16 * u + col;
+        page[u] = (int)kv_div(j, c.page_div);
+        off[u] = j - page[u] * c.page_size;
+        page[u] -= p0;
+      }
+      locate(first);
       load(c.k_codes, c.k_scales, kt);
       load(c.v_codes, c.v_scales, vt);
     }
@@ -534,7 +563,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   for (int i = threadIdx.x; i < now.pages + next.pages; i += 256) {
     const bool second = i >= now.pages;
     page_of[second ? kFewPages + i - now.pages : i] =
-        second ? page_at(next.b, next.begin, i - now.pages) : page_at(now.b, now.begin, i);
+        second ? page_at(next, next.begin, i - now.pages) : page_at(now, now.begin, i);
   }
   lds_barrier();
   begin_span(now, now.begin);
@@ -729,7 +758,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   from = to;
   if (from < end) {
     lds_barrier();
-    for (int i = threadIdx.x; i < pages_of(from, end); i += 256) page_of[buf * kFewPages + i] = page_at(now.b, from, i);
+    for (int i = threadIdx.x; i < pages_of(from, end); i += 256) page_of[buf * kFewPages + i] = page_at(now, from, i);
     lds_barrier();
     begin_span(now, from);
   }
@@ -800,7 +829,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     kv_scan(c, a, sh.rows, base, before, again);
     more_runs = next_run(again, next);
     if (more_runs)
-      for (int i = threadIdx.x; i < next.pages; i += 256) page_of[(buf ^ 1) * kFewPages + i] = page_at(next.b, next.begin, i);
+      for (int i = threadIdx.x; i < next.pages; i += 256) page_of[(buf ^ 1) * kFewPages + i] = page_at(next, next.begin, i);
   }
   lds_barrier();  // the sums have been read and the next page numbers are there
   }
@@ -860,8 +889,16 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   // The page number of this thread's key, as it stands in the table (checked
   // when it is used, a tile later: nothing may wait for it here).  Past the
   // end the last key's.
-  auto lookup = [&](int tile) {
-    return a.page_table[b * a.table_stride + kv_div(min(tile + key_of, end - 1), c.page_div)];
+  const KvStep step = kv_step(c, TILE);
+  const int32_t* table = a.page_table + b * a.table_stride;
+  const int last_page = begin < end ? (int)kv_div(end - 1, c.page_div) : 0;
+  int page_l = kv_div(begin + key_of, c.page_div);  // page and offset of the next tile to look up
+  int off_l = begin + key_of - page_l * c.page_size;
+  int page_d = page_l, off_d = off_l;               // .. and to load
+  auto lookup = [&]() {
+    const int p = table[min(page_l, last_page)];
+    kv_advance(step, c.page_size, page_l, off_l);
+    return p;
   };
   KvGroups<NG, EXACT> kt, vt;
   int live = 0;
@@ -870,7 +907,8 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
     const int j = tile + key_of;
     const bool there = (page >= 0) & (page < c.pages) & (j < end);
     live = there | (j >= end);  // past the end every row's mask holds
-    const uint64_t row = kv_offset(place, page, j - (int)kv_div(j, c.page_div) * c.page_size);
+    const uint64_t row = kv_page_start(place, page) + kv_row_start<NG, EXACT>(off_d, c.dim);
+    kv_advance(step, c.page_size, page_d, off_d);
     if constexpr (BOTH) {
       kt = kv_load<NG, EXACT, false>(c.k_codes, c.k_scales, row, c.dim, g0, there);
       vt = kv_load<NG, EXACT, false>(c.v_codes, c.v_scales, row, c.dim, g0, there);
@@ -894,8 +932,8 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   };
   int page = 0, page2 = 0;
   if (begin < end) {
-    page = lookup(begin);
-    page2 = lookup(begin + TILE);
+    page = lookup();
+    page2 = lookup();
   }
 
   // queries: row `col` of this wave's 32
@@ -942,13 +980,13 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   if (begin < end) {
     load(begin, page);
     page = page2;
-    page2 = lookup(begin + 2 * TILE);
+    page2 = lookup();
     store_flags(0);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) store_piece(0, i);
-    if (begin + TILE < end) load(begin + TILE, page);
+    load(begin + TILE, page);
     page = page2;
-    page2 = lookup(begin + 3 * TILE);
+    page2 = lookup();
     lds_barrier();
   }
   int buf = 0;
@@ -999,9 +1037,9 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (tile + 2 * TILE < end) load(tile + 2 * TILE, page);
+    load(tile + 2 * TILE, page);  // (past the end: nothing)
     page = page2;
-    page2 = lookup(tile + 4 * TILE);
+    page2 = lookup();
     {
       const bool edge = tile < all_lo || tile + TILE > all_hi, holes = have != ~0ull;
       if (edge) {
@@ -1338,7 +1376,7 @@ hipError_t allow_lds(K* kernel, bool (&set)[64]) {
 template <int NG, bool EXACT>
 hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvShare& sh, const KvPlan& p, int dt, bool q_vec,
                       hipStream_t s) {
-  const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 2 * 4 * kFewPages;
+  const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 2 * 8 * kFewPages;
 #define KV_FEW(MT, SPLIT)                                                                         \
   do {                                                                                            \
     static bool set[64];                                                                          \
