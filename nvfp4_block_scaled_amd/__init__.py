@@ -763,25 +763,29 @@ class KVCache:
         codes, scales, device = k_codes.shape, k_scales.shape, k_codes.device
         if len(codes) != 4:
             raise ValueError("k_codes must be [pages, heads, page_size, dim/2]")
-        if v_codes.shape != codes or v_scales.shape != scales or scales[:3] != codes[:3] \
-                or scales[3] * 8 != codes[3]:
+        pages, heads, page_size, half = codes
+        if v_codes.shape != codes or v_scales.shape != scales or half & 7 \
+                or scales != (pages, heads, page_size, half >> 3):
             raise ValueError("the codes and scales of keys and values describe different shapes")
-        for t in (k_codes, k_scales, v_codes, v_scales):
-            if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous():
-                raise ValueError("codes and scales must be contiguous uint8 tensors of one device")
-        pointers = []
-        for g, name in ((global_scale_k, "global_scale_k"), (global_scale_v, "global_scale_v")):
-            if g is not None and (g.numel() != 1 or g.dtype is not torch.float32 or g.device != device):
-                raise ValueError(f"{name} must be a float32 scalar on the cache's device")
-            pointers.append(None if g is None else g.data_ptr())
+        if not (k_codes.dtype is k_scales.dtype is v_codes.dtype is v_scales.dtype is torch.uint8
+                and device == k_scales.device == v_codes.device == v_scales.device
+                and k_codes.is_contiguous() and k_scales.is_contiguous()
+                and v_codes.is_contiguous() and v_scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous uint8 tensors of one device")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.global_scale_k, self.global_scale_v = global_scale_k, global_scale_v
-        self.pages, self.heads, self.page_size, half = codes
-        self.dim = 2 * half
-        self.device = device
-        self._struct = _KVCacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                      v_scales.data_ptr(), *pointers, self.pages, self.page_size, self.heads,
-                                      self.dim)
+        self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, 2 * half, device
+        self._struct = _KVCacheStruct(
+            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+            None if global_scale_k is None else _kv_scalar(global_scale_k, "global_scale_k", device),
+            None if global_scale_v is None else _kv_scalar(global_scale_v, "global_scale_v", device),
+            pages, page_size, heads, self.dim)
+
+
+def _kv_scalar(g, name, device):
+    if g.numel() != 1 or g.dtype is not torch.float32 or g.device != device:
+        raise ValueError(f"{name} must be a float32 scalar on the cache's device")
+    return g.data_ptr()
 
 
 def kv_cache(pages, page_size, heads, dim, global_scale_k=None, global_scale_v=None, device="cuda"):
