@@ -281,30 +281,24 @@ __device__ __forceinline__ float kv_query_top(KvRaw<SPLIT>& r, int dt) {
   for (int i = 0; i < 4 * SPLIT; ++i) r.w[i] = opaque((int)r.w[i]);
   return top;
 }
-// Times `power` as one or two float16.
+// Times 2^-e as one or two float16.
 template <int SPLIT>
-__device__ __forceinline__ void kv_query_halves(const KvRaw<SPLIT>& r, int dt, float power, f16x8& hi, f16x8& lo) {
+__device__ __forceinline__ void kv_query_halves(const KvRaw<SPLIT>& r, int dt, int e, f16x8& hi, f16x8& lo) {
   float x[8];
   kv_unpack_query<SPLIT>(r, dt, x);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = x[i] * power;
+    const float y = __builtin_ldexpf(x[i], -e);
     hi[i] = (_Float16)y;
     if constexpr (SPLIT == 2) lo[i] = (_Float16)(y - (float)hi[i]);
   }
 }
 
-// The power of two 2^-e that brings a row of largest magnitude `top` to
-// 2^13 .. 2^14, and 2^e.  Rows of zeros, infinities and NaN stay as they are.
-__device__ __forceinline__ float kv_row_power(float top, float& back) {
+// e such that 2^-e brings a row of largest magnitude `top` to 2^13 .. 2^14.
+// Rows of zeros, infinities and NaN stay as they are.
+__device__ __forceinline__ int kv_row_exponent(float top) {
   const int field = (int)((__float_as_uint(top) >> 23) & 0xFFu);
-  if (!(top > 0.0f) || field == 255) {
-    back = 1.0f;
-    return 1.0f;
-  }
-  const int e = max(-112, field - 140);
-  back = __builtin_ldexpf(1.0f, e);
-  return __builtin_ldexpf(1.0f, -e);
+  return !(top > 0.0f) || field == 255 ? 0 : field - 140;
 }
 
 template <int DT>
@@ -584,11 +578,10 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     for (int t = 0; t < STEPS; ++t) top = fmaxf(top, kv_query_top<SPLIT>(raw[m][t], dt));
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    float back;
-    const float power = kv_row_power(top, back);
-    factor[m] = key_factor * back;
+    const int e = kv_row_exponent(top);
+    factor[m] = __builtin_ldexpf(key_factor, e);
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[m][t], dt, power, q[m][0][t], q[m][SPLIT - 1][t]);
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[m][t], dt, e, q[m][0][t], q[m][SPLIT - 1][t]);
     const int r = 16 * m + col;
     const int pos = rg.context - rg.n + (int)kv_div(r, a.group_div);
     see_hi[m] = r >= rows ? 0 : a.causal ? min(rg.hi, pos + 1) : rg.hi;
@@ -953,11 +946,10 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
       top = fmaxf(top, kv_query_top<SPLIT>(raw[t], dt));
     }
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    float back;
-    const float power = kv_row_power(top, back);
-    factor = a.scale * kLog2e * global_decode(c.global_k) * back;
+    const int e = kv_row_exponent(top);
+    factor = __builtin_ldexpf(a.scale * kLog2e * global_decode(c.global_k), e);
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, power, q[0][t], q[SPLIT - 1][t]);
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, e, q[0][t], q[SPLIT - 1][t]);
   }
   const int pos = rg.context - rg.n + qi;
   const int see_hi = !row_live ? 0 : a.causal ? min(end, pos + 1) : end;
