@@ -642,7 +642,8 @@ typedef struct nvfp4_kv_cache {
  *           [0, pages * page_size) is skipped (padding).  Two tokens with the
  *           same slot leave it undefined.
  * Errors: bad dtype or cache, tokens < 0, negative stride, NULL pointer, k
- * or v not aligned to its element; UNSUPPORTED for tokens * dim / 8 >= 2^31.
+ * or v not aligned to its element; UNSUPPORTED for tokens * dim / 8 >= 2^31
+ * or tokens * heads * dim >= 2^36.
  */
 nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
                             int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,

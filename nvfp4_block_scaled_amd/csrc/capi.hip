@@ -1213,7 +1213,7 @@ static nvfp4_status check_kv(const char* op, const nvfp4_kv_cache* cache, nvfp4_
   if (tokens < 0)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tokens (%lld) must be >= 0.", op, (long long)tokens);
   if (tokens > INT32_MAX || tokens * (cache->dim / 8) > INT32_MAX - 4096 ||
-      (tokens * (cache->dim / 8) / 512 + 1) * 2 * cache->heads > INT32_MAX)
+      (tokens * (cache->dim / 8) / 512 + 1) * 2 * cache->heads >= 1 << 24)
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large (tokens * dim / 8 of 2^31 or more).", op);
   *c = nvfp4::KvCache{cache->k_codes,        cache->k_scales,       cache->v_codes,     cache->v_scales,
                       cache->global_scale_k, cache->global_scale_v, (int)cache->pages,  (int)cache->page_size,
