@@ -618,7 +618,8 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
  *   k_codes, v_codes    device uint8 [pages, heads, page_size, dim/2], 16-byte aligned
  *   k_scales, v_scales  device uint8 [pages, heads, page_size, dim/16], 16-byte aligned
  * page_size >= 1, dim a multiple of 16 and at most 256, pages * page_size <
- * 2^31, heads < 2^15, the codes of one page below 4 GiB.  The struct is read during the call only; the memory is the caller's.
+ * 2^31, heads < 2^15, the codes of one page below 4 GiB.  The struct is read
+ * during the call only; the memory is the caller's.
  * Slots that were never written may hold any bytes: no call reads a token
  * outside the slots or contexts that it is given.
  */
@@ -692,7 +693,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
  * The cached values are exact in the products (codes times block scales fit
  * float16; the global scales multiply scores and sums in float32); each
  * probability is rounded to float16 before its product with the values, for
- * float32 q to a pair of float16.
+ * float32 q to a pair of float16.  Small probabilities keep their bits too
+ * (2^-11 of each, not of the largest).
  * Errors: bad dtype or cache, negative or zero sizes (tokens or seqs = 0 is
  * a no-op), query_heads not a multiple of heads, query_starts NULL with
  * tokens != seqs or max_queries != 1, window < 0 or window > 0 without

@@ -334,10 +334,10 @@ __device__ __forceinline__ void kv_store4(int dt, void* out, int64_t e, const fl
 // pair, or the end of one and the beginning of the next ones.  The part of
 // pair p that workgroup g computes has the number g + p, which no other part
 // has.  A pair that one workgroup takes whole is written out by it; the parts
-// of the others are joined by a second launch.  (One workgroup per fixed
+// of the others are joined by a second launch, 5 us.  (One workgroup per fixed
 // chunk of keys instead cost 3 us of start and end for each chunk, and left
-// compute units idle in the last round: 57 - 110 us against 46 us for 32
-// contexts of up to 8192, 8 heads.)
+// compute units idle in the last round: 57 - 110 us, by the chunk's length,
+// against 50 for 32 contexts of up to 8192, 8 heads.)
 constexpr int kFewWaves = 4;
 constexpr int kFewTile = 32;
 constexpr int kFewStep = kFewWaves * kFewTile;
@@ -407,6 +407,13 @@ __device__ __forceinline__ int kv_units_each(const KvCache& c, const KvAttention
 // O^T = V^T P^T, so probabilities never leave their lane.  Values are decoded
 // the same way, written to the wave's own LDS as float16 and read back
 // transposed (ds_read_b64_tr_b16); nothing in the loop waits for another wave.
+//
+// Bound by memory while contexts are long: 4 x 131072 keys, 8 heads of 128,
+// 604 MB, 118 us with the join, 5.1 TB/s.  Shorter ones show the start, a chain of
+// four dependent loads (lengths, page number, codes; queries beside them),
+// about 7 us, and the join: 32 contexts of up to 8192, 166 MB, 50 us, 3.3
+// TB/s.  A whole tile in flight a wave and three workgroups a CU cover the
+// latency (1 or 2 a CU: 81 and 58 us).
 
 constexpr int few_row_bytes(int NG) { return 128 * NG + 32; }  // a key's values in LDS: +32 spreads the banks
 constexpr int kFewPages = 512;  // pages staged at a time
@@ -847,6 +854,16 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 // earlier) are decoded into the other, and the loads of the one after it are
 // under way; one barrier a tile.  Rows of LDS are padded so that the 16-byte
 // reads of K and the transposing reads of V touch every bank once.
+//
+// Bound by instruction issue: the 16 scores a lane holds of a 32 x 32 tile
+// take 512 cycles of the matrix cores (dim 128) and about 320 of the vector
+// units (each an exponential, 8.6, a multiply-add, 4.9, half a conversion to
+// float16, 3.7, maximum and sum), besides decoding and LDS reads.  4096 causal queries over as many
+// keys, 32 heads of 128: 182 us, 750 TFLOP/s; up to 1023 queries each of 5
+// sequences over up to 9001 keys: 427 us, 715 TFLOP/s; a large bfloat16
+// matrix product reaches 1280.  256 rows and 8 waves share the decoding
+// further, but leave one workgroup a CU: 192 against 198 us and 470 against
+// 440 (kernels of the time).
 //
 // Too few workgroups for the GPU split the keys further (KvChunks).
 constexpr int kManyRows = 128;
@@ -1315,7 +1332,9 @@ __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttentio
 // ----------------------------------------------------------------- launches
 
 // Contexts of up to so many keys are left to one workgroup a pair: no parts, no
-// second launch.
+// second launch.  8 heads of 128, us, alone against shared out with the join:
+// 700 keys, 1 sequence 14.1 / 13.4, 16 sequences 15.0 / 18.0; 1024 keys 16.2 /
+// 13.3 and 17.2 / 18.5; 2048 keys, 1 sequence, 24.7 / 14.0.
 constexpr int kFewAlone = 1024;
 
 struct KvPlan {
@@ -1328,8 +1347,9 @@ struct KvPlan {
 constexpr int few_groups(int dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : dim <= 192 ? 3 : 4; }
 
 // Up to 32 rows a (sequence, kv head) the keys are streamed once past all of
-// them, which the few-rows kernel does at the speed of memory; more rows are
-// matrix work.
+// them; more rows are matrix work.  32 rows, 8 x 30000 keys, 4 heads, few
+// against many, us: dim 128 76 / 90, float32 92 / 175; dim 256 128 / 254,
+// float32 282 / 317 (40 rows of dim 128 on the many-rows kernel: 95).
 KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_queries * a.groups;
@@ -1348,7 +1368,11 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
     const int64_t tiles = pairs * p.row_tiles;
-    // short contexts are not worth a second launch for less than a whole factor of two
+    // As many workgroups as run at once, rounded to the nearest number of
+    // splits; for short contexts rounded down, as a second launch is worth only
+    // a whole factor there.  3 x 400 queries, 32 heads of 128, us, nearest
+    // against down: 2000 keys 102 / 88, 4200 keys 168 / 168, 9000 keys 315 /
+    // 371; 3 x 777 over 777 keys, 16 heads, 57 / 34.
     int64_t splits = (2 * device_cu_count() + (keys >= 4096 ? tiles / 2 : 0)) / tiles;
     const int64_t most = keys / 256;
     if (splits > most) splits = most;

@@ -34,7 +34,7 @@ __device__ __forceinline__ void load_values(const void* base, int64_t e, float (
   }
 }
 
-// Half group h of a head: its token and place there.  A lane takes kEach of
+// Half group h of a head: its token and place there.  A lane takes so many of
 // them, a workgroup's width apart, all their loads ahead of the first use.
 constexpr int kWriteEach = 2, kReadEach = 4;
 
