@@ -409,7 +409,7 @@ __device__ __forceinline__ int kv_units_each(const KvCache& c, const KvAttention
 // transposed (ds_read_b64_tr_b16); nothing in the loop waits for another wave.
 //
 // Bound by memory while contexts are long: 4 x 131072 keys, 8 heads of 128,
-// 604 MB, 118 us with the join, 5.1 TB/s.  Shorter ones show the start, a chain of
+// 604 MB, 112 - 118 us with the join, 5.1 - 5.4 TB/s.  Shorter ones show the start, a chain of
 // four dependent loads (lengths, page number, codes; queries beside them),
 // about 7 us, and the join: 32 contexts of up to 8192, 166 MB, 50 us, 3.3
 // TB/s.  A whole tile in flight a wave and three workgroups a CU cover the
@@ -859,9 +859,9 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 // take 512 cycles of the matrix cores (dim 128) and about 320 of the vector
 // units (each an exponential, 8.6, a multiply-add, 4.9, half a conversion to
 // float16, 3.7, maximum and sum), besides decoding and LDS reads.  4096 causal queries over as many
-// keys, 32 heads of 128: 182 us, 750 TFLOP/s; up to 1023 queries each of 5
-// sequences over up to 9001 keys: 427 us, 715 TFLOP/s; a large bfloat16
-// matrix product reaches 1280.  256 rows and 8 waves share the decoding
+// keys, 32 heads of 128: 182 - 194 us by the machine, 710 - 755 TFLOP/s; up to
+// 1023 queries each of 5 sequences over up to 9001 keys: 427 - 492 us, 620 -
+// 715 TFLOP/s; a large bfloat16 matrix product reaches 1280.  256 rows and 8 waves share the decoding
 // further, but leave one workgroup a CU: 192 against 198 us and 470 against
 // 440 (kernels of the time).
 //
