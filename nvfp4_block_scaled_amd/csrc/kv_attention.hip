@@ -1332,10 +1332,18 @@ __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttentio
 // ----------------------------------------------------------------- launches
 
 // Contexts of up to so many keys are left to one workgroup a pair: no parts, no
-// second launch.  8 heads of 128, us, alone against shared out with the join:
-// 700 keys, 1 sequence 14.1 / 13.4, 16 sequences 15.0 / 18.0; 1024 keys 16.2 /
-// 13.3 and 17.2 / 18.5; 2048 keys, 1 sequence, 24.7 / 14.0.
-constexpr int kFewAlone = 1024;
+// second launch, and with many pairs fewer runs to begin.  8 heads of 128, us,
+// alone against shared out with the join:
+//   700 keys: 1 sequence 14.1 / 13.4, 16 sequences 15.0 / 18.0; 1024 keys: 16.2 /
+//   13.3, 17.2 / 18.5
+//   2048 keys: 1 sequence 24.7 / 14.0; 16 26.2 / 27.6 (heads of 256 40 / 32); 64
+//   40 / 51; 128, lengths up to that 55 / 82
+//   4096 keys: 64 sequences 72 / 83, lengths up to that 58 / 63
+// Past 4096 keys one long context among short ones would keep all waiting.
+constexpr int kFewAlone = 1024, kFewAloneMost = 4096;
+constexpr int64_t few_alone(int64_t pairs) {
+  return pairs >= (kFewAloneMost - kFewAlone) / 6 ? kFewAloneMost : kFewAlone + 6 * pairs;
+}
 
 struct KvPlan {
   bool few;
@@ -1363,8 +1371,9 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
     // as many workgroups as run at once, but no more than there can be units
     const int64_t units = pairs * (keys > kFewStep ? (keys + kFewStep - 1) / kFewStep : 1);
     const int64_t most = (int64_t)device_cu_count() * few_occupancy(few_groups(c.dim), p.mt, split);
-    p.groups = (int)(keys <= kFewAlone ? pairs : units < most ? units : most);
-    parts = keys > kFewAlone ? (size_t)(p.groups + pairs) * 16 * p.mt : 0;
+    const bool alone = keys <= few_alone(pairs);
+    p.groups = (int)(alone ? pairs : units < most ? units : most);
+    parts = alone ? 0 : (size_t)(p.groups + pairs) * 16 * p.mt;
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
     const int64_t tiles = pairs * p.row_tiles;
