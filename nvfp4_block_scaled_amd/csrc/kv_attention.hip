@@ -409,7 +409,7 @@ __device__ __forceinline__ int kv_units_each(const KvCache& c, const KvAttention
 // transposed (ds_read_b64_tr_b16); nothing in the loop waits for another wave.
 //
 // Bound by memory while contexts are long: 4 x 131072 keys, 8 heads of 128,
-// 604 MB, 112 - 118 us with the join, 5.1 - 5.4 TB/s.  Shorter ones show the start, a chain of
+// 604 MB, 112 - 120 us with the join, 5.0 - 5.4 TB/s.  Shorter ones show the start, a chain of
 // four dependent loads (lengths, page number, codes; queries beside them),
 // about 7 us, and the join: 32 contexts of up to 8192, 166 MB, 50 us, 3.3
 // TB/s.  A whole tile in flight a wave and three workgroups a CU cover the
