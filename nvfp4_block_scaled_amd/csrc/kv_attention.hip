@@ -290,14 +290,14 @@ __device__ __forceinline__ float kv_query_top(KvRaw<SPLIT>& r, int dt) {
   for (int i = 0; i < 4 * SPLIT; ++i) r.w[i] = opaque((int)r.w[i]);
   return top;
 }
-// Times 2^-e as one or two float16.
+// Times sign 2^-e as one or two float16.
 template <int SPLIT>
-__device__ __forceinline__ void kv_query_halves(const KvRaw<SPLIT>& r, int dt, int e, f16x8& hi, f16x8& lo) {
+__device__ __forceinline__ void kv_query_halves(const KvRaw<SPLIT>& r, int dt, int e, float sign, f16x8& hi, f16x8& lo) {
   float x[8];
   kv_unpack_query<SPLIT>(r, dt, x);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = __builtin_ldexpf(x[i], -e);
+    const float y = __builtin_ldexpf(x[i], -e) * sign;
     hi[i] = (_Float16)y;
     if constexpr (SPLIT == 2) lo[i] = (_Float16)(y - (float)hi[i]);
   }
@@ -597,7 +597,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     const int e = kv_row_exponent(top);
     factor[m] = __builtin_ldexpf(key_factor, e);
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[m][t], dt, e, q[m][0][t], q[m][SPLIT - 1][t]);
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[m][t], dt, e, 1.0f, q[m][0][t], q[m][SPLIT - 1][t]);
     const int r = 16 * m + col;
     const int pos = rg.context - rg.n + (int)kv_div(r, a.group_div);
     see_hi[m] = r >= rows ? 0 : a.causal ? min(rg.hi, pos + 1) : rg.hi;
@@ -973,9 +973,16 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
     }
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const int e = kv_row_exponent(top);
+    // The masks and extremes below are those of the bare products, so the
+    // factor has to be positive.  Its sign (or NaN) goes into the query.  A
+    // factor of 0, of a global scale of 0 or of a row so small that it
+    // underflows, becomes the smallest normal number: scores stay below 2^-90,
+    // as good as 0, and those that are masked stay -inf.
     factor = __builtin_ldexpf(a.scale * kLog2e * global_decode(c.global_k), e);
+    const float sign = factor < 0.0f ? -1.0f : factor != factor ? factor : 1.0f;
+    factor = fmaxf(__builtin_fabsf(factor), 0x1p-126f);
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, e, q[0][t], q[SPLIT - 1][t]);
+    for (int t = 0; t < STEPS; ++t) kv_query_halves<SPLIT>(raw[t], dt, e, sign, q[0][t], q[SPLIT - 1][t]);
   }
   const int pos = rg.context - rg.n + qi;
   const int see_hi = !row_live ? 0 : a.causal ? min(end, pos + 1) : end;
