@@ -48,7 +48,13 @@ constexpr float kNone = -__builtin_huge_valf();
 // scores of 1.8 nats deviation, 5 x up to 1023 queries over up to 9001 keys:
 // 441 us without any such handling, 468 with it; with kLag 3 and kBias 12, a
 // window of 2^26, 550.
+//
+// Large scores.  A weight's exponent is score - sub with sub = maximum - kBias
+// rounded.  Beyond kBig that rounding, and that of scores which are products
+// never rounded by themselves, could let weights pass 65504; so there exponents
+// are kept below kMost apart.  Elsewhere they are at most kLag + kBias + 2^-4.
 constexpr float kLag = 0.9f, kBias = 15.0f;
+constexpr float kBig = 0x1p18f, kMost = 15.99f;
 constexpr float kSmall = -14.0f, kShift = 29.0f;
 constexpr float kUp = 0x1p29f, kDown = 0x1p-29f;
 constexpr float kRest = 0x1p11f;
@@ -234,6 +240,9 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
   return r;
 }
+
+// A weight's exponent, at most kMost (a NaN stays one).
+__device__ __forceinline__ float kv_most(float t) { return t > kMost ? kMost : t; }
 
 // ----------------------------------------------------------------- queries
 
@@ -612,6 +621,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 
   f32x4 acc[MT][DB];
   float m_run[MT], sub[MT], l_run[MT];
+  bool large = false;  // some row has had a maximum beyond kBig
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     m_run[m] = kNone;
@@ -682,6 +692,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
         const float keep = m_run[m] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m_run[m] - next);
         m_run[m] = next;
         sub[m] = next == kNone ? -kBias : next - kBias;
+        large |= __any(__builtin_fabsf(sub[m]) > kBig) != 0;
         l_run[m] *= keep;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -690,6 +701,10 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[m][i] -= sub[m];
+      if (large) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[m][i] = kv_most(x[m][i]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; i += 2) low = min3(low, x[m][i], x[m][i + 1]);
     }
@@ -1001,6 +1016,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
   float m_run = kNone, sub = -kBias, l_run = 0.0f;
+  uint64_t large = 0;  // lanes whose rows have had a maximum beyond kBig
 
   if (begin < end) {
     load(begin, page);
@@ -1105,6 +1121,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         const float keep = m_run == kNone ? 0.0f : __builtin_amdgcn_exp2f(m_run - next);
         m_run = next;
         sub = next == kNone ? -kBias : next - kBias;
+        large |= __ballot(__builtin_fabsf(sub) > kBig);
         l_run *= keep;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -1122,15 +1139,30 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         p[u][i >> 3][0][i & 7] = (_Float16)w;
         if constexpr (SPLIT == 2) p[u][i >> 3][SPLIT - 1][i & 7] = (_Float16)((w - (float)(_Float16)w) * kRest);
       };
-      if (__any(low - sub < kSmall)) {  // the bands of small weights, then the rest
-        const float f = opaque(factor), below = opaque(sub);
+      float by = factor, below = sub;  // a weight's exponent is s * by - below
+      if (__ballot(low - sub < kSmall) | large) {  // the bands of small weights, then the rest
+        if (large) {
+          const float f = opaque(factor), less = opaque(sub);
+          const bool big = __builtin_fabsf(less) > kBig;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+#pragma clang fp contract(off)
+              const float x = s[u][i] * f;
+              s[u][i] = big ? kv_most(x - less) : s[u][i];
+            }
+          by = big ? 1.0f : by;
+          below = big ? 0.0f : below;
+        }
+        const float f = opaque(by), less = opaque(below);
         float shift = kShift, up = kUp, down = kDown;
         bool any = false;
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float t = __builtin_fmaf(s[u][i], f, -below);
+            const float t = __builtin_fmaf(s[u][i], f, -less);
             any |= (t < kSmall) & (t > kNone);
           }
         for (int band = 1; band < kBands && __any(any); ++band) {
@@ -1139,7 +1171,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
           for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float t = __builtin_fmaf(s[u][i], f, -below) + shift;
+              const float t = __builtin_fmaf(s[u][i], f, -less) + shift;
               const bool lower = (t < kSmall) & (band < kBands - 1);
               const bool in = (t < kSmall + kShift) & !lower;
               const float w = in ? __builtin_amdgcn_exp2f(t) : 0.0f;
@@ -1171,7 +1203,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            s[u][i] = __builtin_fmaf(s[u][i], f, -below) < kSmall ? kNone : s[u][i];
+            s[u][i] = __builtin_fmaf(s[u][i], f, -less) < kSmall ? kNone : s[u][i];
       }
       // Output, in a fixed order too: V fragments kAhead products ahead, and the
       // probabilities of the next 16 keys between the products of these.
@@ -1181,7 +1213,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         auto fetch = [&](int n) { vf[n % (kAhead + 1)] = values_of(n / DB, n % DB); };
         auto probability = [&](int g, int j) {
           const int u = g >> 1, i = 8 * (g & 1) + j;
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], factor, -sub));
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], by, -below));
           l_run += w;
           weight(u, i, w);
         };

@@ -67,3 +67,73 @@ def test_other_global_scales(dtype, queries):
     sees = torch.cat([torch.arange(c - queries, c) >= 0 for c in contexts]).cuda()
     assert torch.isnan(got[sees]).all() and torch.isnan(lse[sees]).all()
     assert not got[~sees].any() and (lse[~sees] == float("-inf")).all() and not sees.all()
+
+
+def _attend(cache, table, contexts, counts, q, scale, causal, window):
+    starts = [0]
+    for n in counts:
+        starts.append(starts[-1] + n)
+    lens = torch.tensor(contexts, dtype=torch.int32, device="cuda")
+    got, lse = nv.nvfp4_kv_attention(q, cache, table.cuda(), lens, scale=scale, causal=causal, window=window,
+                                     query_starts=torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                                     max_queries=max(counts), max_context=max(contexts), return_lse=True)
+    torch.cuda.synchronize()
+    return got, lse, starts
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("queries", ROWS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("sign", [0, -1])
+def test_large_scores(dtype, queries, dim, sign):
+    """Scores of 2^16 and far more, of both signs or all negative.  A score's error e (as in _kv.py) is then
+    above 1, so that keys whose scores lie within 2 e of the largest may share the output in any way: it lies
+    between the least and the greatest of their values, up to the roundings of weights and output.  Keys 40
+    below those weigh nothing.  Mostly one key is left, and the output is its value."""
+    contexts, counts, page, groups, inf = [600, 130, queries], [queries] * 3, 16, 2, float("inf")
+    table, pages, _ = _batch(contexts, page, 5)
+    cache = _kv.random_cache(pages, page, 1, dim, 2200 + dim)
+    if sign:
+        cache.k_codes &= 0x77
+    held = {n: getattr(cache, n).cpu()[:, 0] for n in ("k_codes", "k_scales", "v_codes", "v_scales")}
+    unit = _kv.UNIT[dtype]
+    single_float = dtype is torch.float32
+    base = torch.randn(sum(counts), groups, dim, generator=torch.Generator().manual_seed(2201 + dim))
+    if sign:
+        base = -base.abs()
+    alone = 0
+    for size in (3e4, 1e7, 1e9, 1e30):
+        by = min(size, 2e3) if dtype is torch.float16 else size  # (beyond float16: the scale makes up for it)
+        q = (base * by).to(dtype)
+        scale = dim ** -0.5 * (size / by)
+        for causal, window in MASKS:
+            what = (dtype, dim, sign, size, causal, window)
+            got, lse, starts = _attend(cache, table, contexts, counts, q.cuda(), scale, causal, window)
+            assert torch.isfinite(got).all() and torch.isfinite(lse).all(), what
+            for b, context in enumerate(contexts):
+                j = torch.arange(context)
+                at, off = table[b].long()[j // page], j % page
+                k = _kv.values(held["k_codes"][at, off], held["k_scales"][at, off], 20.0)
+                v = _kv.values(held["v_codes"][at, off], held["v_scales"][at, off], 6.0)
+                x = q[starts[b]:starts[b + 1]].double()  # [queries, groups, dim]
+                pos = torch.arange(context - queries, context).view(-1, 1, 1)
+                hidden = (j > pos) if causal else torch.zeros(queries, 1, context, dtype=torch.bool)
+                if window:
+                    hidden = hidden | (j <= pos - window)
+                s = (x @ k.t() * scale).masked_fill(hidden, -inf)
+                most = (x.abs() @ k.abs().t() * scale).masked_fill(hidden, 0.0).amax(-1)
+                e = ((dim + 8) * 2.0 ** -24 + (2.0 ** -22 if single_float else 0.0)) * most
+                want = torch.logsumexp(s, -1)
+                here = slice(starts[b], starts[b + 1])
+                assert ((lse[here].cpu().double() - want).abs() <=
+                        e + 2.0 ** -20 + context * 2.0 ** -24 + 2.0 ** -22 * want.abs()).all(), what
+                near = (s >= (s.amax(-1) - 2 * e - 40).unsqueeze(-1)).unsqueeze(-1)  # [queries, groups, keys, 1]
+                alone += int((near.sum(2) == 1).sum())
+                low = torch.where(near, v, torch.full_like(v, inf)).amin(2)
+                high = torch.where(near, v, torch.full_like(v, -inf)).amax(2)
+                slack = ((2.0 ** -22 if single_float else 2.0 ** -11) + unit + 2.0 ** -18) * (1 + 2 * unit) * \
+                    torch.maximum(low.abs(), high.abs()) + 1e-12
+                o = got[here].cpu().double()
+                assert ((o >= low - slack) & (o <= high + slack)).all(), what
+    say(f"large scores {dtype} d{dim} queries {queries} sign {sign}: {alone} rows of one key")
+    assert alone > 0
