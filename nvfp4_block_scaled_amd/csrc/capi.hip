@@ -1278,7 +1278,7 @@ static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, 
   a->group_div = nvfp4::kv_make_div((uint32_t)a->groups);
   a->max_queries = (int)(max_queries < tokens ? max_queries : tokens);
   a->max_keys = (int)max_context;
-  a->window = (int)(window > INT32_MAX ? 0 : window);
+  a->window = (int)(window >= max_context ? 0 : window);  // positions stay below max_context: it hides nothing
   a->tokens = tokens;
   return NVFP4_OK;
 }

@@ -62,6 +62,11 @@ constexpr int kBands = 3;  // outputs stay below 2^45 2^58
 
 // ----------------------------------------------------------------- ranges
 
+// The first key that the query at position `pos` (below 0: before the context) may see.
+__device__ __forceinline__ int kv_window_begin(const KvAttention& a, int pos) {
+  return a.causal && a.window > 0 ? max(0, max(pos, 0) - a.window + 1) : 0;  // (without overflow for any window)
+}
+
 // The rows [row0, row0 + rows) of a sequence and the keys [lo, hi) that any of them may see.
 struct KvRange {
   int first, n, context;  // first token and number of queries, context length
@@ -74,13 +79,13 @@ __device__ __forceinline__ KvRange kv_range(const KvAttention& a, int b, int row
   // what lies outside the sizes that the caller gave is not touched
   r.first = max(0, min(r.first, (int)a.tokens));
   r.n = max(0, min(min(r.n, a.max_queries), (int)a.tokens - r.first));
-  r.context = a.context_lens[b];
+  r.context = max(0, a.context_lens[b]);
   r.lo = 0;
   r.hi = min(r.context, a.max_keys);
   if (a.causal) {
     const int q0 = kv_div(row0, a.group_div), q1 = min((int)kv_div(row0 + rows - 1, a.group_div), r.n - 1);
     r.hi = min(r.hi, r.context - r.n + q1 + 1);
-    if (a.window > 0) r.lo = max(0, r.context - r.n + q0 - a.window + 1);
+    r.lo = kv_window_begin(a, r.context - r.n + q0);
   }
   return r;
 }
@@ -610,13 +615,13 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     const int r = 16 * m + col;
     const int pos = rg.context - rg.n + (int)kv_div(r, a.group_div);
     see_hi[m] = r >= rows ? 0 : a.causal ? min(rg.hi, pos + 1) : rg.hi;
-    see_lo[m] = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    see_lo[m] = kv_window_begin(a, pos);
   }
   // keys that every row sees: [all_lo, all_hi)
   int all_hi = rg.hi, all_lo = 0;
   if (a.causal) {
     all_hi = min(rg.hi, rg.context - rg.n + 1);
-    if (a.window > 0) all_lo = max(0, rg.context - a.window);
+    all_lo = kv_window_begin(a, rg.context - 1);
   }
 
   f32x4 acc[MT][DB];
@@ -1001,13 +1006,13 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   }
   const int pos = rg.context - rg.n + qi;
   const int see_hi = !row_live ? 0 : a.causal ? min(end, pos + 1) : end;
-  const int see_lo = a.causal && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  const int see_lo = kv_window_begin(a, pos);
   // keys that every row of this wave sees
   int all_lo = 0, all_hi = end;
   if (a.causal) {
     const int w0 = min(row0 + 32 * wave, rows - 1), base = rg.context - rg.n;
     all_hi = min(end, base + (int)kv_div(w0, a.group_div) + 1);
-    if (a.window > 0) all_lo = max(0, base + (int)kv_div(min(w0 + 31, rows - 1), a.group_div) - a.window + 1);
+    all_lo = kv_window_begin(a, base + (int)kv_div(min(w0 + 31, rows - 1), a.group_div));
   }
 
   f32x16 acc[DB];

@@ -137,3 +137,20 @@ def test_large_scores(dtype, queries, dim, sign):
                 assert ((o >= low - slack) & (o <= high + slack)).all(), what
     say(f"large scores {dtype} d{dim} queries {queries} sign {sign}: {alone} rows of one key")
     assert alone > 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 31 + 5, 2 ** 40])
+@pytest.mark.parametrize("queries", [4, 45])
+def test_huge_windows(dtype, window, queries):
+    """Windows that hide nothing, also for queries that stand before the context."""
+    say(f"window {window} {dtype} queries {queries}")
+    _run([1, 3, 200, 0, 60], [queries] * 5, 1, 2, 64, 16, dtype, 2400, window=window)
+    _run([1, 3, 200, 0, 60], [queries] * 5, 1, 2, 64, 16, dtype, 2401, window=window)
+
+
+@pytest.mark.parametrize("queries", [4, 45])
+def test_windows_around_the_longest_context(queries):
+    """A window as long as max_context is none; one key less hides the first key from the last query."""
+    for window in (198, 199, 200, 201):
+        _run([200, 199, 3, 60], [queries] * 4, 1, 2, 64, 16, torch.bfloat16, 2402, window=window)
