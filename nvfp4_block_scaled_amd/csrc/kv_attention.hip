@@ -30,6 +30,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNone = -__builtin_huge_valf();
+constexpr float kNaN = __builtin_nanf("");
 
 // A tile's scores move its running maximum only when one exceeds it by more
 // than 2^kLag, so that tiles whose maximum hardly grows skip the rescaling of
@@ -198,6 +199,25 @@ __device__ __forceinline__ _Float16 kv_scale_of(const KvGroups<NG, EXACT>& r, in
   if constexpr (!EXACT) return kv_scale2(r.s[g]).x;
   const f16x2 two = kv_scale2(g < 2 ? r.s[0] : r.s[0] >> 16);
   return g & 1 ? two.y : two.x;
+}
+// Which groups' block scales are no numbers (bit 8 g + 7 of a joint one), and
+// the scales without them.
+template <int NG, bool EXACT>
+__device__ __forceinline__ uint32_t kv_no_numbers(const KvGroups<NG, EXACT>& r) {
+  if constexpr (EXACT) return ((r.s[0] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  uint32_t bad = 0u;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) bad |= (((r.s[g] & 0x7Fu) + 1u) & 0x80u) << (8 * g);
+  return bad;
+}
+template <int NG, bool EXACT>
+__device__ __forceinline__ void kv_drop(KvGroups<NG, EXACT>& r, uint32_t bad) {
+  if constexpr (EXACT) {
+    r.s[0] &= ~((bad >> 7) * 0xFFu);
+  } else {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) r.s[g] = bad >> (8 * g + 7) & 1u ? 0u : r.s[g];
+  }
 }
 // Dwords 2g, 2g + 1 (group g) as 16 float16.
 template <int NG, bool EXACT>
@@ -677,6 +697,37 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[m][i] = s[m][i >> 2][i & 3] * factor[m];
+      if (masked && m == 0 && rg.n > 1) {
+        // A value that is no number must not reach the rows that do not see
+        // its key (0 times it is NaN).  Those that do get their NaN here, and
+        // the tile is left without it.  (The heads of one query see the same keys.)
+        uint8_t* const held = mine + opaque(col) * RB + 32 * NG * opaque(quarter);  // this lane's groups
+        bool any = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const _Float16 v = *reinterpret_cast<const _Float16*>(held + 16 * u * RB + 32 * g);
+            any |= v != v;
+          }
+        if (__any(any)) {
+#pragma unroll 1
+          for (int i = 0; i < 2 * NG; ++i) {
+            const int u = i / NG, g = i - u * NG;
+            f16x8* at = reinterpret_cast<f16x8*>(held + 16 * u * RB + 32 * g);
+            const bool own = at[0][0] != at[0][0];
+            for (uint64_t lanes = __ballot(own); lanes; lanes &= lanes - 1) {
+              const int l = __builtin_ctzll(lanes), key = tile + 16 * u + (l & 15), group = NG * (l >> 4) + g;
+#pragma unroll
+              for (int mm = 0; mm < MT; ++mm)
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                  if (d == group && key >= see_lo[mm] && key < see_hi[mm]) acc[mm][d] = f32x4{kNaN, kNaN, kNaN, kNaN};
+            }
+            if (own) at[0] = at[1] = f16x8{0, 0, 0, 0, 0, 0, 0, 0};
+          }
+        }
+      }
       if (masked) {
         const int h = 4 * opaque(quarter);
         const int lo = see_lo[m] - tile - h, hi = see_hi[m] - tile - h;
@@ -906,7 +957,10 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   constexpr int KROW = many_k_row(NG), VROW = many_v_row(NG), BUF = TILE * (KROW + VROW);
   constexpr bool BOTH = TILE == 64;  // every thread decodes keys and values; else half of them each
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ uint64_t exists[2][4];  // four lanes a key: which keys of a buffer exist
+  // four lanes a key: which keys of a buffer exist, with values that are
+  // numbers; where some do not, also which exist and which have other values
+  __shared__ uint64_t fine[2][4], exists[2][4], odd[2][4];
+  __shared__ uint32_t odd_groups[2][256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 31, half = lane >> 5;
   const int b = blockIdx.y;
@@ -965,9 +1019,23 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
     uint8_t* at = lds + buf * BUF + (of_v ? TILE * KROW + key_of * VROW : key_of * KROW) + 32 * g0 + 16 * w;
     *reinterpret_cast<f16x8*>(at) = kv_decode8(x.w[w], kv_scale_of(x, w >> 1));
   };
+  // A value that is no number must not reach the rows that do not see its key
+  // (0 times it is NaN): it is decoded as 0, and the rows that do get their
+  // NaN from these notes.
   auto store_flags = [&](int buf) {
-    const uint64_t bits = __ballot(live != 0);
-    if (lane == 0) exists[buf][wave] = bits;
+    const uint32_t bad = BOTH ? kv_no_numbers(vt) : second ? kv_no_numbers(kt) : 0u;
+    const uint64_t bits = __ballot((live != 0) & (bad == 0u));
+    if (lane == 0) fine[buf][wave] = bits;
+    if (~bits) {
+      const uint64_t there = __ballot(live != 0), others = __ballot(bad != 0u);
+      if (lane == 0) {
+        exists[buf][wave] = there;
+        odd[buf][wave] = others;
+      }
+      odd_groups[buf][opaque((int)threadIdx.x)] = bad;
+      if constexpr (BOTH) kv_drop(vt, bad);
+      else kv_drop(kt, bad);
+    }
   };
   int page = 0, page2 = 0;
   if (begin < end) {
@@ -1048,8 +1116,8 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
     uint64_t have = ~0ull;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) have &= exists[buf][i];
-    store_flags(buf ^ 1);
+    for (int i = 0; i < 4; ++i) have &= fine[buf][i];
+    if (!BOTH) store_flags(buf ^ 1);
     // largest and smallest scores, in four chains; those of the first 32 keys
     // while the others' products run
     float top4[4], low4[4];
@@ -1074,6 +1142,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 #pragma unroll
         for (int e = SPLIT - 1; e >= 0; --e)
           s[n / STEPS] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[n % (kAhead + 1)], q[e][n % STEPS], s[n / STEPS], 0, 0, 0);
+        if (BOTH && n * PIECES / N == 2 * NG - 1 && (n + 1) * PIECES / N == 2 * NG) store_flags(buf ^ 1);  // ahead of values
         // (after the last tile: what is decoded then is not read)
         if (n * PIECES / N != (n + 1) * PIECES / N) store_piece(buf ^ 1, n * PIECES / N);
         if (SUB == 2 && n >= STEPS + 2 && n < STEPS + 4) {
@@ -1099,14 +1168,33 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
             s[u][i] = ((key >= lo) & (key < hi)) ? s[u][i] : kNone;
           }
       }
-      if (holes) {  // pages that are not there
+      if (holes) {  // pages that are not there, values that are no numbers
         const int h = opaque(half);
+        const int lo = opaque(see_lo), hi = opaque(see_hi);
+        uint64_t there[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const bool noted = fine[buf][w] != ~0ull;
+          there[w] = noted ? exists[buf][w] : ~0ull;
+          for (uint64_t lanes = noted ? odd[buf][w] : 0ull; lanes; lanes &= lanes - 1) {
+            const int thread = 64 * w + __builtin_ctzll(lanes), key = tile + ((BOTH ? thread : thread & 127) >> 2);
+            const uint32_t groups = odd_groups[buf][thread];
+            if (key >= lo && key < hi)
+#pragma unroll
+              for (int i = 0; i < 2 * DB; ++i) {
+                const int g = i - NG * (thread & 3);
+                if (g >= 0 && g < NG && (groups >> (8 * g + 7) & 1u))
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) acc[i >> 1][8 * (i & 1) + j] = kNaN;
+              }
+          }
+        }
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int key = 8 * (i >> 2) + 4 * h + (i & 3);  // of this half tile
-            if (!(exists[buf][2 * u + (i >> 3)] >> (4 * (key & 15)) & 1)) s[u][i] = kNone;
+            if (!(there[2 * u + (i >> 3)] >> (4 * (key & 15)) & 1)) s[u][i] = kNone;
           }
       }
       if (SUB == 1 || edge || holes) {

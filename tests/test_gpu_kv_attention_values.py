@@ -154,3 +154,54 @@ def test_windows_around_the_longest_context(queries):
     """A window as long as max_context is none; one key less hides the first key from the last query."""
     for window in (198, 199, 200, 201):
         _run([200, 199, 3, 60], [queries] * 4, 1, 2, 64, 16, torch.bfloat16, 2402, window=window)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [16, 64, 96, 128, 192, 256])
+@pytest.mark.parametrize("queries", [4, 13, 45])
+@pytest.mark.parametrize("causal,window", MASKS)
+def test_values_not_a_number(dtype, dim, queries, causal, window):
+    """A held value whose block scale is no number makes NaN of its 16 elements for the queries that see its key,
+    and changes no bit of anything else: hidden keys, ends of tiles, a page that is not there beside it, split
+    contexts."""
+    say(f"values that are no number {dtype} d{dim} queries {queries} causal {causal} window {window}")
+    contexts, counts, page, groups = [130, 64, 3000, queries], [queries] * 4, 16, 2
+    table, pages, _ = _batch(contexts, page, 7)
+    table[0, 6] = -1
+    cache = _kv.random_cache(pages, page, 1, dim, 2500 + dim)
+    q = torch.randn(sum(counts), groups, dim, generator=torch.Generator().manual_seed(2501)).to(dtype).cuda()
+    want, want_lse, starts = _attend(cache, table, contexts, counts, q, dim ** -0.5, causal, window)
+    places = [(0, 129, 0), (0, 127, dim // 16 - 1), (0, 95, 0), (0, 112, 0), (1, 63, 0), (1, 62, dim // 32),
+              (1, 64 - queries, 0), (2, 2999, dim // 16 - 1), (2, 2960, 0), (2, 5, 0), (3, queries - 1, 0), (3, 1, 0)]
+    for b, j, group in places:
+        cache.v_scales[int(table[b, j // page]), 0, j % page, group] = 0x7F if j % 2 else 0xFF
+        for i in range(queries):
+            pos = contexts[b] - queries + i
+            if not causal or (j <= pos and (not window or j > pos - window)):
+                want[starts[b] + i, :, 16 * group:16 * group + 16] = float("nan")
+    got, lse, _ = _attend(cache, table, contexts, counts, q, dim ** -0.5, causal, window)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0)) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("queries", [4, 13, 45])
+@pytest.mark.parametrize("window", [0, 37])
+def test_keys_not_a_number(dtype, queries, window):
+    """A held key that is no number makes NaN of the queries that see it; the others keep within their bound."""
+    contexts, counts, page, dim = [130, 64, queries], [queries] * 3, 16, 128
+    table, pages, _ = _batch(contexts, page, 7)
+    cache = _kv.random_cache(pages, page, 1, dim, 2600)
+    q = torch.randn(sum(counts), 2, dim, generator=torch.Generator().manual_seed(2601)).to(dtype).cuda()
+    lens, starts = torch.tensor(contexts, dtype=torch.int32), [0, queries, 2 * queries, 3 * queries]
+    out, ref_lse, bound, lse_bound = _kv.reference(q, cache, table, lens, starts, dim ** -0.5, True, window)
+    for b, j in ((0, 128), (1, 63), (2, queries - 2)):
+        cache.k_scales[int(table[b, j // page]), 0, j % page, 3] = 0x7F
+    got, lse, _ = _attend(cache, table, contexts, counts, q, dim ** -0.5, True, window)
+    bad = torch.zeros(3 * queries, dtype=torch.bool)
+    for b, j in ((0, 128), (1, 63), (2, queries - 2)):
+        pos = torch.arange(contexts[b] - queries, contexts[b])
+        bad[starts[b]:starts[b + 1]] = (j <= pos) & (j > pos - window if window else True)
+    assert torch.isnan(got[bad.cuda()]).all() and torch.isnan(lse[bad.cuda()]).all() and 0 < bad.sum() < 3 * queries
+    off, off_lse = (got.cpu().double() - out).abs(), (lse.cpu().double() - ref_lse).abs()
+    assert (off[~bad] <= bound[~bad]).all() and (off_lse[~bad] <= lse_bound[~bad]).all()
