@@ -43,12 +43,13 @@ constexpr float kNaN = __builtin_nanf("");
 // Small weights.  Below 2^-14 a float16 loses bits, and in a 4-bit cache an
 // output may consist of small weights alone (the keys with large weights
 // hold an exact 0 there).  So weights below 2^kSmall, 2^-29 of the largest,
-// enter the product apart, in bands of 2^kShift with the output scaled along,
-// and so keep their bits.  Tiles without such weights, nearly all unless a
-// row's scores spread over more than 20 nats, skip this.  Measured with
-// scores of 1.8 nats deviation, 5 x up to 1023 queries over up to 9001 keys:
-// 441 us without any such handling, 468 with it; with kLag 3 and kBias 12, a
-// window of 2^26, 550.
+// enter products of their own, in bands of 2^kShift, with the output or their
+// sums scaled along, and so keep their bits down to 2^-145 of the largest.
+// Tiles without such weights, nearly all unless a row's scores spread over more
+// than 20 nats, skip this.  Measured with scores of 1.8 nats deviation, 5 x up
+// to 1023 queries over up to 9001 keys: 441 us without any such handling, 468
+// with it; with kLag 3 and kBias 12, a window of 2^26, 550; with all bands'
+// sums apart, which needs no scaled output, 474 against 443.
 //
 // Large scores.  A weight's exponent is score - sub with sub = maximum - kBias
 // rounded.  Beyond kBig that rounding, and that of scores which are products
@@ -59,7 +60,7 @@ constexpr float kBig = 0x1p18f, kMost = 15.99f;
 constexpr float kSmall = -14.0f, kShift = 29.0f;
 constexpr float kUp = 0x1p29f, kDown = 0x1p-29f;
 constexpr float kRest = 0x1p11f;
-constexpr int kBands = 3;  // outputs stay below 2^45 2^58
+constexpr int kBands = 5, kNearBands = 3;  // outputs stay below 2^45, in near bands 2^45 2^58
 
 // ----------------------------------------------------------------- ranges
 
@@ -770,20 +771,12 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       p[m][0][i] = (_Float16)w;
       if constexpr (SPLIT == 2) p[m][SPLIT - 1][i] = (_Float16)((w - (float)(_Float16)w) * kRest);
     };
-    auto multiply = [&]() {
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const uint8_t* at = mine + (4 * quarter + (col >> 2)) * RB + 32 * d + 8 * (col & 3);
-        const f16x8 vf = kv_read_transposed(at, at + 16 * RB);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int e = SPLIT - 1; e >= 0; --e)
-            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e ? kv_rest_values(vf) : vf, p[m][e], acc[m][d], 0, 0, 0);
-      }
+    auto values_of = [&](int d) {
+      const uint8_t* at = mine + (4 * quarter + (col >> 2)) * RB + 32 * d + 8 * (col & 3);
+      return kv_read_transposed(at, at + 16 * RB);
     };
     if (__any(low < kSmall)) {  // the bands of small weights, then the rest
-      float shift = kShift, up = kUp, down = kDown;
+      float shift = kShift, down = kDown;
       bool any = false;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -804,20 +797,20 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
             weight(m, i, w);
           }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int d = 0; d < DB; ++d) {
+          const f16x8 vf = values_of(d);
 #pragma unroll
-          for (int d = 0; d < DB; ++d)
+          for (int m = 0; m < MT; ++m) {
+            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][d][i] *= up;
-        multiply();
+            for (int e = SPLIT - 1; e >= 0; --e)
+              sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(e ? kv_rest_values(vf) : vf, p[m][e], sum, 0, 0, 0);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][d][i] *= down;
+            for (int i = 0; i < 4; ++i) acc[m][d][i] += sum[i] * down;
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
         shift += kShift;
-        up *= kUp;
         down *= kDown;
       }
 #pragma unroll
@@ -833,7 +826,15 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
         l_run[m] += w;
         weight(m, i, w);
       }
-    multiply();
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      const f16x8 vf = values_of(d);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = SPLIT - 1; e >= 0; --e)
+          acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e ? kv_rest_values(vf) : vf, p[m][e], acc[m][d], 0, 0, 0);
+    }
   }
   from = to;
   if (from < end) {
@@ -955,6 +956,7 @@ __global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1))
 kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   constexpr int DP = 64 * NG, TILE = many_tile(NG), SUB = TILE / 32, STEPS = DP / 16, DB = DP / 32;
   constexpr int KROW = many_k_row(NG), VROW = many_v_row(NG), BUF = TILE * (KROW + VROW);
+  constexpr int NEAR = NG * SPLIT <= 4 ? kNearBands : 1;  // (more registers would be spilled)
   constexpr bool BOTH = TILE == 64;  // every thread decodes keys and values; else half of them each
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // four lanes a key: which keys of a buffer exist, with values that are
@@ -1258,14 +1260,15 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
             const float t = __builtin_fmaf(s[u][i], f, -less);
             any |= (t < kSmall) & (t > kNone);
           }
-        for (int band = 1; band < kBands && __any(any); ++band) {
+        int band = 1;
+        for (; band < NEAR && __any(any); ++band) {  // the output scaled along: few instructions
           any = false;
 #pragma unroll
           for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float t = __builtin_fmaf(s[u][i], f, -less) + shift;
-              const bool lower = (t < kSmall) & (band < kBands - 1);
+              const bool lower = t < kSmall;
               const bool in = (t < kSmall + kShift) & !lower;
               const float w = in ? __builtin_amdgcn_exp2f(t) : 0.0f;
               l_run += w * down;
@@ -1290,6 +1293,39 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
             for (int i = 0; i < 16; ++i) acc[d][i] *= down;
           shift += kShift;
           up *= kUp;
+          down *= kDown;
+        }
+        for (; band < kBands && __any(any); ++band) {  // where that would pass float32: sums apart
+          any = false;
+#pragma unroll
+          for (int g = 0; g < 2 * SUB; ++g) {  // (16 keys at a time: few registers)
+            f16x8 w8[SPLIT];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float t = __builtin_fmaf(s[g >> 1][8 * (g & 1) + j], f, -less) + shift;
+              const bool lower = (t < kSmall) & (band < kBands - 1);
+              const bool in = (t < kSmall + kShift) & !lower;
+              const float w = in ? __builtin_amdgcn_exp2f(t) : 0.0f;
+              l_run += w * down;
+              any |= lower & (t > kNone);
+              w8[0][j] = (_Float16)w;
+              if constexpr (SPLIT == 2) w8[SPLIT - 1][j] = (_Float16)((w - (float)(_Float16)w) * kRest);
+            }
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              const f16x8 vf = values_of(g, d);
+              f32x16 sum;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+#pragma unroll
+              for (int e = SPLIT - 1; e >= 0; --e)
+                sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(e ? kv_rest_values(vf) : vf, w8[e], sum, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[d][i] += sum[i] * down;
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          shift += kShift;
           down *= kDown;
         }
 #pragma unroll

@@ -205,3 +205,32 @@ def test_keys_not_a_number(dtype, queries, window):
     assert torch.isnan(got[bad.cuda()]).all() and torch.isnan(lse[bad.cuda()]).all() and 0 < bad.sum() < 3 * queries
     off, off_lse = (got.cpu().double() - out).abs(), (lse.cpu().double() - ref_lse).abs()
     assert (off[~bad] <= bound[~bad]).all() and (off_lse[~bad] <= lse_bound[~bad]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [16, 64, 128, 192, 256])
+@pytest.mark.parametrize("queries", [1, 13, 45])
+@pytest.mark.parametrize("size", [3.0, 8.0, 14.0])
+def test_small_weights(dtype, dim, queries, size):
+    """Each output element takes its value from keys of one score alone, down to 84 below the largest (a weight of
+    2^-121): its own bits are kept, whatever the largest weight."""
+    say(f"small weights {dtype} d{dim} queries {queries} size {size}")
+    contexts, page = [200, 77], 16
+    table, pages, _ = _batch(contexts, page, 9)
+    cache = _kv.random_cache(pages, page, 1, dim, 2700, None, None)
+    level = torch.arange(page) % 8  # the code, and the element that its keys' values have
+    k = torch.zeros(pages, 1, page, dim // 2, dtype=torch.uint8)
+    k[:, 0, :, 0] = level.to(torch.uint8)
+    v = torch.zeros(pages, 1, page, dim, dtype=torch.uint8)
+    v[:, 0, torch.arange(page), level] = torch.randint(1, 8, (pages, page), generator=torch.Generator().manual_seed(2701),
+                                                       dtype=torch.uint8)
+    cache.k_codes.copy_(k)
+    cache.v_codes.copy_(v[..., 0::2] | v[..., 1::2] << 4)
+    cache.k_scales.fill_(0x38)
+    cache.v_scales.fill_(0x38)
+    q = torch.zeros(2 * queries, 2, dim)
+    q[:, 0, 0], q[:, 1, 0] = -size, size  # the first heads prefer keys of 0, the second those of 6
+    q = q.to(dtype).cuda()
+    got, lse, starts = _attend(cache, table, contexts, [queries] * 2, q, 1.0, True, 0)
+    lens = torch.tensor(contexts, dtype=torch.int32)
+    _kv.check(got, lse, _kv.reference(q, cache, table, lens, starts, 1.0), f"{dtype} d{dim} size {size}")
