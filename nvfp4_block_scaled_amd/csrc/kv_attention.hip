@@ -467,6 +467,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   constexpr int DP = 64 * NG, STEPS = 2 * NG, DB = DP / 16, RB = few_row_bytes(NG);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ float stat_m[kFewWaves][16 * MT], stat_l[kFewWaves][16 * MT];
+  __shared__ uint32_t no_numbers[2][16 * MT];  // per row, of this run and the next one: groups that are NaN
   uint64_t* page_of = reinterpret_cast<uint64_t*>(lds + kFewWaves * kFewTile * RB);  // of this run and of the next one
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, quarter = lane >> 4;
@@ -610,6 +611,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
     page_of[second ? kFewPages + i - now.pages : i] =
         second ? page_at(next, next.begin, i - now.pages) : page_at(now, now.begin, i);
   }
+  if (threadIdx.x < 32 * MT) (&no_numbers[0][0])[threadIdx.x] = 0u;
   lds_barrier();
   begin_span(now, now.begin);
 
@@ -700,8 +702,10 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       for (int i = 0; i < 8; ++i) x[m][i] = s[m][i >> 2][i & 3] * factor[m];
       if (masked && m == 0 && rg.n > 1) {
         // A value that is no number must not reach the rows that do not see
-        // its key (0 times it is NaN).  Those that do get their NaN here, and
-        // the tile is left without it.  (The heads of one query see the same keys.)
+        // its key (0 times it is NaN).  Those that do are noted for the end of
+        // the run, and the tile is left without it.  (The heads of one query see
+        // the same keys.)  NaN put into the sums here instead costs heads of 256
+        // with 17 to 32 rows their registers: 8 x up to 8000, 86 us against 53.
         uint8_t* const held = mine + opaque(col) * RB + 32 * NG * opaque(quarter);  // this lane's groups
         bool any = false;
 #pragma unroll
@@ -721,9 +725,8 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
               const int l = __builtin_ctzll(lanes), key = tile + 16 * u + (l & 15), group = NG * (l >> 4) + g;
 #pragma unroll
               for (int mm = 0; mm < MT; ++mm)
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-                  if (d == group && key >= see_lo[mm] && key < see_hi[mm]) acc[mm][d] = f32x4{kNaN, kNaN, kNaN, kNaN};
+                if (quarter == 0 && key >= see_lo[mm] && key < see_hi[mm])
+                  atomicOr(&no_numbers[buf][16 * mm + col], 1u << group);
             }
             if (own) at[0] = at[1] = f16x8{0, 0, 0, 0, 0, 0, 0, 0};
           }
@@ -885,6 +888,8 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += by * o[j];
       }
+      // (buf is the next run's already, if there is one)
+      if (rg.n > 1 && (no_numbers[more_runs ? buf ^ 1 : buf][r] >> (d >> 4) & 1u)) v[0] = v[1] = v[2] = v[3] = kNaN;
       const int qi = kv_div(r, a.group_div);
       const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + head * a.groups + (r - qi * a.groups);
       if (now.whole) {
@@ -913,6 +918,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
       for (int i = threadIdx.x; i < next.pages; i += 256) page_of[(buf ^ 1) * kFewPages + i] = page_at(next, next.begin, i);
   }
   lds_barrier();  // the sums have been read and the next page numbers are there
+  if (threadIdx.x < 16 * MT) no_numbers[buf ^ 1][threadIdx.x] = 0u;  // (for the run after this one)
   }
 }
 
