@@ -700,7 +700,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
  * tokens != seqs or max_queries != 1, window < 0 or window > 0 without
  * causal, scale not positive, max_context out of range, NULL or misaligned
  * pointers, workspace too small; UNSUPPORTED for sizes of 2^31 or more,
- * query_heads or seqs above 65535.
+ * max_context above 2^31 - 4096, query_heads or seqs above 65535.
  */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
                                          int64_t seqs, int64_t max_queries, int64_t max_context,

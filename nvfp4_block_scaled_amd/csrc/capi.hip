@@ -1269,7 +1269,7 @@ static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, 
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] query_heads (%lld) must be a multiple of heads (%d).", op,
                 (long long)query_heads, c.heads);
   if (window < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] window must be >= 0.", op);
-  if (query_heads > 65535 || seqs > 65535 || max_queries > INT32_MAX / query_heads || max_context > INT32_MAX ||
+  if (query_heads > 65535 || seqs > 65535 || max_queries > INT32_MAX / query_heads || max_context > nvfp4::kKvMaxKeys ||
       tokens > INT32_MAX / query_heads || seqs * c.heads > (((int64_t)1 << 30) / (max_context / 128 + 1)))
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large.", op);
   a->seqs = (int)seqs;

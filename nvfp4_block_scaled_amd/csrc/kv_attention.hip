@@ -69,6 +69,9 @@ __device__ __forceinline__ int kv_window_begin(const KvAttention& a, int pos) {
   return a.causal && a.window > 0 ? max(0, max(pos, 0) - a.window + 1) : 0;  // (without overflow for any window)
 }
 
+// Positions stay below kKvMaxKeys, some thousands below 2^31: a tile or a
+// chunk past the end of a context is still an int.
+//
 // The rows [row0, row0 + rows) of a sequence and the keys [lo, hi) that any of them may see.
 struct KvRange {
   int first, n, context;  // first token and number of queries, context length
@@ -81,7 +84,7 @@ __device__ __forceinline__ KvRange kv_range(const KvAttention& a, int b, int row
   // what lies outside the sizes that the caller gave is not touched
   r.first = max(0, min(r.first, (int)a.tokens));
   r.n = max(0, min(min(r.n, a.max_queries), (int)a.tokens - r.first));
-  r.context = max(0, a.context_lens[b]);
+  r.context = max(0, min(a.context_lens[b], kKvMaxKeys));
   r.lo = 0;
   r.hi = min(r.context, a.max_keys);
   if (a.causal) {
@@ -485,7 +488,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   // Keys whose page numbers are staged at a time.
   const int span = (int)min((int64_t)1 << 30, (int64_t)(kFewPages - 2) * c.page_size / kFewStep * kFewStep);
   auto pages_of = [&](int from, int end) {
-    return from < end ? (int)kv_div(min(end, from + span) - 1, c.page_div) - (int)kv_div(from, c.page_div) + 1 : 0;
+    return from < end ? (int)kv_div(from + min(end - from, span) - 1, c.page_div) - (int)kv_div(from, c.page_div) + 1 : 0;
   };
   KvScan scan;
   int unit = 0, last_unit = 0, base = 0, before = 0;
@@ -584,7 +587,7 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
   };
   // This wave's first tile of the keys from `from` on, whose page numbers are staged.
   auto begin_span = [&](const Run& r, int from) {
-    to = min(r.end, from + span);
+    to = from + min(r.end - from, span);
     staged = pages_of(from, r.end);
     const int first = from + wave * kFewTile;
     if (first < to) {
@@ -980,7 +983,8 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   const KvRange rg = kv_range(a, b, row0, kManyRows);
   const int rows = rg.n * a.groups;
   if (row0 >= rows) return;
-  const int begin = rg.lo + split * sp.chunk, end = min(rg.hi, begin + sp.chunk);
+  const int keys = max(0, rg.hi - rg.lo), before = min(keys, split * sp.chunk);
+  const int begin = rg.lo + before, end = begin + min(keys - before, sp.chunk);
   if (begin >= end && split > 0) return;  // the first chunk's workgroup answers for rows that see nothing
 
   // what this thread decodes: NG groups of one key (and of its value)
@@ -1498,7 +1502,7 @@ __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttentio
   const int r = qi * a.groups + qh % a.groups;  // its row among those of its kv head
   const KvRange rg = kv_range(a, blockIdx.y, r / kManyRows * kManyRows, kManyRows);
   if (qi >= rg.n) return;
-  const int parts = rg.hi > rg.lo ? (rg.hi - rg.lo + sp.chunk - 1) / sp.chunk : 1;
+  const int parts = rg.hi > rg.lo ? (rg.hi - rg.lo - 1) / sp.chunk + 1 : 1;
   const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + qh;
   kv_join<1>(c, a, dt, sp.sums, sp.stats, row * sp.splits, 1, parts, row);
 }

@@ -156,6 +156,7 @@ struct KvCache {
   KvDiv page_div;
 };
 constexpr int kKvMaxDim = 256;
+constexpr int kKvMaxKeys = INT32_MAX - 4095;  // of a context
 // tokens * dim / 8 < 2^31; strides in elements; 2 * heads <= 65535
 hipError_t launch_kv_write(const KvCache& c, const void* k, const void* v, int dt, int64_t tokens,
                            int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
