@@ -753,11 +753,17 @@ def nvfp4_mx_qqmm_packed(x, w, out=None, workspace=None):
 
 # ------------------------------------------------------------------ key/value cache
 
+_KV_HELD = ("k_codes", "k_scales", "v_codes", "v_scales", "global_scale_k", "global_scale_v")
+
+
 class KVCache:
     """A paged key/value cache held in NVFP4: codes uint8 [pages, heads,
     page_size, dim/2] and scales uint8 [pages, heads, page_size, dim/16] for
     keys and for values, and the float32 device scalars of their global
-    scales (None: factor 1).  Slot = page * page_size + offset in the page."""
+    scales (None: factor 1).  Slot = page * page_size + offset in the page.
+    Any of these may be assigned anew and is checked like at the start; the
+    sizes follow from them.  A tensor's own memory must stay where it is
+    while the cache has it (no resize_ or set_)."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, global_scale_k=None, global_scale_v=None):
         codes, scales, device = k_codes.shape, k_scales.shape, k_codes.device
@@ -772,14 +778,26 @@ class KVCache:
                 and k_codes.is_contiguous() and k_scales.is_contiguous()
                 and v_codes.is_contiguous() and v_scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous uint8 tensors of one device")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.global_scale_k, self.global_scale_v = global_scale_k, global_scale_v
-        self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, 2 * half, device
-        self._struct = _KVCacheStruct(
+        struct = _KVCacheStruct(
             k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
             None if global_scale_k is None else _kv_scalar(global_scale_k, "global_scale_k", device),
             None if global_scale_v is None else _kv_scalar(global_scale_v, "global_scale_v", device),
-            pages, page_size, heads, self.dim)
+            pages, page_size, heads, 2 * half)
+        self.__dict__.update(
+            k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, global_scale_k=global_scale_k,
+            global_scale_v=global_scale_v, pages=pages, heads=heads, page_size=page_size, dim=2 * half, device=device,
+            _struct=struct)
+
+    def __setattr__(self, name, value):
+        if name in _KV_HELD:  # the struct that calls get holds pointers: made anew
+            KVCache.__init__(self, **{**{n: self.__dict__[n] for n in _KV_HELD}, name: value})
+        elif name in self.__dict__:
+            raise AttributeError(f"a KVCache's {name} follows from its codes and cannot be assigned")
+        else:
+            super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a KVCache's {name} cannot be deleted")
 
 
 def _kv_scalar(g, name, device):

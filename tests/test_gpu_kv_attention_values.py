@@ -234,3 +234,22 @@ def test_small_weights(dtype, dim, queries, size):
     got, lse, starts = _attend(cache, table, contexts, [queries] * 2, q, 1.0, True, 0)
     lens = torch.tensor(contexts, dtype=torch.int32)
     _kv.check(got, lse, _kv.reference(q, cache, table, lens, starts, 1.0), f"{dtype} d{dim} size {size}")
+
+
+def test_scales_and_codes_assigned_anew():
+    """A cache whose global scales and codes are assigned anew gives what a cache made of them gives."""
+    table, pages, _ = _batch([100], 16, 3)
+    a, b = (_kv.random_cache(pages, 16, 2, 64, seed, *g) for seed, g in ((1, (20.0, 6.0)), (2, (5.0, 30.0))))
+    slots = torch.arange(pages * 16, device="cuda")
+    q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+    lens = torch.tensor([100], dtype=torch.int32, device="cuda")
+
+    def results(c):
+        return [*nv.nvfp4_kv_read(c, slots, dtype=torch.float32), nv.nvfp4_kv_attention(q, c, table.cuda(), lens)]
+
+    old = results(a)
+    for n in ("global_scale_k", "global_scale_v", "k_codes", "k_scales", "v_codes", "v_scales"):
+        setattr(a, n, getattr(b, n))
+    new = results(a)
+    assert all(torch.equal(x, y) for x, y in zip(new, results(b)))
+    assert not any(torch.equal(x, y) for x, y in zip(new, old))
