@@ -643,8 +643,9 @@ typedef struct nvfp4_kv_cache {
  *           [0, pages * page_size) is skipped (padding).  Two tokens with the
  *           same slot leave it undefined.
  * Errors: bad dtype or cache, tokens < 0, negative stride, NULL pointer, k
- * or v not aligned to its element; UNSUPPORTED for tokens * dim / 8 >= 2^31
- * or tokens * heads * dim >= 2^36.
+ * or v not aligned to its element; UNSUPPORTED for tokens * dim / 8 above
+ * 2^31 - 4097 and for (tokens * dim / 4096 + 1) * heads >= 2^23 (quotients
+ * rounded down; about tokens * heads * dim >= 2^35).
  */
 nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
                             int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
@@ -700,7 +701,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
  * tokens != seqs or max_queries != 1, window < 0 or window > 0 without
  * causal, scale not positive, max_context out of range, NULL or misaligned
  * pointers, workspace too small; UNSUPPORTED for sizes of 2^31 or more,
- * max_context above 2^31 - 4096, query_heads or seqs above 65535.
+ * max_context above 2^31 - 4096, query_heads or seqs above 65535, seqs *
+ * heads * (max_context / 128 + 1) above 2^30, max_queries * query_heads / 128
+ * (rounded up per kv head) of 2^24 or more.
  */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
                                          int64_t seqs, int64_t max_queries, int64_t max_context,

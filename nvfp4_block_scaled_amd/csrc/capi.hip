@@ -1212,12 +1212,20 @@ static nvfp4_status check_kv(const char* op, const nvfp4_kv_cache* cache, nvfp4_
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] a page's codes must stay below 4 GiB.", op);
   if (tokens < 0)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tokens (%lld) must be >= 0.", op, (long long)tokens);
-  if (tokens > INT32_MAX || tokens * (cache->dim / 8) > INT32_MAX - 4096 ||
-      (tokens * (cache->dim / 8) / 512 + 1) * 2 * cache->heads >= 1 << 24)
-    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large (tokens * dim / 8 of 2^31 or more).", op);
   *c = nvfp4::KvCache{cache->k_codes,        cache->k_scales,       cache->v_codes,     cache->v_scales,
                       cache->global_scale_k, cache->global_scale_v, (int)cache->pages,  (int)cache->page_size,
                       (int)cache->heads,     (int)cache->dim,       nvfp4::kv_make_div((uint32_t)cache->page_size)};
+  return NVFP4_OK;
+}
+
+// What a write or read can launch: an int counts the half groups of a head, and
+// its grid is of fewer than 2^24 workgroups of 256.
+static nvfp4_status check_kv_tokens(const char* op, const nvfp4::KvCache& c, int64_t tokens) {
+  if (tokens > INT32_MAX || tokens * (c.dim / 8) > INT32_MAX - 4096)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large (tokens * dim / 8 above 2^31 - 4097).", op);
+  if ((tokens * (c.dim / 8) / 512 + 1) * 2 * c.heads >= 1 << 24)
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "[%s] Sizes too large ((tokens * dim / 4096 + 1) * heads of 2^23 or more).", op);
   return NVFP4_OK;
 }
 
@@ -1228,6 +1236,7 @@ nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const vo
   const char* op = "kv_write";
   nvfp4::KvCache c;
   if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
+  if (nvfp4_status st = check_kv_tokens(op, c, tokens)) return st;
   if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write] strides must be >= 0.");
   if (tokens > 0) {
@@ -1247,6 +1256,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
   const char* op = "kv_read";
   nvfp4::KvCache c;
   if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
+  if (nvfp4_status st = check_kv_tokens(op, c, tokens)) return st;
   if (tokens > 0) {
     if (!k || !v || !slots)
       return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_read] k, v and slots must not be NULL.");
@@ -1272,11 +1282,14 @@ static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, 
   if (query_heads > 65535 || seqs > 65535 || max_queries > INT32_MAX / query_heads || max_context > nvfp4::kKvMaxKeys ||
       tokens > INT32_MAX / query_heads || seqs * c.heads > (((int64_t)1 << 30) / (max_context / 128 + 1)))
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large.", op);
+  const int64_t most = max_queries < tokens ? max_queries : tokens;
+  if ((most * (query_heads / c.heads) + 127) / 128 * c.heads >= 1 << 24)  // workgroups of a sequence
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large (max_queries * query_heads / 128 of 2^24 or more).", op);
   a->seqs = (int)seqs;
   a->query_heads = (int)query_heads;
   a->groups = (int)(query_heads / c.heads);
   a->group_div = nvfp4::kv_make_div((uint32_t)a->groups);
-  a->max_queries = (int)(max_queries < tokens ? max_queries : tokens);
+  a->max_queries = (int)most;
   a->max_keys = (int)max_context;
   a->window = (int)(window >= max_context ? 0 : window);  // positions stay below max_context: it hides nothing
   a->tokens = tokens;

@@ -1519,8 +1519,9 @@ __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttentio
 //   4096 keys: 64 sequences 72 / 83, lengths up to that 58 / 63
 // Past 4096 keys one long context among short ones would keep all waiting.
 constexpr int kFewAlone = 1024, kFewAloneMost = 4096;
+// (A launch has fewer than 2^24 workgroups.)
 constexpr int64_t few_alone(int64_t pairs) {
-  return pairs >= (kFewAloneMost - kFewAlone) / 6 ? kFewAloneMost : kFewAlone + 6 * pairs;
+  return pairs >= 1 << 24 ? -1 : pairs >= (kFewAloneMost - kFewAlone) / 6 ? kFewAloneMost : kFewAlone + 6 * pairs;
 }
 
 struct KvPlan {

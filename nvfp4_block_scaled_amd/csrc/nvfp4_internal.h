@@ -157,7 +157,7 @@ struct KvCache {
 };
 constexpr int kKvMaxDim = 256;
 constexpr int kKvMaxKeys = INT32_MAX - 4095;  // of a context
-// tokens * dim / 8 < 2^31; strides in elements; 2 * heads <= 65535
+// tokens * dim / 8 < 2^31 - 4096; strides in elements; fewer than 2^24 workgroups (check_kv_tokens)
 hipError_t launch_kv_write(const KvCache& c, const void* k, const void* v, int dt, int64_t tokens,
                            int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
                            const int64_t* slots, hipStream_t s);

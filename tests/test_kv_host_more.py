@@ -51,3 +51,69 @@ def test_cache_attributes_refused():
     assert all(getattr(c, n) is t for n, t in before.items())
     _points_at(c)
     c.owner = "anything else may be kept on it"
+
+
+UNSUP = nv.NVFP4_ERR_UNSUPPORTED
+BF16 = 2
+A, B, C, D, E = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000  # fake aligned addresses
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(nv.LIB_PATH):
+        from nvfp4_block_scaled_amd import build
+        build.build()
+    lib = nv.load_library()
+    lib.nvfp4_debug_set_arch_override(b"gfx942")  # nothing reaches a device
+    yield lib
+    lib.nvfp4_debug_set_arch_override(None)
+
+
+def _struct(heads, dim, pages=10, page=16):
+    return nv._KVCacheStruct(A, B, C, D, None, None, pages, page, heads, dim)
+
+
+def _says(L, status, text):
+    assert status == UNSUP and text in L.nvfp4_last_error().decode(), L.nvfp4_last_error()
+
+
+@pytest.mark.parametrize("heads,dim", [(2, 128), (8, 128), (1, 16), (32767, 256), (5, 80), (64, 240)])
+def test_codec_limits(L, heads, dim):
+    """Writes and reads take the tokens that the header states, and no more."""
+    # (t dim / 4096 + 1) heads < 2^23, rounded down: t dim / 4096 <= (2^23 - 1) / heads - 1
+    most = min((2 ** 31 - 4097) // (dim // 8), (((2 ** 23 - 1) // heads) * 512 - 1) // (dim // 8))
+    c = _struct(heads, dim)
+    for tokens, text in ((most, "gfx950"), (most + 1, "too large")):
+        _says(L, L.nvfp4_kv_write(c, A, B, BF16, tokens, dim, dim, dim, dim, C, None), text)
+        _says(L, L.nvfp4_kv_read(c, A, tokens, B, C, BF16, None), text)
+
+
+def _attend(L, c, tokens, query_heads, seqs, max_queries, max_context, pages=8, window=0):
+    need = L.nvfp4_kv_attention_workspace_size(c, tokens, query_heads, seqs, max_queries, max_context, window)
+    return L.nvfp4_kv_attention(c, A, BF16, tokens, query_heads, 1, 1, B, seqs, pages, C, D, max_queries, max_context,
+                                0.1, 1, window, E, None, E, need, None)
+
+
+def test_attention_limits(L):
+    """Attention's limits are its own: not those of writes, and every launch fits a grid."""
+    _says(L, _attend(L, _struct(8, 128), 2 ** 26, 8, 4, 5, 100), "gfx950")  # more tokens than a write takes
+    _says(L, _attend(L, _struct(8, 128), 2 ** 28, 8, 4, 5, 100), "too large")
+    one = _struct(1, 16)
+    _says(L, _attend(L, one, 2 ** 31 - 1, 1, 1, (2 ** 24 - 1) * 128, 100), "gfx950")
+    _says(L, _attend(L, one, 2 ** 31 - 1, 1, 1, (2 ** 24 - 1) * 128 + 1, 100), "too large")
+    far = _struct(1, 16, page=2 ** 22)
+    _says(L, _attend(L, far, 1, 1, 1, 1, 2 ** 31 - 4096, pages=512), "gfx950")
+    _says(L, _attend(L, far, 1, 1, 1, 1, 2 ** 31 - 4095, pages=512), "too large")
+
+
+def test_workspace_sizes(L):
+    """A long context is shared out and needs a workspace; one workgroup a pair needs none, and is no choice where
+    there are 2^24 pairs."""
+    size = L.nvfp4_kv_attention_workspace_size
+    need = size(_struct(2, 128, pages=1 << 16), 1, 8, 1, 1, 1 << 20, 0)
+    assert need > 0
+    many = _struct(16384, 16)
+    assert size(many, 1023, 16384, 1023, 1, 100, 0) == 0 and size(many, 1024, 16384, 1024, 1, 100, 0) > 0
+    for window in (1 << 20, 1 << 40):  # as good as none
+        assert size(_struct(2, 128, pages=1 << 16), 1, 8, 1, 1, 1 << 20, window) == need
