@@ -690,7 +690,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
  *                 aligned; rows of tokens outside every sequence are not written
  *   lse           device float [tokens, query_heads], natural logarithm, or NULL
  *   workspace     device, nvfp4_kv_attention_workspace_size() bytes (the same
- *                 arguments), 256-byte aligned; may be NULL when that is 0
+ *                 arguments, asked with the stream's device current: it goes
+ *                 by its compute units), 256-byte aligned; NULL when that is 0
  * The cached values are exact in the products (codes times block scales fit
  * float16; the global scales multiply scores and sums in float32); each
  * probability is rounded to float16 before its product with the values, for

@@ -786,7 +786,7 @@ class KVCache:
         self.__dict__.update(
             k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, global_scale_k=global_scale_k,
             global_scale_v=global_scale_v, pages=pages, heads=heads, page_size=page_size, dim=2 * half, device=device,
-            _struct=struct)
+            _gpu=device.index if device.type == "cuda" else None, _struct=struct)
 
     def __setattr__(self, name, value):
         if name in _KV_HELD:  # the struct that calls get holds pointers: made anew
@@ -817,11 +817,19 @@ def kv_cache(pages, page_size, heads, dim, global_scale_k=None, global_scale_v=N
     return KVCache(held(2), held(16), held(2), held(16), global_scale_k, global_scale_v)
 
 
+# the current stream of a device, as an integer, and the current device: torch.cuda's own functions take several
+# times as long, which shows in calls of 10 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _kv_stream(cache):
-    """The current stream of the cache's device, as an integer."""
-    if cache.device.type != "cuda":
+    """The current stream of the cache's device, as an integer; None when another device is the current one."""
+    index = cache._gpu
+    if index is None:
         raise ValueError("the cache must be on a GPU")
-    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+    return _raw_stream(index) if index == _current_device() else None
 
 
 def _kv_rows(t, name, cache, shape):
@@ -848,8 +856,11 @@ def nvfp4_kv_write(cache, k, v, slots):
     """Quantize the keys and values [tokens, heads, dim] of new tokens into
     slots (int64 [tokens]; a slot outside the cache skips its token).  k and v
     may be strided views with a contiguous last dimension."""
-    L = load_library()
     stream = _kv_stream(cache)
+    if stream is None:
+        with torch.cuda.device(cache.device):
+            return nvfp4_kv_write(cache, k, v, slots)
+    L = load_library()
     shape = k.shape
     if len(shape) != 3 or shape[1] != cache.heads or shape[2] != cache.dim:
         raise ValueError(f"k must be [tokens, {cache.heads}, {cache.dim}], not {tuple(shape)}")
@@ -866,8 +877,11 @@ def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, out=None):
     """(k, v), each [tokens, heads, dim] of dtype: what the cache holds in
     slots (int64 [tokens]; zeros for a slot outside the cache).  out: the pair
     of tensors to write."""
-    L = load_library()
     stream = _kv_stream(cache)
+    if stream is None:
+        with torch.cuda.device(cache.device):
+            return nvfp4_kv_read(cache, slots, dtype, out)
+    L = load_library()
     if slots.dim() != 1:
         raise ValueError("slots must be int64 [tokens]")
     tokens = slots.shape[0]
@@ -887,16 +901,17 @@ def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, out=None):
 
 
 @functools.lru_cache(maxsize=4096)
-def _kv_attention_bytes(pages, page_size, heads, dim, *sizes):
-    """Bytes of workspace: a function of the sizes alone."""
+def _kv_attention_bytes(device, pages, page_size, heads, dim, *sizes):
+    """Bytes of workspace: a function of the sizes and of the GPU with index `device`."""
     s = _KVCacheStruct(256, 256, 256, 256, None, None, pages, page_size, heads, dim)
-    return load_library().nvfp4_kv_attention_workspace_size(s, *sizes)
+    with torch.cuda.device(device):
+        return load_library().nvfp4_kv_attention_workspace_size(s, *sizes)
 
 
 def kv_attention_workspace(cache, tokens, query_heads, seqs, max_queries, max_context, window=0):
     """(workspace, bytes) for nvfp4_kv_attention calls of these sizes."""
-    nbytes = _kv_attention_bytes(cache.pages, cache.page_size, cache.heads, cache.dim, tokens, query_heads, seqs,
-                                 max_queries, max_context, window)
+    nbytes = _kv_attention_bytes(cache._gpu, cache.pages, cache.page_size, cache.heads, cache.dim, tokens,
+                                 query_heads, seqs, max_queries, max_context, window)
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device), nbytes
 
 
@@ -911,8 +926,12 @@ def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, ma
     1/sqrt(dim); window > 0 keeps the last `window` keys of each query.
     Returns out [tokens, query_heads, dim], with return_lse also the float32
     log-sum-exp [tokens, query_heads] of the scores."""
-    L = load_library()
     stream = _kv_stream(cache)
+    if stream is None:
+        with torch.cuda.device(cache.device):
+            return nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts, max_queries, max_context, scale,
+                                      causal, window, return_lse, out, workspace)
+    L = load_library()
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.dim:
         raise ValueError(f"q must be [tokens, query_heads, {cache.dim}], not {tuple(shape)}")
@@ -938,8 +957,8 @@ def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, ma
         raise ValueError("out must be contiguous and have q's shape, dtype and device")
     lse = torch.empty((tokens, query_heads), dtype=torch.float32, device=cache.device) if return_lse else None
     if workspace is None:
-        nbytes = _kv_attention_bytes(cache.pages, cache.page_size, cache.heads, cache.dim, tokens, query_heads,
-                                     seqs, max_queries, max_context, window)
+        nbytes = _kv_attention_bytes(cache._gpu, cache.pages, cache.page_size, cache.heads, cache.dim, tokens,
+                                     query_heads, seqs, max_queries, max_context, window)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     else:

@@ -106,6 +106,26 @@ nvfp4_status check_device(const char* op, hipStream_t stream) {
   return NVFP4_OK;
 }
 
+// While one lives, the device behind `stream` is the current one (what a launch
+// asks of its device, as its compute units, it asks of the current one).
+class StreamDevice {
+ public:
+  explicit StreamDevice(hipStream_t stream) {
+    int dev = 0, cur = 0;
+    if (stream && hipStreamGetDevice(stream, &dev) == hipSuccess && hipGetDevice(&cur) == hipSuccess && dev != cur &&
+        hipSetDevice(dev) == hipSuccess)
+      before_ = cur;
+  }
+  ~StreamDevice() {
+    if (before_ >= 0) (void)hipSetDevice(before_);
+  }
+  StreamDevice(const StreamDevice&) = delete;
+  StreamDevice& operator=(const StreamDevice&) = delete;
+
+ private:
+  int before_ = -1;
+};
+
 nvfp4_status launched(const char* op, hipError_t e) {
   if (e != hipSuccess) return fail(NVFP4_ERR_DEVICE, "[%s] Kernel launch failed: %s", op, hipGetErrorString(e));
   return ok();
@@ -1247,6 +1267,7 @@ nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const vo
   }
   if (nvfp4_status st = check_device(op, stream)) return st;
   if (tokens == 0) return ok();
+  const StreamDevice on(stream);
   return launched(op, nvfp4::launch_kv_write(c, k, v, dt, tokens, k_token_stride, k_head_stride,
                                              v_token_stride, v_head_stride, slots, stream));
 }
@@ -1265,6 +1286,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
   }
   if (nvfp4_status st = check_device(op, stream)) return st;
   if (tokens == 0) return ok();
+  const StreamDevice on(stream);
   return launched(op, nvfp4::launch_kv_read(c, slots, tokens, k, v, dt, stream));
 }
 
@@ -1336,6 +1358,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
     return fail(NVFP4_ERR_INVALID_ARGUMENT,
                 "[kv_attention] without query_starts every sequence has one query: tokens must equal seqs "
                 "and max_queries 1.");
+  const StreamDevice on(stream);
   const size_t need = tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
   if (tokens > 0 && seqs > 0) {
     if (!q || !out || !context_lens || (max_context > 0 && !page_table))

@@ -21,6 +21,8 @@
 // Rows.  The `groups` query heads of a kv head and the queries of a sequence
 // share its keys, so they form the rows r = query * groups + head of one
 // product, and keys and values are read once for all of them.
+#include <atomic>
+
 #include "kv_device.h"
 
 namespace nvfp4 {
@@ -1576,9 +1578,10 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
 
 constexpr int kMaxLds = 144 * 1024;  // leaves room for the kernels' static LDS
 
-// Lets `kernel` have more than 64 KB of dynamic LDS; once per device.
+// Lets `kernel` have more than 64 KB of dynamic LDS; once per device (or twice,
+// by two threads at once).
 template <typename K>
-hipError_t allow_lds(K* kernel, bool (&set)[64]) {
+hipError_t allow_lds(K* kernel, std::atomic<bool> (&set)[64]) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) dev = 0;
   if (dev < 0 || dev >= 64 || set[dev]) return hipSuccess;
@@ -1594,7 +1597,7 @@ hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvShare& sh,
   const size_t lds = (size_t)kFewWaves * kFewTile * few_row_bytes(NG) + 2 * 8 * kFewPages;
 #define KV_FEW(MT, SPLIT)                                                                         \
   do {                                                                                            \
-    static bool set[64];                                                                          \
+    static std::atomic<bool> set[64];                                                             \
     if (hipError_t e = allow_lds(&kv_few_kernel<NG, MT, SPLIT, EXACT>, set)) return e;            \
     kv_few_kernel<NG, MT, SPLIT, EXACT><<<p.groups, 256, lds, s>>>(c, a, sh, dt, q_vec);          \
   } while (0)
@@ -1612,7 +1615,7 @@ hipError_t launch_many(const KvCache& c, const KvAttention& a, const KvChunks& s
   const dim3 grid((unsigned)(sp.row_tiles * c.heads * sp.splits), a.seqs);
 #define KV_MANY(SPLIT)                                                                            \
   do {                                                                                            \
-    static bool set[64];                                                                          \
+    static std::atomic<bool> set[64];                                                             \
     if (hipError_t e = allow_lds(&kv_many_kernel<NG, SPLIT, EXACT>, set)) return e;               \
     kv_many_kernel<NG, SPLIT, EXACT><<<grid, 256, many_lds(NG), s>>>(c, a, sp, dt, q_vec);        \
   } while (0)

@@ -117,3 +117,61 @@ def test_workspace_sizes(L):
     assert size(many, 1023, 16384, 1023, 1, 100, 0) == 0 and size(many, 1024, 16384, 1024, 1, 100, 0) > 0
     for window in (1 << 20, 1 << 40):  # as good as none
         assert size(_struct(2, 128, pages=1 << 16), 1, 8, 1, 1, 1 << 20, window) == need
+
+
+class _Devices:
+    """Two GPUs as torch shows them: the current one, and the changes to it."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.entered = 0, []
+        devices = self
+
+        class device:
+            def __init__(self, which):
+                self.index = which if isinstance(which, int) else which.index
+
+            def __enter__(self):
+                self.before, devices.current = devices.current, self.index
+                devices.entered.append(self.index)
+
+            def __exit__(self, *_):
+                devices.current = self.before
+
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(nv, "_current_device", lambda: devices.current)
+
+
+def test_calls_run_on_the_device_of_their_cache(monkeypatch):
+    """A cache on another GPU than the current one: every call makes that current, and leaves the current one after."""
+    import types
+    devices = _Devices(monkeypatch)
+    seen = []
+
+    def stream(index):
+        seen.append((index, devices.current))
+        raise InterruptedError
+
+    monkeypatch.setattr(nv, "_raw_stream", stream)
+    cache = types.SimpleNamespace(device=torch.device("cuda:1"), _gpu=1, pages=2, heads=1, page_size=4, dim=16)
+    for call in (lambda: nv.nvfp4_kv_write(cache, None, None, None), lambda: nv.nvfp4_kv_read(cache, None),
+                 lambda: nv.nvfp4_kv_attention(None, cache, None, None)):
+        with pytest.raises(InterruptedError):
+            call()
+        assert seen.pop() == (1, 1) and devices.entered.pop() == 1 and devices.current == 0
+    cache.device, cache._gpu = torch.device("cuda:0"), 0
+    with pytest.raises(InterruptedError):
+        nv.nvfp4_kv_read(cache, None)
+    assert seen.pop() == (0, 0) and not devices.entered
+
+
+def test_workspace_bytes_are_of_a_device(monkeypatch):
+    """GPUs may differ in compute units: the bytes of one are not remembered for the other."""
+    import types
+    devices = _Devices(monkeypatch)
+    library = types.SimpleNamespace(nvfp4_kv_attention_workspace_size=lambda *_: (100, 300)[devices.current])
+    monkeypatch.setattr(nv, "load_library", lambda: library)
+    nv._kv_attention_bytes.cache_clear()
+    sizes = (2, 4, 1, 16, 1, 1, 1, 1, 8, 0)
+    assert [nv._kv_attention_bytes(d, *sizes) for d in (0, 1, 0, 1)] == [100, 300, 100, 300]
+    assert devices.entered == [0, 1]
+    nv._kv_attention_bytes.cache_clear()
