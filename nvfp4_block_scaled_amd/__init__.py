@@ -915,15 +915,18 @@ def kv_attention_workspace(cache, tokens, query_heads, seqs, max_queries, max_co
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device), nbytes
 
 
-def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, max_queries=1,
+def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, max_queries=None,
                        max_context=None, scale=None, causal=True, window=0, return_lse=False, out=None,
                        workspace=None):
     """Attention of q [tokens, query_heads, dim] over the cached keys and
     values of seqs sequences: page_table int32 [seqs, table_pages],
     context_lens int32 [seqs] (cached tokens, the queries' own included),
     query_starts int32 [seqs + 1] (None: one query a sequence).  max_queries
-    and max_context bound what is on the device; scale defaults to
-    1/sqrt(dim); window > 0 keeps the last `window` keys of each query.
+    and max_context bound what is on the device (without them: all tokens may
+    be one sequence's, with query_starts, and a context fills its row of the
+    page table); the closer, the faster.  scale defaults to 1/sqrt(dim);
+    window > 0 keeps the last `window` keys of each query.  No gradient
+    passes through the call.
     Returns out [tokens, query_heads, dim], with return_lse also the float32
     log-sum-exp [tokens, query_heads] of the scores."""
     stream = _kv_stream(cache)
@@ -947,6 +950,8 @@ def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, ma
     if query_starts is not None:
         _kv_index(query_starts, "query_starts", cache, torch.int32, (seqs + 1,))
         starts = query_starts.data_ptr()
+    if max_queries is None:
+        max_queries = 1 if starts is None else max(tokens, 1)
     if max_context is None:
         max_context = table_pages * cache.page_size
     if scale is None:

@@ -253,3 +253,18 @@ def test_scales_and_codes_assigned_anew():
     new = results(a)
     assert all(torch.equal(x, y) for x, y in zip(new, results(b)))
     assert not any(torch.equal(x, y) for x, y in zip(new, old))
+
+
+@pytest.mark.parametrize("counts", [[3, 1, 0, 2], [50, 7, 1, 0], [1, 1, 1, 1]])
+def test_query_counts_that_are_not_stated(counts):
+    """Without max_queries every query of query_starts is answered, whatever the output's memory held."""
+    contexts = [130, 64, 20, 5]
+    table, pages, _ = _batch(contexts, 16, 7)
+    cache = _kv.random_cache(pages, 16, 2, 64, 2800)
+    starts = [sum(counts[:i]) for i in range(5)]
+    q = torch.randn(starts[-1], 4, 64, generator=torch.Generator().manual_seed(2801)).bfloat16().cuda()
+    lens = torch.tensor(contexts, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    got, lse = nv.nvfp4_kv_attention(q, cache, table.cuda(), lens, return_lse=True, out=out,
+                                     query_starts=torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    _kv.check(got, lse, _kv.reference(q, cache, table, lens, starts, 0.125), f"counts {counts}")
