@@ -13,6 +13,7 @@
 #include <string>
 
 #include "../../include/nvfp4.h"
+#include "kv_internal.h"
 #include "nvfp4_internal.h"
 
 namespace {

@@ -8,6 +8,7 @@
 // s / page_size.
 #pragma once
 
+#include "kv_internal.h"
 #include "nvfp4_device.h"
 #include "nvfp4_internal.h"
 

@@ -175,3 +175,14 @@ def test_workspace_bytes_are_of_a_device(monkeypatch):
     assert [nv._kv_attention_bytes(d, *sizes) for d in (0, 1, 0, 1)] == [100, 300, 100, 300]
     assert devices.entered == [0, 1]
     nv._kv_attention_bytes.cache_clear()
+
+
+def test_cache_declarations_keep_to_their_header():
+    """bench.py reports measured traffic only for the sources and the two shared headers that it was measured on:
+    the cache's declarations stand in a header of their own, so that they do not void those figures."""
+    import os
+    csrc = os.path.join(os.path.dirname(nv.LIB_PATH), "csrc")
+    for shared in ("nvfp4_internal.h", "nvfp4_device.h"):
+        with open(os.path.join(csrc, shared)) as f:
+            text = f.read()
+        assert "kv_" not in text and "Kv" not in text, shared
