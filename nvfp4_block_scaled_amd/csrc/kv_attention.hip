@@ -12,11 +12,14 @@
 // matrix cores multiply it without any rounding; the global scales go into
 // the factor of the scores and into the output.  A query row is brought into
 // float16's range by a power of two, which keeps every bit of a float16 or
-// bfloat16 element (down to 2^-38 of the row's largest); a float32 element
-// becomes the sum of two float16, 22 bits.  Probabilities are rounded to
-// float16 for their product with the values (2^-12 relative, below the
-// rounding of a 16-bit output; float32: two float16 again).  Scores, the
-// running maximum, sums and outputs are float32.
+// bfloat16 element down to 2^-27 of the row's largest, and smaller ones to
+// within 2^-38 of it; a float32 element becomes the sum of two float16, 22
+// bits.  Probabilities are rounded to float16 for their product with the values
+// (2^-11 of each: an eighth of a bfloat16 output's own rounding, as much as a
+// float16 output's; float32: two float16 again, 2^-22).  Scores, the running
+// maximum, sums and outputs are float32.
+//
+// What a mask hides reaches no output, not even as NaN (notes in both kernels).
 //
 // Rows.  The `groups` query heads of a kv head and the queries of a sequence
 // share its keys, so they form the rows r = query * groups + head of one
@@ -449,18 +452,24 @@ __device__ __forceinline__ int kv_units_each(const KvCache& c, const KvAttention
 // transposed (ds_read_b64_tr_b16); nothing in the loop waits for another wave.
 //
 // Bound by memory while contexts are long: 4 x 131072 keys, 8 heads of 128,
-// 604 MB, 112 - 120 us with the join, 5.0 - 5.4 TB/s.  Shorter ones show the start, a chain of
-// four dependent loads (lengths, page number, codes; queries beside them),
-// about 7 us, and the join: 32 contexts of up to 8192, 166 MB, 50 us, 3.3
-// TB/s.  A whole tile in flight a wave and three workgroups a CU cover the
-// latency (1 or 2 a CU: 81 and 58 us).
+// 604 MB, 112 - 120 us with the join, 5.0 - 5.4 TB/s (vector units busy 58 %
+// of the time, LDS 31 %, matrix cores 12 %).  Shorter ones show the start, a
+// chain of four dependent loads (lengths, page number, codes; queries beside
+// them), about 7 us, and the join: 32 contexts of up to 8192, 166 MB, 49 us,
+// 3.4 TB/s.  A whole tile in flight a wave and three workgroups a CU cover the
+// latency (1 or 2 a CU: 81 and 58 us).  With 17 to 32 rows one workgroup a CU
+// has its registers, and that latency shows: 8 x 30000 keys, 4 heads of 128, 16
+// rows 45 us, 24 rows 78, 32 rows 80.
 
 constexpr int few_row_bytes(int NG) { return 128 * NG + 32; }  // a key's values in LDS: +32 spreads the banks
 constexpr int kFewPages = 512;  // pages staged at a time
 constexpr uint64_t kNoPage = ~0ull;
 
-// Waves per SIMD (and workgroups per CU) that the registers of an instance
-// allow without spills.
+// Waves per SIMD, and workgroups per CU, that an instance's registers are cut
+// to.  What the compiler then spills, vector registers by <dim / 64, row tiles,
+// float16 a query element>: <1, 1, 1> 9, <2, 1, 1> 2, <1, 2, 1> 17, <4, 1, 1> 2,
+// <4, 2, 1> 37, <4, 2, 2> 175, the others none; for heads that are no whole 64s
+// up to 25 more.  All spill 148 to 228 scalar registers into vector lanes.
 constexpr int few_occupancy(int NG, int MT, int SPLIT) {
   const int size = NG * MT * SPLIT;
   return size == 1 ? 4 : size == 2 ? 3 : size <= 4 && MT == 1 ? 2 : 1;
@@ -938,15 +947,21 @@ kv_few_kernel(KvCache c, KvAttention a, KvShare sh, int dt, bool q_vec) {
 // under way; one barrier a tile.  Rows of LDS are padded so that the 16-byte
 // reads of K and the transposing reads of V touch every bank once.
 //
-// Bound by instruction issue: the 16 scores a lane holds of a 32 x 32 tile
-// take 512 cycles of the matrix cores (dim 128) and about 320 of the vector
-// units (each an exponential, 8.6, a multiply-add, 4.9, half a conversion to
-// float16, 3.7, maximum and sum), besides decoding and LDS reads.  4096 causal queries over as many
-// keys, 32 heads of 128: 182 - 194 us by the machine, 710 - 755 TFLOP/s; up to
-// 1023 queries each of 5 sequences over up to 9001 keys: 427 - 492 us, 620 -
-// 715 TFLOP/s; a large bfloat16 matrix product reaches 1280.  256 rows and 8 waves share the decoding
-// further, but leave one workgroup a CU: 192 against 198 us and 470 against
-// 440 (kernels of the time).
+// No unit bounds it alone.  4096 causal queries over as many keys, 32 heads of
+// 128: vector units busy 48 % of the time, LDS 37 % (its bank conflicts 14 %),
+// matrix cores 28 %; a wave waits 28 % of its time, and 26 % more for its turn
+// to issue.  Two waves a SIMD, in step by a barrier a tile, do not cover one
+// another better than that.  By hand: the 16 scores a lane holds of a 32 x 32
+// tile take 512 cycles of the matrix cores and about 320 of the vector units
+// (each an exponential, 8.6, a multiply-add, 4.9, half a conversion to float16,
+// 3.7, maximum and sum), decoding besides, and the four waves' 16 KB each of
+// fragments of a tile 512 cycles of the CU's LDS.  187 - 203 us by the machine,
+// 680 - 735 TFLOP/s; up to 1023 queries each of 5 sequences over up to 9001
+// keys: 421 - 453 us, 675 - 725 TFLOP/s; a large float16 matrix product reaches
+// 1324.  256 rows and 8 waves share the decoding further, but not the reads of
+// fragments, and leave one workgroup a CU: 192 against 198 us and 470 against
+// 440 (kernels of the time).  float32 queries: one workgroup a CU for its
+// registers, and four products for one.
 //
 // Too few workgroups for the GPU split the keys further (KvChunks).
 constexpr int kManyRows = 128;
@@ -1519,7 +1534,9 @@ __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttentio
 //   2048 keys: 1 sequence 24.7 / 14.0; 16 26.2 / 27.6 (heads of 256 40 / 32); 64
 //   40 / 51; 128, lengths up to that 55 / 82
 //   4096 keys: 64 sequences 72 / 83, lengths up to that 58 / 63
-// Past 4096 keys one long context among short ones would keep all waiting.
+// Past 4096 keys one long context among short ones would keep all waiting.  With
+// few pairs the rule gives up to 3 us (1 sequence of 1024 keys) for one launch
+// and no workspace; the size of a head is not in it.
 constexpr int kFewAlone = 1024, kFewAloneMost = 4096;
 // (A launch has fewer than 2^24 workgroups.)
 constexpr int64_t few_alone(int64_t pairs) {
@@ -1538,7 +1555,7 @@ constexpr int few_groups(int dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : dim 
 // Up to 32 rows a (sequence, kv head) the keys are streamed once past all of
 // them; more rows are matrix work.  32 rows, 8 x 30000 keys, 4 heads, few
 // against many, us: dim 128 76 / 90, float32 92 / 175; dim 256 128 / 254,
-// float32 282 / 317 (40 rows of dim 128 on the many-rows kernel: 95).
+// float32 282 / 317 (48 rows of dim 128 on the many-rows kernel: 92, 96 rows 105).
 KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_queries * a.groups;
@@ -1558,7 +1575,8 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
     const int64_t tiles = pairs * p.row_tiles;
-    // As many workgroups as run at once, rounded to the nearest number of
+    // As many workgroups as run at once (two a CU: heads of up to 128 in 16 bits
+    // and of 64 in 32; the other instances run one), rounded to the nearest number of
     // splits; for short contexts rounded down, as a second launch is worth only
     // a whole factor there.  3 x 400 queries, 32 heads of 128, us, nearest
     // against down: 2000 keys 102 / 88, 4200 keys 168 / 168, 9000 keys 315 /
