@@ -696,7 +696,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
  * float16; the global scales multiply scores and sums in float32); each
  * probability is rounded to float16 before its product with the values, for
  * float32 q to a pair of float16.  Small probabilities keep their bits too
- * (2^-11 of each, not of the largest).
+ * (2^-11 of each, not of the largest), down to 2^-126 of the largest.  Keys
+ * that a query does not see leave its output alone whatever they hold; a block
+ * scale that is NaN makes NaN of its 16 values for the queries that see its key.
  * Errors: bad dtype or cache, negative or zero sizes (tokens or seqs = 0 is
  * a no-op), query_heads not a multiple of heads, query_starts NULL with
  * tokens != seqs or max_queries != 1, window < 0 or window > 0 without
