@@ -607,6 +607,37 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
                                  int64_t n, int64_t k, void* out, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * nvfp4_mx_rms_norm -- root-mean-square norm of the rows of x [rows, k], with
+ * the residual's addition in front and an mx encode behind it, in one pass:
+ *     h = T(x + residual)                   (x without a residual)
+ *     r = float32(1 / sqrt(sum(h^2) / k + eps)), the squares summed in float64
+ *     y = (h * r) * weight                  float32, each product rounded
+ *     codes, scales = nvfp4_mx_quantize of the float32 y
+ * except that a group with a y that is NaN gets the scale byte 255, NaN (and
+ * codes without meaning), so that a NaN does not vanish in the encode.
+ *   x         device [rows, k] of type dt
+ *   residual  device [rows, k] of type dt, or NULL
+ *   weight    device [k] of type dt, or NULL: ones
+ *   eps       > 0 and finite
+ *   packed    0: codes and scales row-major, as nvfp4_mx_quantize writes them;
+ *             else in the operand layout above (sizes from nvfp4_mx_pack_size),
+ *             its padding zeroed, as nvfp4_mx_quantize_packed writes it
+ *   sum       device [rows, k] of type dt, written with h, or NULL; may be x
+ *             or residual themselves
+ *   normed    device [rows, k] of type dt, written with T(y), or NULL; may be
+ *             x or residual if sum is not the same
+ * All device pointers but scales 16-byte aligned.  Other overlaps of outputs
+ * with inputs or each other leave them undefined.
+ * Errors: bad dtype or mode, rows < 0 (rows = 0 is a no-op), k not a positive
+ * multiple of 32, eps not positive, NULL codes or scales, misaligned pointers,
+ * sum equal to normed; UNSUPPORTED for 2^22 rows or more, k above 2^30.
+ */
+nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* weight, nvfp4_dtype dt,
+                               nvfp4_mx_mode mode, int64_t rows, int64_t k, double eps, int packed,
+                               void* sum, void* normed, uint8_t* codes, uint8_t* scales,
+                               hipStream_t stream);
+
 /* ---------------------------------------------------------------- key/value cache
  *
  * A paged cache of keys and values held in NVFP4, and attention over it.

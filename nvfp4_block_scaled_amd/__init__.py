@@ -21,6 +21,8 @@ The functions carry the C entry points' names (see include/nvfp4.h):
                                                       (same, on the packed copy)
     nvfp4_mx_quantize / _dequantize / _quant_dequant / _pack / _qqmm / _qqmm_packed
                                                       (the mxfp4 / mxfp8 modes)
+    nvfp4_mx_rms_norm(x, weight, mode, residual, ...) -> MxNormed
+                                                      (norm with residual, its output encoded)
     KVCache(...), kv_cache(pages, page_size, heads, dim, ...)
                                                       (a paged key/value cache held in NVFP4)
     nvfp4_kv_write(cache, k, v, slots)                (quantize tokens into their slots)
@@ -34,6 +36,7 @@ requires ("mlx 0.30.7.2 -> 0.30.7.6" diff, page 8).
 import ctypes
 import functools
 import os
+import typing
 
 import torch
 
@@ -109,6 +112,7 @@ def load_library():
         "nvfp4_mx_qqmm": (I, [P, I, I, P, P, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_qqmm_packed": (I, [P, I, I, P, P, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_gather_qmm": (I, [P, I, I, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
+        "nvfp4_mx_rms_norm": (I, [P, P, P, I, I, I64, I64, ctypes.c_double, I, P, P, P, P, P]),
         "nvfp4_kv_write": (I, [C, P, P, I, I64, I64, I64, I64, I64, P, P]),
         "nvfp4_kv_read": (I, [C, P, I64, P, P, I, P]),
         "nvfp4_kv_attention_workspace_size": (SZ, [C, I64, I64, I64, I64, I64, I64]),
@@ -751,6 +755,66 @@ def nvfp4_mx_qqmm_packed(x, w, out=None, workspace=None):
     return out
 
 
+class MxNormed(typing.NamedTuple):
+    """What nvfp4_mx_rms_norm gives: `quantized`, (codes, scales) or an
+    MxPacked; `sum`, x + residual in x's type (x itself without a residual);
+    `normed`, the norm's output in x's type, or None."""
+    quantized: typing.Any
+    sum: torch.Tensor
+    normed: typing.Optional[torch.Tensor]
+
+
+def nvfp4_mx_rms_norm(x, weight=None, mode="mxfp8", residual=None, eps=1e-6, packed=False, normed=False,
+                      sum_out=None, out=None):
+    """Root-mean-square norm of the rows of x [..., k], encoded in an mx mode:
+    h = x + residual (rounded to x's type), y = h / sqrt(mean(h^2) + eps) *
+    weight, and y's codes and scales straight from float32 (of a group with a
+    NaN the scale is NaN).  packed: in the operand layout of
+    nvfp4_mx_mm_packed.  normed: y in x's type too.  sum_out, out: what to
+    write the sum (x or residual themselves will do) and the (codes, scales) or
+    MxPacked to.  No gradient passes through the call.  Returns MxNormed."""
+    L = load_library()
+    bits = _mx_mode(mode)
+    _dev(x, "x")
+    code = _dtype_code(x, "x")
+    rows, k = _rows_k(x)
+    for t, name, shape in ((residual, "residual", x.shape), (weight, "weight", (k,)), (sum_out, "sum_out", x.shape)):
+        if t is None:
+            continue
+        if t.dtype is not x.dtype or t.shape != shape or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {x.dtype} {tuple(shape)} on x's device")
+    if x.device.index != torch.cuda.current_device():
+        with torch.cuda.device(x.device):
+            return nvfp4_mx_rms_norm(x, weight, mode, residual, eps, packed, normed, sum_out, out)
+    if packed:
+        cb, sb = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        _check(L.nvfp4_mx_pack_size(bits, rows, k, ctypes.byref(cb), ctypes.byref(sb)))
+        if out is None:
+            out = MxPacked(torch.empty(cb.value, dtype=torch.uint8, device=x.device),
+                           torch.empty(sb.value, dtype=torch.uint8, device=x.device), (rows, k), mode)
+        elif not isinstance(out, MxPacked) or out.mode != mode or out.shape != (rows, k):
+            raise ValueError("out must be an MxPacked of this shape and mode")
+        codes, scales = out.codes, out.scales
+        sizes = ((cb.value,), (sb.value,))
+    else:
+        sizes = (tuple(x.shape[:-1]) + (_mx_code_cols(k, mode),), tuple(x.shape[:-1]) + (k // 32,))
+        if out is None:
+            out = tuple(torch.empty(s, dtype=torch.uint8, device=x.device) for s in sizes)
+        codes, scales = out
+    for t, s in zip((codes, scales), sizes):
+        if t.dtype is not torch.uint8 or t.shape != s or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"out's codes and scales must be contiguous uint8 {sizes} on x's device")
+    total = sum_out
+    if total is None and residual is not None:
+        total = torch.empty_like(x)
+    y = torch.empty_like(x) if normed else None
+    _check(L.nvfp4_mx_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                               None if weight is None else weight.data_ptr(), code, bits, rows, k, eps, int(bool(packed)),
+                               None if total is None else total.data_ptr(), None if y is None else y.data_ptr(),
+                               codes.data_ptr(), scales.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    return MxNormed(out, x if total is None else total, y)
+
+
 # ------------------------------------------------------------------ key/value cache
 
 _KV_HELD = ("k_codes", "k_scales", "v_codes", "v_scales", "global_scale_k", "global_scale_v")
@@ -1075,7 +1139,7 @@ __all__ = [
     "qqmm_workspace", "gather_workspace", "quantize", "dequantize", "qqmm", "gather_qmm",
     "MX_MODES", "MxPacked", "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_quant_dequant",
     "nvfp4_mx_pack", "mx_qqmm_workspace", "nvfp4_mx_qqmm", "nvfp4_mx_qqmm_packed",
-    "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "nvfp4_gather_qmm_indexed",
+    "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "MxNormed", "nvfp4_mx_rms_norm", "nvfp4_gather_qmm_indexed",
     "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "nvfp4_kv_read",
     "kv_attention_workspace", "nvfp4_kv_attention",
 ]

@@ -14,6 +14,7 @@
 
 #include "../../include/nvfp4.h"
 #include "kv_internal.h"
+#include "layer_internal.h"
 #include "nvfp4_internal.h"
 
 namespace {
@@ -1204,6 +1205,32 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
   if (he != hipSuccess) return launched(op, he);
   return launched(op, nvfp4::launch_mx_gather_gemm(x, dt, mode, w_codes, w_scales, offsets, perm, t,
                                                     t * top_k, top_k, e, n, k, out, stream));
+}
+
+nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* weight, nvfp4_dtype dt,
+                               nvfp4_mx_mode mode, int64_t rows, int64_t k, double eps, int packed,
+                               void* sum, void* normed, uint8_t* codes, uint8_t* scales,
+                               hipStream_t stream) {
+  const char* op = "mx_rms_norm";
+  if (nvfp4_status st = check_mx(op, x, dt, mode, rows, k)) return st;
+  if (!(eps > 0.0) || eps > 1.0e300)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[mx_rms_norm] eps must be positive and finite.");
+  if (rows > 0) {
+    CHECK_PTR("mx_rms_norm", codes);
+    CHECK_PTR("mx_rms_norm", scales);
+    if (!aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) || !aligned(normed, 16) || !aligned(codes, 16))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                  "[mx_rms_norm] residual, weight, sum, normed and codes must be 16-byte aligned.");
+    if (sum && sum == normed)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[mx_rms_norm] sum and normed must be different memory.");
+  }
+  if (rows >= (int64_t)1 << 22 || k > (int64_t)1 << 30)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[mx_rms_norm] Sizes too large (2^22 rows or more, or k above 2^30).");
+  if (nvfp4_status st = check_device(op, stream)) return st;
+  if (rows == 0) return ok();
+  const StreamDevice on(stream);
+  const nvfp4::MxNorm n{x, residual, weight, sum, normed, codes, scales, rows, k, eps, packed != 0};
+  return launched(op, nvfp4::launch_mx_norm(n, dt, mode, stream));
 }
 
 // ------------------------------------------------------------------ key/value cache
