@@ -684,6 +684,40 @@ nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const vo
                             hipStream_t stream);
 
 /*
+ * nvfp4_kv_write_rotated -- nvfp4_kv_write with the position rotation of the
+ * keys on the way, and of the queries beside it, in one launch.  The first
+ * rotary_dim values of a head form pairs (a, b): values i and i + rotary_dim/2,
+ * or with `interleaved` 2i and 2i + 1.  With the cosine c and sine s of pair i
+ * in the table's row `position`,
+ *     a' = a c - b s,   b' = b c + a s
+ * in float32, each product and sum rounded by itself; the rest of the head
+ * stays as it is.  Keys are quantized from these float32 values (no rounding
+ * to T between), values as by nvfp4_kv_write, queries rounded to T.
+ *   k, v, slots  as nvfp4_kv_write
+ *   positions    device int32 [tokens]; a token whose position lies outside
+ *                [0, table_rows) is not written and its q_out row is zeros
+ *   table        device float [table_rows, rotary_dim], 16-byte aligned: the
+ *                rotary_dim/2 cosines of a position, then its sines
+ *   rotary_dim   a positive multiple of 16, at most dim
+ *   q            device, type dt, strides as k's: element (t, h, d); NULL with
+ *                query_heads = 0: no queries
+ *   q_out        device [tokens, query_heads, dim] of type dt, 16-byte aligned,
+ *                written for every token, also one whose slot skips it; it may
+ *                not overlap the inputs
+ * Errors: as nvfp4_kv_write; rotary_dim out of range or no multiple of 16,
+ * table_rows < 0, query_heads < 0, NULL or misaligned table, positions, q or
+ * q_out; UNSUPPORTED for 2^26 tokens or more, query_heads above 65535,
+ * table_rows of 2^31 or more.
+ */
+nvfp4_status nvfp4_kv_write_rotated(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
+                                    int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                                    const int32_t* positions, const float* table, int64_t table_rows,
+                                    int64_t rotary_dim, int interleaved, const void* q, int64_t query_heads,
+                                    int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                                    hipStream_t stream);
+
+/*
  * nvfp4_kv_read -- the keys and values held in `slots`, dequantized to dt:
  * T(e2m1(q) * (e4m3(s) * g/2688)), as nvfp4_dequantize.
  *   slots  device int64 [tokens]; a slot outside [0, pages * page_size) gives zeros

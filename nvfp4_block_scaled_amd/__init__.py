@@ -26,6 +26,8 @@ The functions carry the C entry points' names (see include/nvfp4.h):
     KVCache(...), kv_cache(pages, page_size, heads, dim, ...)
                                                       (a paged key/value cache held in NVFP4)
     nvfp4_kv_write(cache, k, v, slots)                (quantize tokens into their slots)
+    nvfp4_kv_write_rotated(cache, k, v, slots, positions, table, q)
+                                                      (the same with the position rotation) -> q rotated
     nvfp4_kv_read(cache, slots, dtype)                -> (k, v)
     nvfp4_kv_attention(q, cache, page_table, context_lens, ...)
                                                       -> out or (out, lse)
@@ -114,6 +116,8 @@ def load_library():
         "nvfp4_mx_gather_qmm": (I, [P, I, I, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_rms_norm": (I, [P, P, P, I, I, I64, I64, ctypes.c_double, I, P, P, P, P, P]),
         "nvfp4_kv_write": (I, [C, P, P, I, I64, I64, I64, I64, I64, P, P]),
+        "nvfp4_kv_write_rotated": (I, [C, P, P, I, I64, I64, I64, I64, I64, P, P, P, I64, I64, I, P, I64, I64, I64,
+                                       P, P]),
         "nvfp4_kv_read": (I, [C, P, I64, P, P, I, P]),
         "nvfp4_kv_attention_workspace_size": (SZ, [C, I64, I64, I64, I64, I64, I64]),
         "nvfp4_kv_attention": (I, [C, P, I, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, ctypes.c_float,
@@ -937,6 +941,65 @@ def nvfp4_kv_write(cache, k, v, slots):
                             vt, vh, slots.data_ptr(), stream))
 
 
+def rotation_table(length, rotary_dim, base=10000.0, scale=1.0, device="cuda"):
+    """The float32 table [length, rotary_dim] of nvfp4_kv_write_rotated for positions 0 .. length - 1: the
+    cosines and sines of position * scale * base^(-2i / rotary_dim), the angles in 64 bits."""
+    if rotary_dim <= 0 or rotary_dim % 16:
+        raise ValueError("rotary_dim must be a positive multiple of 16")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * scale * base ** (-i / rotary_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def nvfp4_kv_write_rotated(cache, k, v, slots, positions, table, q=None, interleaved=False, out=None):
+    """nvfp4_kv_write with the keys rotated by positions (int32 [tokens]) on
+    the way, and the queries q [tokens, query_heads, dim] beside them: pairs of
+    the first rotary_dim values, halves of them or (interleaved) neighbours.
+    table: float32 [positions, rotary_dim], cosines then sines
+    (rotation_table).  A token whose position is outside the table is skipped
+    and its queries come back as zeros.  No gradient passes through the call.
+    Returns the rotated queries (out, if given), or None without q."""
+    stream = _kv_stream(cache)
+    if stream is None:
+        with torch.cuda.device(cache.device):
+            return nvfp4_kv_write_rotated(cache, k, v, slots, positions, table, q, interleaved, out)
+    L = load_library()
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != cache.heads or shape[2] != cache.dim:
+        raise ValueError(f"k must be [tokens, {cache.heads}, {cache.dim}], not {tuple(shape)}")
+    kt, kh = _kv_rows(k, "k", cache, shape)
+    vt, vh = _kv_rows(v, "v", cache, shape)
+    if v.dtype is not k.dtype:
+        raise ValueError("k and v must have one dtype")
+    tokens = shape[0]
+    _kv_index(slots, "slots", cache, torch.int64, (tokens,))
+    _kv_index(positions, "positions", cache, torch.int32, (tokens,))
+    table_shape = table.shape
+    if len(table_shape) != 2:
+        raise ValueError("table must be float32 [positions, rotary_dim]")
+    _kv_index(table, "table", cache, torch.float32, table_shape)
+    query_heads = qt = qh = 0
+    if q is not None:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != tokens or q_shape[2] != cache.dim:
+            raise ValueError(f"q must be [{tokens}, query_heads, {cache.dim}], not {tuple(q_shape)}")
+        qt, qh = _kv_rows(q, "q", cache, q_shape)
+        if q.dtype is not k.dtype:
+            raise ValueError("q and k must have one dtype")
+        query_heads = q_shape[1]
+        if out is None:
+            out = torch.empty(q_shape, dtype=q.dtype, device=cache.device)
+        elif out.shape != q_shape or out.dtype is not q.dtype or out.device != cache.device or not out.is_contiguous():
+            raise ValueError("out must be contiguous and have q's shape, dtype and device")
+    elif out is not None:
+        raise ValueError("out without q")
+    _check(L.nvfp4_kv_write_rotated(cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"), tokens, kt, kh, vt, vh,
+                                    slots.data_ptr(), positions.data_ptr(), table.data_ptr(), table_shape[0],
+                                    table_shape[1], 1 if interleaved else 0, q.data_ptr() if query_heads else None,
+                                    query_heads, qt, qh, out.data_ptr() if query_heads else None, stream))
+    return out
+
+
 def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, out=None):
     """(k, v), each [tokens, heads, dim] of dtype: what the cache holds in
     slots (int64 [tokens]; zeros for a slot outside the cache).  out: the pair
@@ -1140,6 +1203,6 @@ __all__ = [
     "MX_MODES", "MxPacked", "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_quant_dequant",
     "nvfp4_mx_pack", "mx_qqmm_workspace", "nvfp4_mx_qqmm", "nvfp4_mx_qqmm_packed",
     "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "MxNormed", "nvfp4_mx_rms_norm", "nvfp4_gather_qmm_indexed",
-    "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "nvfp4_kv_read",
+    "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "rotation_table", "nvfp4_kv_write_rotated", "nvfp4_kv_read",
     "kv_attention_workspace", "nvfp4_kv_attention",
 ]

@@ -1300,6 +1300,62 @@ nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const vo
                                              v_token_stride, v_head_stride, slots, stream));
 }
 
+nvfp4_status nvfp4_kv_write_rotated(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
+                                    int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                                    const int32_t* positions, const float* table, int64_t table_rows,
+                                    int64_t rotary_dim, int interleaved, const void* q, int64_t query_heads,
+                                    int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                                    hipStream_t stream) {
+  const char* op = "kv_write_rotated";
+  nvfp4::KvCache c;
+  if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
+  if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0 || q_token_stride < 0 ||
+      q_head_stride < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write_rotated] strides must be >= 0.");
+  if (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > c.dim)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "[kv_write_rotated] rotary_dim (%lld) must be a positive multiple of 16 and at most dim (%d).",
+                (long long)rotary_dim, c.dim);
+  if (table_rows < 0 || query_heads < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write_rotated] table_rows and query_heads must be >= 0.");
+  if (tokens > 0) {
+    if (!k || !v || !slots || !positions || (table_rows > 0 && !table))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write_rotated] k, v, slots, positions and table must not be NULL.");
+    if (query_heads > 0 && (!q || !q_out))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_write_rotated] q and q_out must not be NULL with query heads.");
+    if (!aligned(k, dtype_size(dt)) || !aligned(v, dtype_size(dt)) || !aligned(q, dtype_size(dt)) || !aligned(slots, 8) ||
+        !aligned(positions, 4) || !aligned(table, 16) || !aligned(q_out, 16))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                  "[kv_write_rotated] table and q_out must be 16-byte aligned, the others to their elements.");
+  }
+  if (tokens >= (int64_t)1 << 26 || query_heads > 65535 || table_rows > INT32_MAX)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[kv_write_rotated] Sizes too large.");
+  if (nvfp4_status st = check_device(op, stream)) return st;
+  if (tokens == 0) return ok();
+  const StreamDevice on(stream);
+  nvfp4::KvRotate a{};
+  a.k = k;
+  a.v = v;
+  a.q = query_heads > 0 ? q : nullptr;
+  a.q_out = q_out;
+  a.tokens = tokens;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  a.q_token = query_heads > 0 ? q_token_stride : 0;
+  a.q_head = query_heads > 0 ? q_head_stride : 0;
+  a.slots = slots;
+  a.positions = positions;
+  a.table = table;
+  a.table_rows = table_rows;
+  a.rotary = (int)rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.query_heads = (int)query_heads;
+  return launched(op, nvfp4::launch_kv_rotate(c, a, dt, stream));
+}
+
 nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k,
                            void* v, nvfp4_dtype dt, hipStream_t stream) {
   const char* op = "kv_read";
