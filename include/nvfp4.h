@@ -785,6 +785,37 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
                                 size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * nvfp4_kv_tree_attention -- nvfp4_kv_attention for drafted tokens that form
+ * trees: sequence b's n queries are tokens that a drafter has proposed, and
+ * their keys and values are the last n of its context of L cached tokens (in
+ * the queries' order, whatever their positions).  Query i sees
+ *   - key j < L - n: all of them, or with a window > 0 those with
+ *     j > positions[i] - window;
+ *   - key L - n + d, draft d's: if bit d % 64 of word d / 64 of its row of
+ *     `tree` is set (its ancestors' bits as a rule, and its own; nothing is
+ *     added to them, and a window does not touch them)
+ * as far as j < L and the page's number lies in [0, pages).  With L < n the
+ * first n - L drafts have no key.
+ *   tree        device uint64 [tokens, tree_words], 8-byte aligned; bits from n
+ *               on count for nothing
+ *   tree_words  at least max_queries / 64, rounded up
+ *   positions   device int32 [tokens], or NULL without a window; taken as at
+ *               least L - n and at most L - 1
+ *   the other arguments, the numbers and the errors as nvfp4_kv_attention with
+ *   query_starts, which must not be NULL here; the workspace is
+ *   nvfp4_kv_attention_workspace_size() of the same sizes.
+ * Errors besides: tree_words too small (or of 2^25 or more), NULL or
+ * misaligned tree or positions.
+ */
+nvfp4_status nvfp4_kv_tree_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
+                                     int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
+                                     const int32_t* page_table, int64_t seqs, int64_t table_pages,
+                                     const int32_t* context_lens, const int32_t* query_starts,
+                                     int64_t max_queries, int64_t max_context, float scale, const uint64_t* tree,
+                                     int64_t tree_words, const int32_t* positions, int64_t window, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Test hook: treat every device as having this gcnArchName (NULL restores the
  * real query).  Lets host-only tests reach the unsupported-device error.
  */

@@ -31,6 +31,8 @@ The functions carry the C entry points' names (see include/nvfp4.h):
     nvfp4_kv_read(cache, slots, dtype)                -> (k, v)
     nvfp4_kv_attention(q, cache, page_table, context_lens, ...)
                                                       -> out or (out, lse)
+    nvfp4_kv_tree_attention(q, cache, page_table, context_lens, query_starts, tree, ...)
+                                                      (of drafted tokens that form a tree)
 Global scales are float32 device tensors with one element (per expert: e
 elements, any shape such as [e, 1, 1]), as the pages' validate_global_scale
 requires ("mlx 0.30.7.2 -> 0.30.7.6" diff, page 8).
@@ -122,6 +124,8 @@ def load_library():
         "nvfp4_kv_attention_workspace_size": (SZ, [C, I64, I64, I64, I64, I64, I64]),
         "nvfp4_kv_attention": (I, [C, P, I, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, ctypes.c_float,
                                    I, I64, P, P, P, SZ, P]),
+        "nvfp4_kv_tree_attention": (I, [C, P, I, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, ctypes.c_float,
+                                        P, I64, P, I64, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -1105,6 +1109,86 @@ def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, ma
     return (out, lse) if return_lse else out
 
 
+def kv_trees(parents):
+    """(tree int64 [tokens, words], depths int32 [tokens]) of drafted tokens on the CPU, from their parents: a list
+    for each sequence with the index of each draft's parent among the drafts before it, -1 for one that follows
+    the context.  A draft sees its ancestors and itself; its position is the context's before the drafts plus its
+    depth."""
+    words = max((-(-len(p) // 64) for p in parents), default=1) or 1
+    rows, depths = [], []
+    for sequence in parents:
+        bits, depth = [], []
+        for d, p in enumerate(sequence):
+            if not -1 <= p < d:
+                raise ValueError(f"draft {d}: its parent ({p}) must be an earlier draft, or -1")
+            bits.append(1 << d | (bits[p] if p >= 0 else 0))
+            depth.append(depth[p] + 1 if p >= 0 else 0)
+        depths += depth
+        for b in bits:
+            parts = [b >> 64 * w & 2 ** 64 - 1 for w in range(words)]
+            rows.append([x - 2 ** 64 if x >> 63 else x for x in parts])
+    return (torch.tensor(rows, dtype=torch.int64).reshape(len(rows), words), torch.tensor(depths, dtype=torch.int32))
+
+
+def nvfp4_kv_tree_attention(q, cache, page_table, context_lens, query_starts, tree, max_queries=None, max_context=None,
+                            scale=None, positions=None, window=0, return_lse=False, out=None, workspace=None):
+    """nvfp4_kv_attention for drafted tokens that form trees.  A sequence's queries are the last n tokens of its
+    context; tree int64 [tokens, words] holds a bit for each draft of the query's sequence that it sees, its own
+    among them (kv_trees); the tokens before the drafts are seen by all, with window > 0 those behind positions
+    (int32 [tokens]) - window.  max_queries bounds a sequence's drafts (without it: all tokens, or as many as
+    tree has bits, may be one sequence's).  No gradient passes through the call."""
+    stream = _kv_stream(cache)
+    if stream is None:
+        with torch.cuda.device(cache.device):
+            return nvfp4_kv_tree_attention(q, cache, page_table, context_lens, query_starts, tree, max_queries, max_context,
+                                           scale, positions, window, return_lse, out, workspace)
+    L = load_library()
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"q must be [tokens, query_heads, {cache.dim}], not {tuple(shape)}")
+    tokens, query_heads, _ = shape
+    qt, qh = _kv_rows(q, "q", cache, shape)
+    table_shape, tree_shape = page_table.shape, tree.shape
+    if len(table_shape) != 2:
+        raise ValueError("page_table must be int32 [seqs, table_pages]")
+    if len(tree_shape) != 2 or tree_shape[0] != tokens:
+        raise ValueError(f"tree must be int64 [{tokens}, words]")
+    seqs, table_pages = table_shape
+    _kv_index(page_table, "page_table", cache, torch.int32, table_shape)
+    _kv_index(context_lens, "context_lens", cache, torch.int32, table_shape[:1])
+    _kv_index(query_starts, "query_starts", cache, torch.int32, (seqs + 1,))
+    _kv_index(tree, "tree", cache, torch.int64, tree_shape)
+    if positions is not None:
+        _kv_index(positions, "positions", cache, torch.int32, (tokens,))
+    if max_queries is None:
+        max_queries = max(min(tokens, 64 * tree_shape[1]), 1)
+    if max_context is None:
+        max_context = table_pages * cache.page_size
+    if scale is None:
+        scale = cache.dim ** -0.5
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=cache.device)
+    elif out.shape != shape or out.dtype is not q.dtype or out.device != cache.device or not out.is_contiguous():
+        raise ValueError("out must be contiguous and have q's shape, dtype and device")
+    lse = torch.empty((tokens, query_heads), dtype=torch.float32, device=cache.device) if return_lse else None
+    if workspace is None:
+        nbytes = _kv_attention_bytes(cache._gpu, cache.pages, cache.page_size, cache.heads, cache.dim, tokens,
+                                     query_heads, seqs, max_queries, max_context, window)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _check(L.nvfp4_kv_tree_attention(cache._struct, q.data_ptr(), _dtype_code(q, "q"), tokens, query_heads, qt, qh,
+                                     page_table.data_ptr(), seqs, table_pages, context_lens.data_ptr(),
+                                     query_starts.data_ptr(), max_queries, max_context, scale, tree.data_ptr(),
+                                     tree_shape[1], None if positions is None else positions.data_ptr(), window,
+                                     out.data_ptr(), lse.data_ptr() if return_lse else None,
+                                     workspace.data_ptr() if nbytes else None, nbytes, stream))
+    return (out, lse) if return_lse else out
+
+
 # ------------------------------------------------------------------ MLX-style names
 
 def _mode_check(group_size, bits, mode, global_scales=()):
@@ -1204,5 +1288,5 @@ __all__ = [
     "nvfp4_mx_pack", "mx_qqmm_workspace", "nvfp4_mx_qqmm", "nvfp4_mx_qqmm_packed",
     "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "MxNormed", "nvfp4_mx_rms_norm", "nvfp4_gather_qmm_indexed",
     "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "rotation_table", "nvfp4_kv_write_rotated", "nvfp4_kv_read",
-    "kv_attention_workspace", "nvfp4_kv_attention",
+    "kv_attention_workspace", "nvfp4_kv_attention", "kv_trees", "nvfp4_kv_tree_attention",
 ]

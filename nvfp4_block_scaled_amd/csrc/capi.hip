@@ -1414,14 +1414,18 @@ size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t to
   return tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
 }
 
-nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
-                                int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
-                                const int32_t* page_table, int64_t seqs, int64_t table_pages,
-                                const int32_t* context_lens, const int32_t* query_starts,
-                                int64_t max_queries, int64_t max_context, float scale, int causal,
-                                int64_t window, void* out, float* lse, void* workspace,
-                                size_t workspace_bytes, hipStream_t stream) {
-  const char* op = "kv_attention";
+// Both attention calls; `tree` is null for queries at consecutive positions.
+struct TreeArgs {
+  const uint64_t* masks;
+  int64_t words;
+  const int32_t* positions;
+};
+static nvfp4_status attend(const char* op, const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
+                           int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
+                           const int32_t* page_table, int64_t seqs, int64_t table_pages,
+                           const int32_t* context_lens, const int32_t* query_starts, int64_t max_queries,
+                           int64_t max_context, float scale, int causal, int64_t window, const TreeArgs* tree,
+                           void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   nvfp4::KvCache c;
   nvfp4::KvAttention a{};
   if (nvfp4_status st = check_kv(op, cache, dt, tokens, &c)) return st;
@@ -1429,34 +1433,44 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
           check_kv_attention(op, c, tokens, query_heads, seqs, max_queries, max_context, window, &a))
     return st;
   if (!(scale > 0.0f) || scale > 3.0e38f)
-    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] scale must be positive and finite.");
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] scale must be positive and finite.", op);
   if (window > 0 && !causal)
-    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] a window needs causal attention.");
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] a window needs causal attention.", op);
   if (q_token_stride < 0 || q_head_stride < 0)
-    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] strides must be >= 0.");
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] strides must be >= 0.", op);
   if (table_pages < 0 || table_pages > INT32_MAX || max_context > table_pages * c.page_size)
     return fail(NVFP4_ERR_INVALID_ARGUMENT,
-                "[kv_attention] max_context (%lld) must be at most table_pages * page_size.",
+                "[%s] max_context (%lld) must be at most table_pages * page_size.", op,
                 (long long)max_context);
   if (!query_starts && (tokens != seqs || max_queries != 1))
     return fail(NVFP4_ERR_INVALID_ARGUMENT,
-                "[kv_attention] without query_starts every sequence has one query: tokens must equal seqs "
-                "and max_queries 1.");
+                "[%s] without query_starts every sequence has one query: tokens must equal seqs "
+                "and max_queries 1.", op);
+  if (tree) {
+    if (!query_starts) return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] query_starts must not be NULL.", op);
+    if (tree->words <= 0 || tree->words > (INT32_MAX >> 6) || tree->words * 64 < max_queries)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tree_words (%lld) must hold a bit for each of max_queries (%lld).", op,
+                  (long long)tree->words, (long long)max_queries);
+    if (tokens > 0 && (!tree->masks || (window > 0 && !tree->positions)))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tree, and with a window positions, must not be NULL.", op);
+    if (!aligned(tree->masks, 8) || !aligned(tree->positions, 4))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tree must be 8-byte, positions 4-byte aligned.", op);
+  }
   const StreamDevice on(stream);
   const size_t need = tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
   if (tokens > 0 && seqs > 0) {
     if (!q || !out || !context_lens || (max_context > 0 && !page_table))
       return fail(NVFP4_ERR_INVALID_ARGUMENT,
-                  "[kv_attention] q, page_table, context_lens and out must not be NULL.");
+                  "[%s] q, page_table, context_lens and out must not be NULL.", op);
     if (!aligned(q, dtype_size(dt)) || !aligned(out, 16) || !aligned(page_table, 4) ||
         !aligned(context_lens, 4) || !aligned(query_starts, 4) || !aligned(lse, 4))
       return fail(NVFP4_ERR_INVALID_ARGUMENT,
-                  "[kv_attention] out must be 16-byte aligned, the others to their elements.");
+                  "[%s] out must be 16-byte aligned, the others to their elements.", op);
     if (need > 0 && (!workspace || workspace_bytes < need))
-      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] workspace of %zu bytes is smaller than %zu.",
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] workspace of %zu bytes is smaller than %zu.", op,
                   workspace ? workspace_bytes : (size_t)0, need);
     if (need > 0 && !aligned(workspace, 256))
-      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[kv_attention] workspace must be 256-byte aligned.");
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] workspace must be 256-byte aligned.", op);
   }
   if (nvfp4_status st = check_device(op, stream)) return st;
   if (tokens == 0 || seqs == 0) return ok();
@@ -1471,7 +1485,37 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
   a.scale = scale;
   a.causal = causal != 0;
   a.table_stride = table_pages;
-  return launched(op, nvfp4::launch_kv_attention(c, a, dt, workspace, stream));
+  if (!tree) return launched(op, nvfp4::launch_kv_attention(c, a, dt, workspace, stream));
+  a.tree = tree->masks;
+  a.tree_words = (int)tree->words;
+  a.positions = tree->positions;
+  return launched(op, nvfp4::launch_kv_tree_attention(c, a, dt, workspace, stream));
 }
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
+                                int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
+                                const int32_t* page_table, int64_t seqs, int64_t table_pages,
+                                const int32_t* context_lens, const int32_t* query_starts,
+                                int64_t max_queries, int64_t max_context, float scale, int causal,
+                                int64_t window, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  return attend("kv_attention", cache, q, dt, tokens, query_heads, q_token_stride, q_head_stride, page_table, seqs,
+                table_pages, context_lens, query_starts, max_queries, max_context, scale, causal, window, nullptr, out,
+                lse, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_kv_tree_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
+                                     int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
+                                     const int32_t* page_table, int64_t seqs, int64_t table_pages,
+                                     const int32_t* context_lens, const int32_t* query_starts,
+                                     int64_t max_queries, int64_t max_context, float scale, const uint64_t* tree,
+                                     int64_t tree_words, const int32_t* positions, int64_t window, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const TreeArgs t{tree, tree_words, positions};
+  return attend("kv_tree_attention", cache, q, dt, tokens, query_heads, q_token_stride, q_head_stride, page_table, seqs,
+                table_pages, context_lens, query_starts, max_queries, max_context, scale, 1, window, &t, out, lse,
+                workspace, workspace_bytes, stream);
+}
+
 
 }  // extern "C"

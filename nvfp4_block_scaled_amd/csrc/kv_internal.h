@@ -40,8 +40,14 @@ struct KvAttention {
   int seqs, query_heads, groups, max_queries, max_keys, causal, window;
   KvDiv group_div;              // by groups
   int64_t table_stride, tokens;
+  // drafted tokens (launch_kv_tree_attention): masks [tokens, tree_words], and
+  // with a window their positions [tokens]
+  const uint64_t* tree;
+  const int32_t* positions;
+  int tree_words;
 };
 size_t kv_attention_workspace(const KvCache& c, const KvAttention& a);
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s);
+hipError_t launch_kv_tree_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s);
 
 }  // namespace nvfp4
