@@ -638,6 +638,49 @@ nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* 
                                void* sum, void* normed, uint8_t* codes, uint8_t* scales,
                                hipStream_t stream);
 
+/*
+ * nvfp4_moe -- a whole mixture-of-experts layer for a few tokens (a decoding
+ * step; many tokens are nvfp4_gather_qmm's): router, gated expert products on
+ * NVFP4 weights, and their weighted sum.  For every token t, with x as given:
+ *     l_e = x . router_e                    products and sums in float64
+ *     expert_idx[t]: the top_k experts with the largest l, the largest first;
+ *         of equal ones the lower index (a NaN counts as the smallest)
+ *     expert_weights[t]: softmax of the chosen l (normalize), or the chosen
+ *         ones' share of the softmax of all l
+ *     g = x . gate_up_hat[e, i], u = x . gate_up_hat[e, f + i],
+ *     h_i = g / (1 + exp(-g)) * u                                   (i < f)
+ *     out[t] = T( sum_j expert_weights[t, j] * down_hat[e_j] h )
+ * float32 sums of exact products before the global scales (float32 x loses
+ * nothing, h 2^-16 of itself for 16-bit types), one rounding to T.  Sums in
+ * front of the global scale must stay below float32's largest number.
+ *   x              device [t, k] of type dt, 16-byte aligned
+ *   router         device [e, k] of type dt, 16-byte aligned; or NULL:
+ *                  expert_idx and expert_weights are given, and an index
+ *                  outside [0, e) names no expert.  An expert may stand twice
+ *                  among a token's
+ *   expert_idx     device int32 [t, top_k], written (read without a router)
+ *   expert_weights device float [t, top_k], likewise
+ *   gate_up_codes  device uint8 [e, 2 f, k/2]: each expert's gate rows, then its
+ *                  up rows; gate_up_scales uint8 [e, 2 f, k/16]
+ *   down_codes     device uint8 [e, k, f/2]; down_scales uint8 [e, k, f/16]
+ *   global_scale_* device float [e], or NULL
+ *   out            device [t, k] of type dt, 16-byte aligned; zeros for a token
+ *                  without an expert.  May not overlap x
+ *   workspace      device, nvfp4_moe_workspace_size() bytes, 256-byte aligned
+ * Codes 16-byte aligned.
+ * Errors: bad dtype, t < 0 (t = 0 is a no-op), e, top_k, k or f not positive,
+ * k or f no multiple of 16, top_k > e, NULL or misaligned pointers, workspace
+ * too small; UNSUPPORTED for more than 64 tokens, top_k > 32, e > 1024, k or f
+ * of 2^20 or more, min(t * top_k, e) * f / 16 of 2^24 or more.
+ */
+size_t nvfp4_moe_workspace_size(nvfp4_dtype dt, int64_t t, int64_t top_k, int64_t e, int64_t k, int64_t f);
+nvfp4_status nvfp4_moe(const void* x, nvfp4_dtype dt, const void* router, int32_t* expert_idx,
+                       float* expert_weights, int normalize, const uint8_t* gate_up_codes,
+                       const uint8_t* gate_up_scales, const float* global_scale_gate_up,
+                       const uint8_t* down_codes, const uint8_t* down_scales,
+                       const float* global_scale_down, int64_t t, int64_t top_k, int64_t e, int64_t k,
+                       int64_t f, void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ---------------------------------------------------------------- key/value cache
  *
  * A paged cache of keys and values held in NVFP4, and attention over it.

@@ -23,6 +23,8 @@ The functions carry the C entry points' names (see include/nvfp4.h):
                                                       (the mxfp4 / mxfp8 modes)
     nvfp4_mx_rms_norm(x, weight, mode, residual, ...) -> MxNormed
                                                       (norm with residual, its output encoded)
+    nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router, top_k, ...)
+                                                      (an expert layer for a few tokens) -> (out, experts, weights)
     KVCache(...), kv_cache(pages, page_size, heads, dim, ...)
                                                       (a paged key/value cache held in NVFP4)
     nvfp4_kv_write(cache, k, v, slots)                (quantize tokens into their slots)
@@ -117,6 +119,8 @@ def load_library():
         "nvfp4_mx_qqmm_packed": (I, [P, I, I, P, P, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_gather_qmm": (I, [P, I, I, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_mx_rms_norm": (I, [P, P, P, I, I, I64, I64, ctypes.c_double, I, P, P, P, P, P]),
+        "nvfp4_moe_workspace_size": (SZ, [I, I64, I64, I64, I64, I64]),
+        "nvfp4_moe": (I, [P, I, P, P, P, I, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
         "nvfp4_kv_write": (I, [C, P, P, I, I64, I64, I64, I64, I64, P, P]),
         "nvfp4_kv_write_rotated": (I, [C, P, P, I, I64, I64, I64, I64, I64, P, P, P, I64, I64, I, P, I64, I64, I64,
                                        P, P]),
@@ -823,6 +827,90 @@ def nvfp4_mx_rms_norm(x, weight=None, mode="mxfp8", residual=None, eps=1e-6, pac
     return MxNormed(out, x if total is None else total, y)
 
 
+# ------------------------------------------------------------------ expert layer
+
+@functools.lru_cache(maxsize=4096)
+def _moe_bytes(*sizes):
+    return load_library().nvfp4_moe_workspace_size(*sizes)
+
+
+def moe_workspace(t, top_k, e, k, f, dtype, device):
+    """(workspace, bytes) for nvfp4_moe calls of these sizes."""
+    nbytes = _moe_bytes(_DT[dtype], t, top_k, e, k, f)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device), nbytes
+
+
+def nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router=None, top_k=None,
+              global_scale_gate_up=None, global_scale_down=None, normalize=True, expert_idx=None, expert_weights=None,
+              out=None, workspace=None):
+    """A mixture-of-experts layer for a few tokens x [t, k] (at most 64): the
+    top_k experts by x @ router^T (router [e, k] of x's type; sums in float64,
+    of equal ones the lower index), their softmax weights (normalize: over the
+    chosen ones, else over all), the gated products silu(x W_gate^T) * (x
+    W_up^T) with gate_up [e, 2 f, k] (gate rows, then up rows), and the
+    weighted sum of the products with down [e, k, f]; weights in NVFP4.
+    Without a router expert_idx (int32 [t, top_k]; outside [0, e): none) and
+    expert_weights (float32) say who takes part; with one they are what to
+    write to.  No gradient passes through the call.
+    Returns (out [t, k], expert_idx, expert_weights)."""
+    L = load_library()
+    _dev(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [t, k]")
+    code, device = _dtype_code(x, "x"), x.device
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router, top_k, global_scale_gate_up,
+                             global_scale_down, normalize, expert_idx, expert_weights, out, workspace)
+    t, k = x.shape
+    shape = gate_up_codes.shape
+    if len(shape) != 3 or shape[1] % 2:
+        raise ValueError("gate_up_codes must be uint8 [e, 2 f, k/2]")
+    e, f = shape[0], shape[1] // 2
+    for w, name, want in ((gate_up_codes, "gate_up_codes", (e, 2 * f, k // 2)), (gate_up_scales, "gate_up_scales", (e, 2 * f, k // 16)),
+                          (down_codes, "down_codes", (e, k, f // 2)), (down_scales, "down_scales", (e, k, f // 16))):
+        if w.dtype is not torch.uint8 or w.shape != want or w.device != device or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 {want} on x's device, not {w.dtype} {tuple(w.shape)}")
+    g_up, g_down = _gscale(global_scale_gate_up, "global_scale_gate_up", e), _gscale(global_scale_down, "global_scale_down", e)
+    if any(g is not None and g.device != device for g in (g_up, g_down)):
+        raise ValueError("the global scales must be on x's device")
+    if router is not None:
+        if router.dtype is not x.dtype or router.shape != (e, k) or router.device != device or not router.is_contiguous():
+            raise ValueError(f"router must be a contiguous {x.dtype} {(e, k)} on x's device")
+        if top_k is None:
+            if expert_idx is None:
+                raise ValueError("top_k is needed with a router")
+            top_k = expert_idx.shape[-1]
+    else:
+        if expert_idx is None or expert_weights is None:
+            raise ValueError("without a router expert_idx and expert_weights are needed")
+        if top_k is None:
+            top_k = expert_idx.shape[-1]
+    if expert_idx is None:
+        expert_idx = torch.empty((t, top_k), dtype=torch.int32, device=device)
+    if expert_weights is None:
+        expert_weights = torch.empty((t, top_k), dtype=torch.float32, device=device)
+    for w, name, dtype in ((expert_idx, "expert_idx", torch.int32), (expert_weights, "expert_weights", torch.float32)):
+        if w.dtype is not dtype or w.shape != (t, top_k) or w.device != device or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} {(t, top_k)} on x's device")
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.dtype is not x.dtype or out.shape != x.shape or out.device != device or not out.is_contiguous():
+        raise ValueError("out must be contiguous and have x's shape, dtype and device")
+    if workspace is None:
+        workspace, nbytes = moe_workspace(t, top_k, e, k, f, x.dtype, device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on x's device")
+    _check(L.nvfp4_moe(x.data_ptr(), code, None if router is None else router.data_ptr(), expert_idx.data_ptr(),
+                       expert_weights.data_ptr(), int(bool(normalize)), gate_up_codes.data_ptr(), gate_up_scales.data_ptr(),
+                       None if g_up is None else g_up.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(),
+                       None if g_down is None else g_down.data_ptr(), t, top_k, e, k, f, out.data_ptr(), workspace.data_ptr(),
+                       nbytes, torch.cuda.current_stream().cuda_stream))
+    return out, expert_idx, expert_weights
+
+
 # ------------------------------------------------------------------ key/value cache
 
 _KV_HELD = ("k_codes", "k_scales", "v_codes", "v_scales", "global_scale_k", "global_scale_v")
@@ -1286,7 +1374,7 @@ __all__ = [
     "qqmm_workspace", "gather_workspace", "quantize", "dequantize", "qqmm", "gather_qmm",
     "MX_MODES", "MxPacked", "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_quant_dequant",
     "nvfp4_mx_pack", "mx_qqmm_workspace", "nvfp4_mx_qqmm", "nvfp4_mx_qqmm_packed",
-    "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "MxNormed", "nvfp4_mx_rms_norm", "nvfp4_gather_qmm_indexed",
+    "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "MxNormed", "nvfp4_mx_rms_norm", "moe_workspace", "nvfp4_moe", "nvfp4_gather_qmm_indexed",
     "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "rotation_table", "nvfp4_kv_write_rotated", "nvfp4_kv_read",
     "kv_attention_workspace", "nvfp4_kv_attention", "kv_trees", "nvfp4_kv_tree_attention",
 ]

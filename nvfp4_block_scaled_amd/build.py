@@ -18,7 +18,7 @@ CEILING_LIB = os.path.join(HERE, "libnvfp4_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["codec.hip", "qmv.hip", "qmv_packed.hip", "gemm.hip", "smallm.hip", "mx_codec.hip", "mx_gemm.hip", "mx_qmv.hip", "gather_ex.hip", "kv_cache.hip",
-           "kv_attention.hip", "kv_tree_attention.hip", "mx_norm.hip", "kv_rotate.hip", "capi.hip"]
+           "kv_attention.hip", "kv_tree_attention.hip", "mx_norm.hip", "kv_rotate.hip", "moe.hip", "capi.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [

@@ -1233,6 +1233,84 @@ nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* 
   return launched(op, nvfp4::launch_mx_norm(n, dt, mode, stream));
 }
 
+// ------------------------------------------------------------------ expert layer
+
+static nvfp4_status check_moe(const char* op, nvfp4_dtype dt, int64_t t, int64_t top_k, int64_t e, int64_t k, int64_t f) {
+  if (!dtype_ok(dt))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "[%s] Unsupported dtype code %d (float32, float16 and bfloat16 only).", op, (int)dt);
+  if (t < 0 || top_k <= 0 || e <= 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] top_k and e must be positive, t >= 0.", op);
+  if (top_k > e)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] top_k (%lld) must be at most e (%lld).", op, (long long)top_k, (long long)e);
+  if (nvfp4_status st = check_k(op, k)) return st;
+  if (nvfp4_status st = check_k(op, f)) return st;
+  if (t > nvfp4::kMoeMaxTokens || top_k > nvfp4::kMoeMaxTopK || e > nvfp4::kMoeMaxExperts)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] More than %d tokens, %d experts a token or %d experts.", op,
+                nvfp4::kMoeMaxTokens, nvfp4::kMoeMaxTopK, nvfp4::kMoeMaxExperts);
+  if (k >= 1 << 20 || f >= 1 << 20 || (t * top_k < e ? t * top_k : e) * (f / 16) >= 1 << 24)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large.", op);
+  return NVFP4_OK;
+}
+
+size_t nvfp4_moe_workspace_size(nvfp4_dtype dt, int64_t t, int64_t top_k, int64_t e, int64_t k, int64_t f) {
+  if (check_moe("moe_workspace_size", dt, t, top_k, e, k, f)) return 0;
+  return t == 0 ? 0 : nvfp4::moe_workspace(t, top_k, e, k, f, dt);
+}
+
+nvfp4_status nvfp4_moe(const void* x, nvfp4_dtype dt, const void* router, int32_t* expert_idx,
+                       float* expert_weights, int normalize, const uint8_t* gate_up_codes,
+                       const uint8_t* gate_up_scales, const float* global_scale_gate_up,
+                       const uint8_t* down_codes, const uint8_t* down_scales,
+                       const float* global_scale_down, int64_t t, int64_t top_k, int64_t e, int64_t k,
+                       int64_t f, void* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* op = "moe";
+  if (nvfp4_status st = check_moe(op, dt, t, top_k, e, k, f)) return st;
+  if (t > 0) {
+    CHECK_PTR("moe", x);
+    CHECK_PTR("moe", expert_idx);
+    CHECK_PTR("moe", expert_weights);
+    CHECK_PTR("moe", gate_up_codes);
+    CHECK_PTR("moe", gate_up_scales);
+    CHECK_PTR("moe", down_codes);
+    CHECK_PTR("moe", down_scales);
+    CHECK_PTR("moe", out);
+    if (!aligned(x, 16) || !aligned(router, 16) || !aligned(gate_up_codes, 16) || !aligned(down_codes, 16) || !aligned(out, 16))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[moe] x, router, codes and out must be 16-byte aligned.");
+    if (!aligned(expert_idx, 4) || !aligned(expert_weights, 4) || !aligned(global_scale_gate_up, 4) ||
+        !aligned(global_scale_down, 4))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[moe] indices, weights and global scales must be 4-byte aligned.");
+    const size_t need = nvfp4::moe_workspace(t, top_k, e, k, f, dt);
+    if (!workspace || workspace_bytes < need)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[moe] workspace of %zu bytes is smaller than %zu.",
+                  workspace ? workspace_bytes : (size_t)0, need);
+    if (!aligned(workspace, 256))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "[moe] workspace must be 256-byte aligned.");
+  }
+  if (nvfp4_status st = check_device(op, stream)) return st;
+  if (t == 0) return ok();
+  const StreamDevice on(stream);
+  nvfp4::MoeLayer a{};
+  a.x = x;
+  a.router = router;
+  a.expert_idx = expert_idx;
+  a.expert_weights = expert_weights;
+  a.up_codes = gate_up_codes;
+  a.up_scales = gate_up_scales;
+  a.down_codes = down_codes;
+  a.down_scales = down_scales;
+  a.up_global = global_scale_gate_up;
+  a.down_global = global_scale_down;
+  a.out = out;
+  a.tokens = (int)t;
+  a.top_k = (int)top_k;
+  a.experts = (int)e;
+  a.k = (int)k;
+  a.f = (int)f;
+  a.normalize = normalize != 0;
+  return launched(op, nvfp4::launch_moe(a, dt, workspace, stream));
+}
+
 // ------------------------------------------------------------------ key/value cache
 
 static nvfp4_status check_kv(const char* op, const nvfp4_kv_cache* cache, nvfp4_dtype dt, int64_t tokens,

@@ -1,6 +1,6 @@
 // layer_internal.h -- host-side launch functions of a decoder layer's other
-// operators: the norm that encodes its output (mx_norm.hip) and the rotation on
-// the way into the cache (kv_rotate.hip).  Apart from nvfp4_internal.h, as
+// operators: the norm that encodes its output (mx_norm.hip), the rotation on the
+// way into the cache (kv_rotate.hip) and the expert layer (moe.hip).  Apart from nvfp4_internal.h, as
 // kv_internal.h is.
 #pragma once
 
@@ -36,5 +36,23 @@ struct KvRotate {
   KvDiv piece_div;
 };
 hipError_t launch_kv_rotate(const KvCache& c, KvRotate a, int dt, hipStream_t s);
+
+constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 32, kMoeMaxExperts = 1024;
+constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
+struct MoeLayer {
+  const void *x, *router;  // [tokens, k], [experts, k]; router null: idx and weights are given
+  int32_t* expert_idx;     // [tokens, top_k], with their weights
+  float* expert_weights;
+  const uint8_t *up_codes, *up_scales;      // [experts, 2 f, k]: gate rows, then up rows
+  const uint8_t *down_codes, *down_scales;  // [experts, k, f]
+  const float *up_global, *down_global;     // [experts] or null
+  void* out;                                // [tokens, k]
+  int tokens, top_k, experts, k, f, normalize;  // k and f multiples of 16, below 2^20
+  // in the workspace, set by the launch
+  double* logits;                 // [tokens, experts]
+  uint16_t *x_pieces, *h_pieces;  // [pieces][tokens, k], [pieces][tokens * top_k, f]
+};
+size_t moe_workspace(int64_t tokens, int64_t top_k, int64_t experts, int64_t k, int64_t f, int dt);
+hipError_t launch_moe(MoeLayer a, int dt, void* workspace, hipStream_t s);
 
 }  // namespace nvfp4
