@@ -32,6 +32,9 @@ constexpr int kUnit = 256;  // inner values of a row that a wave takes at a time
 
 // ----------------------------------------------------------------- pieces
 
+constexpr int moe_x_pieces(int dt) { return dt == kF32 ? 3 : dt == kF16 ? 2 : 1; }
+constexpr int moe_h_pieces(int dt) { return dt == kF32 ? 3 : 2; }
+
 // v as N bfloat16 whose sum it is (up to 2^-8N of it): the leading bits of what
 // is left, the last one rounded.  An infinity stays in the first alone.
 template <int N>
@@ -46,6 +49,19 @@ __device__ __forceinline__ void moe_pieces(float v, uint16_t (&p)[N]) {
   }
 }
 
+// Where x and h lie in the workspace: per row the units of 256 values, of each
+// the 8 steps of a product in turn, of a step the pieces, and of a piece the 8
+// values of each quarter of a wave (values 64 quarter + 8 step .. of the unit).
+// So the four quarters' loads of a column are one line's 64 bytes; as the values
+// themselves lie they were four lines, and these loads took as long as the
+// weights' (16 tokens, 2 of 8 experts of 4096 x 14336: down products 262 us).
+__host__ __device__ constexpr int64_t moe_row(int inner, int pieces) {
+  return (int64_t)((inner + kUnit - 1) / kUnit) * kUnit * pieces;
+}
+__device__ __forceinline__ int moe_place(int at, int pieces) {  // of the first piece of the 8 values from `at` on
+  return ((at / kUnit * 8 + (at & 63) / 8) * pieces) * 32 + (at & (kUnit - 1)) / 64 * 8;
+}
+
 // ----------------------------------------------------------------- router
 
 __device__ __forceinline__ double moe_wave_sum(double v) {
@@ -54,55 +70,67 @@ __device__ __forceinline__ double moe_wave_sum(double v) {
   return v;
 }
 
-constexpr int kRouterTokens = 4;  // of a wave: the expert's row is loaded once for them
-
-// Workgroups 0 .. routers - 1: logits, a wave an expert and up to four tokens.  The
-// others cut x into pieces (PX > 1).
-template <int DT, int PX>
+// Workgroups 0 .. routers - 1: logits, a workgroup an expert and TOKENS tokens, for
+// which its row is loaded once.  The others lay x out in pieces.
+template <int DT, int PX, int TOKENS>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeLayer a, int routers) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int)blockIdx.x >= routers) {
-    if constexpr (PX > 1) {
-      const int64_t all = (int64_t)a.tokens * a.k;
-      const int64_t h = ((int64_t)(blockIdx.x - routers) * 256 + threadIdx.x);
-      if (h >= all / 8) return;
-      float v[8];
-      load8x<DT>(a.x, h, v);
-      uint16_t p[8][PX];
+    // with zeros behind the end of a row, as weights behind it are 0 and 0 times anything else might be NaN
+    constexpr int PH = moe_h_pieces(DT);
+    const int per_row = (int)moe_row(a.k, 1) / 8, more = (int)moe_row(a.f, 1) - a.f;
+    int h = (int)(blockIdx.x - routers) * 256 + threadIdx.x;
+    if (h >= a.tokens * per_row) {
+      h -= a.tokens * per_row;
+      if (more == 0 || h >= a.tokens * a.top_k * (more / 8)) return;
+      const int p = h / (more / 8), at = a.f + 8 * (h - p * (more / 8));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) moe_pieces<PX>(v[i], p[i]);
+      for (int j = 0; j < PH; ++j)
+        *reinterpret_cast<u32x4*>(a.h_pieces + p * moe_row(a.f, PH) + moe_place(at, PH) + 32 * j) = u32x4{0u, 0u, 0u, 0u};
+      return;
+    }
+    const int t = h / per_row, at = 8 * (h - t * per_row);
+    float v[8] = {};
+    if (at < a.k) load8x<DT>(a.x, (int64_t)t * (a.k / 8) + at / 8, v);
+    uint16_t p[8][PX];
 #pragma unroll
-      for (int j = 0; j < PX; ++j) {
-        u32x4 w;
+    for (int i = 0; i < 8; ++i) moe_pieces<PX>(v[i], p[i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = p[2 * i][j] | (uint32_t)p[2 * i + 1][j] << 16;
-        *reinterpret_cast<u32x4*>(a.x_pieces + j * all + 8 * h) = w;
-      }
+    for (int j = 0; j < PX; ++j) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = p[2 * i][j] | (uint32_t)p[2 * i + 1][j] << 16;
+      *reinterpret_cast<u32x4*>(a.x_pieces + t * moe_row(a.k, PX) + moe_place(at, PX) + 32 * j) = w;
     }
     return;
   }
-  const int chunks = (a.tokens + kRouterTokens - 1) / kRouterTokens;
-  const int job = blockIdx.x * 4 + wave;
-  const int expert = job / chunks, t0 = job % chunks * kRouterTokens;
-  if (expert >= a.experts) return;
-  double sum[kRouterTokens] = {};
-  const int64_t row = (int64_t)expert * (a.k / 8);
-  for (int i = lane; i < a.k / 8; i += 64) {
+  __shared__ double part[4][TOKENS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int chunks = (a.tokens + TOKENS - 1) / TOKENS;
+  const int expert = blockIdx.x / chunks, t0 = (blockIdx.x - expert * chunks) * TOKENS;
+  double sum[TOKENS] = {};
+  const int pieces = a.k / 8;
+  const int64_t row = (int64_t)expert * pieces;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < pieces; i += 256) {
     float w[8];
     load8x<DT>(a.router, row + i, w);
 #pragma unroll
-    for (int j = 0; j < kRouterTokens; ++j) {
+    for (int j = 0; j < TOKENS; ++j) {
       float v[8];
-      load8x<DT>(a.x, (int64_t)min(t0 + j, a.tokens - 1) * (a.k / 8) + i, v);
+      load8x<DT>(a.x, (int64_t)min(t0 + j, a.tokens - 1) * pieces + i, v);
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[j] = __builtin_fma((double)w[c], (double)v[c], sum[j]);
     }
   }
 #pragma unroll
-  for (int j = 0; j < kRouterTokens; ++j) {
-    const double s = moe_wave_sum(sum[j]);
-    if (lane == 0 && t0 + j < a.tokens) a.logits[(int64_t)(t0 + j) * a.experts + expert] = s;
+  for (int j = 0; j < TOKENS; ++j) {
+    const double x = moe_wave_sum(sum[j]);
+    if (lane == 0) part[wave][j] = x;
   }
+  __syncthreads();
+  if (threadIdx.x < TOKENS && t0 + threadIdx.x < a.tokens)
+    a.logits[(int64_t)(t0 + threadIdx.x) * a.experts + expert] =
+        (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
 }
 
 // An order of the logits as whole numbers; a NaN is below all.
@@ -130,19 +158,19 @@ __global__ void __launch_bounds__(256) moe_choose_kernel(MoeLayer a) {
   }
   __syncthreads();
   const double top = l[chosen[0]];
-  double sum = 0.0;
-  if (a.normalize) {
-    for (int j = 0; j < a.top_k; ++j) sum += exp(l[chosen[j]] - top);
-  } else {
+  const double mine = threadIdx.x < a.top_k ? exp(l[chosen[threadIdx.x]] - top) : 0.0;
+  double sum = mine;
+  if (!a.normalize) {
+    sum = 0.0;
     for (int i = threadIdx.x; i < a.experts; i += 256) sum += exp(l[i] - top);
-    sum = moe_wave_sum(sum);
-    if (lane == 0) part[wave] = sum;
-    __syncthreads();
-    sum = part[0] + part[1] + part[2] + part[3];
   }
-  for (int j = threadIdx.x; j < a.top_k; j += 256) {
-    a.expert_idx[t * a.top_k + j] = chosen[j];
-    a.expert_weights[t * a.top_k + j] = (float)(exp(l[chosen[j]] - top) / sum);
+  sum = moe_wave_sum(sum);
+  if (lane == 0) part[wave] = sum;
+  __syncthreads();
+  sum = (part[0] + part[1]) + (part[2] + part[3]);
+  if (threadIdx.x < a.top_k) {
+    a.expert_idx[t * a.top_k + threadIdx.x] = chosen[threadIdx.x];
+    a.expert_weights[t * a.top_k + threadIdx.x] = (float)(mine / sum);
   }
 }
 
@@ -190,22 +218,32 @@ __device__ __forceinline__ int moe_pair(const MoeLayer& a, const MoeLists& s, in
 
 // ----------------------------------------------------------------- products
 
-// 64 consecutive inner values of one row, as loaded: 4 groups of 16.
+// 64 consecutive inner values of one row, as loaded: 4 groups of 16.  WHOLE: rows
+// are whole 64s; then a lane past a row's end loads the row's beginning, and no
+// branch stands between the loads.  Scales past the end are 0, and so are weights.
 struct MoeWeights {
   uint32_t w[8], s;
 };
+template <bool WHOLE>
 __device__ __forceinline__ MoeWeights moe_load(const uint8_t* codes, const uint8_t* scales, int64_t row, int inner, int at) {
   MoeWeights r;
-  const uint8_t* c = codes + row * (inner / 2) + at / 2;
-  const uint8_t* s = scales + row * (inner / 16) + at / 16;
-  if (at + 64 <= inner) {
-    const u32x4_8 x = *reinterpret_cast<const u32x4_8*>(c), y = *reinterpret_cast<const u32x4_8*>(c + 16);
+  const int from = WHOLE && at >= inner ? 0 : at;
+  const uint8_t* c = codes + row * (inner / 2) + from / 2;
+  const uint8_t* s = scales + row * (inner / 16) + from / 16;
+  if (WHOLE || at + 64 <= inner) {
+    const u32x4_8 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c));
+    const u32x4_8 y = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + 16));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       r.w[i] = x[i];
       r.w[4 + i] = y[i];
     }
-    __builtin_memcpy(&r.s, s, 4);
+    if constexpr (WHOLE) {
+      r.s = *reinterpret_cast<const uint32_t*>(s);
+      if (at >= inner) r.s = 0u;
+    } else {
+      __builtin_memcpy(&r.s, s, 4);
+    }
   } else {
     r.s = 0u;
 #pragma unroll
@@ -231,53 +269,65 @@ __device__ __forceinline__ bf16x8 moe_decode8(uint32_t w, float s) {
     r[i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1] * s), __float_as_uint(v[2 * i] * s), 0x07060302u);
   return __builtin_bit_cast(bf16x8, r);
 }
-template <int I>
-__device__ __forceinline__ bf16x8 moe_values(const MoeWeights& r) {
-  return moe_decode8(r.w[I], e4m3_decode_byte<I / 2>(r.s));
-}
-
-// 8 values of a column from element `at` on, zeros past `inner` and of columns that are not there.
-__device__ __forceinline__ bf16x8 moe_column(const uint16_t* p, int at, int inner, bool live) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (live && at < inner) v = *reinterpret_cast<const u32x4*>(p + at);
-  return __builtin_bit_cast(bf16x8, v);
+__device__ __forceinline__ bf16x8 moe_values(const MoeWeights& r, int i) {
+  return moe_decode8(r.w[i], e4m3_decode(r.s >> (8 * (i >> 1))));
 }
 
 // One unit: NR tiles of 16 rows by MT tiles of 16 tokens.  Lane l has row l % 16
-// and inner values 64 (l / 16) .. of the unit on both sides.
-template <int NR, int MT, int P>
-__device__ __forceinline__ void moe_unit(const MoeWeights (&w)[NR], const uint16_t* const (&col)[MT], const bool (&live)[MT],
-                                         int64_t plane, int at, int inner, f32x4 (&acc)[NR][MT]) {
-  auto step = [&](auto index) {
-    constexpr int I = decltype(index)::value;
-    bf16x8 a[NR];
+// and inner values 64 (l / 16) .. of the unit on both sides.  `col`: this lane's
+// column of each tile, at its quarter's values of the unit's first step.
+//
+// `ahead` loads the weights of a later unit.  Loads come back in the order of
+// their issue, so it is called behind the unit's last loads of columns: ahead of
+// them, waiting for those (in a cache) would wait for weights from memory too.
+template <int NR, int MT, int P, typename F>
+__device__ __forceinline__ void moe_unit(const MoeWeights (&w)[NR], const uint16_t* const (&col)[MT], int unit,
+                                         f32x4 (&acc)[NR][MT], F ahead) {
+  constexpr int H = MT * P <= 2 ? 8 : MT * P <= 4 ? 4 : 2;  // steps whose columns are loaded at a time
 #pragma unroll
-    for (int r = 0; r < NR; ++r) a[r] = moe_values<I>(w[r]);
+  for (int c = 0; c < 8 / H; ++c) {
+    bf16x8 b[H][MT][P];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < H; ++i)
 #pragma unroll
-      for (int p = P - 1; p >= 0; --p) {  // the small pieces first
-        const bf16x8 b = moe_column(col[m] + p * plane, at + 8 * I, inner, live[m]);
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < NR; ++r) acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r], b, acc[r][m], 0, 0, 0);
-      }
-  };
-  step(std::integral_constant<int, 0>{});
-  step(std::integral_constant<int, 1>{});
-  step(std::integral_constant<int, 2>{});
-  step(std::integral_constant<int, 3>{});
-  step(std::integral_constant<int, 4>{});
-  step(std::integral_constant<int, 5>{});
-  step(std::integral_constant<int, 6>{});
-  step(std::integral_constant<int, 7>{});
+        for (int p = 0; p < P; ++p)
+          b[i][m][p] = *reinterpret_cast<const bf16x8*>(col[m] + (unit * 8 + c * H + i) * P * 32 + p * 32);
+    __builtin_amdgcn_sched_barrier(0);
+    if (c + 1 == 8 / H) {
+      ahead();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      bf16x8 a[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) a[r] = moe_values(w[r], c * H + i);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int p = P - 1; p >= 0; --p)  // the small pieces first
+#pragma unroll
+          for (int r = 0; r < NR; ++r) acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r], b[i][m][p], acc[r][m], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+// The row that a column without a token reads instead: the first one that has
+// (no line more); its sums are not looked at.  0 if none has.
+__device__ __forceinline__ int moe_instead(int row, bool live) {
+  const uint64_t lanes = __ballot(live);
+  const int other = lanes ? __builtin_amdgcn_readlane(row, __builtin_ctzll(lanes)) : 0;
+  return live ? row : other;
 }
 
 constexpr int kUpWaves = 4;
 
-// 16 gate rows and the 16 up rows that go with them, of one expert: a workgroup, its waves
-// each a share of the inner values.
-template <int MT, int PX, int PH>
-__global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a, const uint16_t* x, int64_t x_plane) {
+// 16 gate rows and the 16 up rows that go with them, of one expert: a workgroup,
+// its waves each a share of the inner values.
+template <int MT, int PX, int PH, bool WHOLE>
+__global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a) {
   __shared__ MoeLists lists;
   __shared__ f32x4 part[kUpWaves][2][MT][64];
   moe_lists(a, lists);
@@ -285,23 +335,32 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a, const
   const int which = blockIdx.x / tiles, f0 = (blockIdx.x - which * tiles) * 16;
   if (which >= lists.count) return;
   const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quarter = lane >> 4;
-  int pair[MT];
-  const uint16_t* at_x[MT];
-  bool live[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    pair[m] = moe_pair(a, lists, 16 * m + col, expert);
-    live[m] = pair[m] >= 0;
-    at_x[m] = x + (int64_t)min(16 * m + col, a.tokens - 1) * a.k;
-  }
-  f32x4 acc[2][MT] = {};
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, quarter = lane >> 4;
   const int units = (a.k + kUnit - 1) / kUnit;
   const int64_t row = (int64_t)expert * 2 * a.f + f0 + col;
-  for (int u = wave; u < units; u += kUpWaves) {
+  MoeWeights w[2][2];
+  auto load = [&](int u, MoeWeights(&x)[2]) {
     const int at = u * kUnit + 64 * quarter;
-    const MoeWeights w[2] = {moe_load(a.up_codes, a.up_scales, row, a.k, at), moe_load(a.up_codes, a.up_scales, row + a.f, a.k, at)};
-    moe_unit<2, MT, PX>(w, at_x, live, x_plane, at, a.k, acc);
+    x[0] = moe_load<WHOLE>(a.up_codes, a.up_scales, row, a.k, at);
+    x[1] = moe_load<WHOLE>(a.up_codes, a.up_scales, row + a.f, a.k, at);
+  };
+  if (wave < units) load(wave, w[0]);
+  const uint16_t* at_x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int t = 16 * m + col;
+    at_x[m] = a.x_pieces + moe_instead(t, moe_pair(a, lists, t, expert) >= 0) * moe_row(a.k, PX) + 8 * quarter;
+  }
+  f32x4 acc[2][MT] = {};
+  for (int u = wave; u < units;) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (u >= units) break;
+      moe_unit<2, MT, PX>(w[j], at_x, u, acc, [&]() {
+        if (u + kUpWaves < units) load(u + kUpWaves, w[1 - j]);
+      });
+      u += kUpWaves;
+    }
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r)
@@ -309,7 +368,6 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a, const
     for (int m = 0; m < MT; ++m) part[wave][r][m][lane] = acc[r][m];
   __syncthreads();
   const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
-  const int64_t h_plane = (int64_t)a.tokens * a.top_k * a.f;
   for (int m = wave; m < MT; m += kUpWaves) {
     const int p = moe_pair(a, lists, 16 * m + col, expert);
     f32x4 g = part[0][0][m][lane], v = part[0][1][m][lane];
@@ -327,57 +385,95 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a, const
     }
 #pragma unroll
     for (int j = 0; j < PH; ++j)
-      *reinterpret_cast<u32x2*>(a.h_pieces + j * h_plane + (int64_t)p * a.f + f0 + 4 * quarter) =
+      *reinterpret_cast<u32x2*>(a.h_pieces + p * moe_row(a.f, PH) + moe_place(f0 + 4 * quarter, PH) + 32 * j + 4 * (quarter & 1)) =
           u32x2{piece[0][j] | (uint32_t)piece[1][j] << 16, piece[2][j] | (uint32_t)piece[3][j] << 16};
   }
 }
 
-constexpr int kDownWaves = 8;
+constexpr int kDownWaves = 16, kDownAhead = 2;
 
-// 16 columns of the output for all tokens: a workgroup, its waves equal runs of
-// the units of all chosen experts' rows.
-template <int DT, int MT, int PH>
+// 16 columns of the output for all tokens: a workgroup, its waves in turn the
+// units of all chosen experts' rows: what they read at a time lies together.
+template <int DT, int MT, int PH, bool WHOLE>
 __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeLayer a) {
   __shared__ MoeLists lists;
   __shared__ f32x4 part[kDownWaves][MT][64];
   moe_lists(a, lists);
   const int n0 = blockIdx.x * 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quarter = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, quarter = lane >> 4;
   const int units = (a.f + kUnit - 1) / kUnit, all = lists.count * units;
-  const int64_t h_plane = (int64_t)a.tokens * a.top_k * a.f;
   f32x4 total[MT] = {};
-  int unit = (int)((int64_t)all * wave / kDownWaves);
-  const int last = (int)((int64_t)all * (wave + 1) / kDownWaves);
-  while (unit < last) {
-    const int which = unit / units;
-    const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
-    const int end = min(last, (which + 1) * units);
+  if (wave < all) {
+    MoeWeights w[kDownAhead + 1][1];
+    // the unit that is loaded next, all of them, and of its expert
+    int next = wave, next_which = wave / units, next_u = wave - next_which * units;
+    int64_t next_row = 0;
+    auto seek = [&]() {
+      next_row = (int64_t)__builtin_amdgcn_readfirstlane(lists.list[next_which]) * a.k + n0 + col;
+    };
+    auto load = [&](MoeWeights& x) {
+      if (next >= all) return;
+      x = moe_load<WHOLE>(a.down_codes, a.down_scales, next_row, a.f, next_u * kUnit + 64 * quarter);
+      next += kDownWaves;
+      next_u += kDownWaves;
+      if (next_u >= units && next < all) {
+        do {
+          next_u -= units;
+          ++next_which;
+        } while (next_u >= units);
+        seek();
+      }
+    };
+    seek();
+#pragma unroll
+    for (int j = 0; j < kDownAhead; ++j) load(w[j][0]);
+
     const uint16_t* at_h[MT];
     bool live[MT];
     float weight[MT];
-    const float factor = global_decode(a.down_global ? a.down_global + expert : nullptr);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int t = 16 * m + col, p = moe_pair(a, lists, t, expert);
-      live[m] = p >= 0;
-      at_h[m] = a.h_pieces + (int64_t)max(p, 0) * a.f;
-      weight[m] = 0.0f;
-      if (p >= 0)  // an expert may stand twice among a token's
-        for (int q = p; q < (t + 1) * a.top_k; ++q)
-          if (lists.idx[q] == expert) weight[m] += a.expert_weights[q];
-      weight[m] *= factor;
-    }
     f32x4 acc[1][MT] = {};
-    const int64_t row = (int64_t)expert * a.k + n0 + col;
-    for (; unit < end; ++unit) {
-      const int at = (unit - which * units) * kUnit + 64 * quarter;
-      const MoeWeights w[1] = {moe_load(a.down_codes, a.down_scales, row, a.f, at)};
-      moe_unit<1, MT, PH>(w, at_h, live, h_plane, at, a.f, acc);
+    int which = wave / units, u = wave - which * units, left = (all - wave + kDownWaves - 1) / kDownWaves;
+    auto begin = [&]() {  // the columns of expert `which`
+      const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
+      const float factor = global_decode(a.down_global ? a.down_global + expert : nullptr);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int t = 16 * m + col, p = moe_pair(a, lists, t, expert);
+        live[m] = p >= 0;
+        at_h[m] = a.h_pieces + moe_instead(p, live[m]) * moe_row(a.f, PH) + 8 * quarter;
+        weight[m] = 0.0f;
+        if (p >= 0)  // an expert may stand twice among a token's
+          for (int q = p; q < (t + 1) * a.top_k; ++q)
+            if (lists.idx[q] == expert) weight[m] += a.expert_weights[q];
+        weight[m] *= factor;
+        acc[0][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    };
+    auto end = [&]() {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total[m][i] = live[m] ? total[m][i] + weight[m] * acc[0][m][i] : total[m][i];
+    };
+    begin();
+    while (left > 0) {
+#pragma unroll
+      for (int j = 0; j <= kDownAhead; ++j) {
+        if (left <= 0) break;
+        moe_unit<1, MT, PH>(w[j], at_h, u, acc, [&]() { load(w[(j + kDownAhead) % (kDownAhead + 1)][0]); });
+        --left;
+        u += kDownWaves;
+        if (u >= units && left > 0) {
+          end();
+          do {
+            u -= units;
+            ++which;
+          } while (u >= units);
+          begin();
+        }
+      }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) total[m][i] = live[m] ? total[m][i] + weight[m] * acc[0][m][i] : total[m][i];
+    end();
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) part[wave][m][lane] = total[m];
@@ -398,9 +494,6 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeLayer a) {
 
 // ----------------------------------------------------------------- launches
 
-constexpr int moe_x_pieces(int dt) { return dt == kF32 ? 3 : dt == kF16 ? 2 : 1; }
-constexpr int moe_h_pieces(int dt) { return dt == kF32 ? 3 : 2; }
-
 struct MoePlan {
   size_t logits, x, h, bytes;  // offsets in the workspace
 };
@@ -409,8 +502,8 @@ MoePlan moe_plan(int64_t tokens, int64_t top_k, int64_t experts, int64_t k, int6
   MoePlan p;
   p.logits = 0;
   p.x = up((size_t)tokens * experts * 8);
-  p.h = p.x + (moe_x_pieces(dt) > 1 ? up((size_t)moe_x_pieces(dt) * tokens * k * 2) : 0);
-  p.bytes = p.h + up((size_t)moe_h_pieces(dt) * tokens * top_k * f * 2);
+  p.h = p.x + up((size_t)tokens * moe_row((int)k, moe_x_pieces(dt)) * 2);
+  p.bytes = p.h + up((size_t)tokens * top_k * moe_row((int)f, moe_h_pieces(dt)) * 2);
   return p;
 }
 
@@ -418,23 +511,31 @@ template <int DT, int MT>
 hipError_t launch_products(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT), PH = moe_h_pieces(DT);
   const int pairs = a.tokens * a.top_k, most = pairs < a.experts ? pairs : a.experts;
-  const uint16_t* x = PX > 1 ? a.x_pieces : reinterpret_cast<const uint16_t*>(a.x);
-  moe_up_kernel<MT, PX, PH><<<(unsigned)(most * (a.f / 16)), 64 * kUpWaves, 0, s>>>(a, x, (int64_t)a.tokens * a.k);
+  const unsigned up = (unsigned)(most * (a.f / 16)), down = (unsigned)(a.k / 16);
+  if (a.k % 64 == 0) moe_up_kernel<MT, PX, PH, true><<<up, 64 * kUpWaves, 0, s>>>(a);
+  else moe_up_kernel<MT, PX, PH, false><<<up, 64 * kUpWaves, 0, s>>>(a);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  moe_down_kernel<DT, MT, PH><<<(unsigned)(a.k / 16), 64 * kDownWaves, 0, s>>>(a);
+  if (a.f % 64 == 0) moe_down_kernel<DT, MT, PH, true><<<down, 64 * kDownWaves, 0, s>>>(a);
+  else moe_down_kernel<DT, MT, PH, false><<<down, 64 * kDownWaves, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t launch(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT);
-  const int chunks = (a.tokens + kRouterTokens - 1) / kRouterTokens;
-  const int routers = a.router ? (a.experts * chunks + 3) / 4 : 0;
-  const int64_t cuts = PX > 1 ? ((int64_t)a.tokens * a.k / 8 + 255) / 256 : 0;
-  if (routers + cuts > 0) {
-    moe_logits_kernel<DT, PX><<<(unsigned)(routers + cuts), 256, 0, s>>>(a, routers);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const int64_t eights = a.tokens * (moe_row(a.k, 1) + a.top_k * (moe_row(a.f, 1) - a.f)) / 8;
+  const unsigned cuts = (unsigned)((eights + 255) / 256);
+  // Few logits: a workgroup each, for the latency; many: four tokens each, for the traffic.
+  if (!a.router) {
+    moe_logits_kernel<DT, PX, 1><<<cuts, 256, 0, s>>>(a, 0);
+  } else if (a.tokens * a.experts <= 1024) {
+    const int routers = a.tokens * a.experts;
+    moe_logits_kernel<DT, PX, 1><<<routers + cuts, 256, 0, s>>>(a, routers);
+  } else {
+    const int routers = (a.tokens + 3) / 4 * a.experts;
+    moe_logits_kernel<DT, PX, 4><<<routers + cuts, 256, 0, s>>>(a, routers);
   }
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (a.router) {
     moe_choose_kernel<<<(unsigned)a.tokens, 256, 0, s>>>(a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
