@@ -671,7 +671,8 @@ nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* 
  * Errors: bad dtype, t < 0 (t = 0 is a no-op), e, top_k, k or f not positive,
  * k or f no multiple of 16, top_k > e, NULL or misaligned pointers, workspace
  * too small; UNSUPPORTED for more than 64 tokens, top_k > 32, e > 1024, k or f
- * of 2^20 or more, min(t * top_k, e) * f / 16 of 2^24 or more.
+ * of 2^20 or more, min(t * top_k, e) * f / 16 of 2^24 or t * top_k * f of 2^29
+ * or more.
  */
 size_t nvfp4_moe_workspace_size(nvfp4_dtype dt, int64_t t, int64_t top_k, int64_t e, int64_t k, int64_t f);
 nvfp4_status nvfp4_moe(const void* x, nvfp4_dtype dt, const void* router, int32_t* expert_idx,

@@ -1248,7 +1248,8 @@ static nvfp4_status check_moe(const char* op, nvfp4_dtype dt, int64_t t, int64_t
   if (t > nvfp4::kMoeMaxTokens || top_k > nvfp4::kMoeMaxTopK || e > nvfp4::kMoeMaxExperts)
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] More than %d tokens, %d experts a token or %d experts.", op,
                 nvfp4::kMoeMaxTokens, nvfp4::kMoeMaxTopK, nvfp4::kMoeMaxExperts);
-  if (k >= 1 << 20 || f >= 1 << 20 || (t * top_k < e ? t * top_k : e) * (f / 16) >= 1 << 24)
+  if (k >= 1 << 20 || f >= 1 << 20 || (t * top_k < e ? t * top_k : e) * (f / 16) >= 1 << 24 ||
+      t * top_k * f >= 1 << 29)
     return fail(NVFP4_ERR_UNSUPPORTED, "[%s] Sizes too large.", op);
   return NVFP4_OK;
 }

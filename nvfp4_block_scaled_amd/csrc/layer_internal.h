@@ -50,7 +50,7 @@ struct MoeLayer {
   int tokens, top_k, experts, k, f, normalize;  // k and f multiples of 16, below 2^20
   // in the workspace, set by the launch
   double* logits;                 // [tokens, experts]
-  uint16_t *x_pieces, *h_pieces;  // of tokens, of pairs (moe_row, moe_place)
+  uint16_t *x_pieces, *h_pieces;  // of tokens (float32, float16), of pairs: moe_row, moe_place
 };
 size_t moe_workspace(int64_t tokens, int64_t top_k, int64_t experts, int64_t k, int64_t f, int dt);
 hipError_t launch_moe(MoeLayer a, int dt, void* workspace, hipStream_t s);

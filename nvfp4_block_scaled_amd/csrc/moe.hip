@@ -19,8 +19,10 @@
 // Tokens are the columns of the products and weights their rows, 16 rows by 16
 // tokens a product.  Weights are the traffic: each workgroup streams rows of
 // one expert and meets all tokens of that expert at once.
-#include "kv_device.h"
+#include <atomic>
+
 #include "layer_internal.h"
+#include "nvfp4_device.h"
 
 namespace nvfp4 {
 
@@ -49,17 +51,13 @@ __device__ __forceinline__ void moe_pieces(float v, uint16_t (&p)[N]) {
   }
 }
 
-// Where x and h lie in the workspace: per row the units of 256 values, of each
-// the 8 steps of a product in turn, of a step the pieces, and of a piece the 8
-// values of each quarter of a wave (values 64 quarter + 8 step .. of the unit).
-// So the four quarters' loads of a column are one line's 64 bytes; as the values
-// themselves lie they were four lines, and these loads took as long as the
-// weights' (16 tokens, 2 of 8 experts of 4096 x 14336: down products 262 us).
+// Where pieces lie: per row the units of 256 values, of each the pieces in turn.
+// (bfloat16 x is one piece as it is.)
 __host__ __device__ constexpr int64_t moe_row(int inner, int pieces) {
-  return (int64_t)((inner + kUnit - 1) / kUnit) * kUnit * pieces;
+  return pieces == 1 ? inner : (int64_t)((inner + kUnit - 1) / kUnit) * kUnit * pieces;
 }
-__device__ __forceinline__ int moe_place(int at, int pieces) {  // of the first piece of the 8 values from `at` on
-  return ((at / kUnit * 8 + (at & 63) / 8) * pieces) * 32 + (at & (kUnit - 1)) / 64 * 8;
+__device__ __forceinline__ int moe_place(int at, int pieces) {  // of the first piece of value `at`
+  return at / kUnit * kUnit * pieces + (at & (kUnit - 1));
 }
 
 // ----------------------------------------------------------------- router
@@ -71,35 +69,27 @@ __device__ __forceinline__ double moe_wave_sum(double v) {
 }
 
 // Workgroups 0 .. routers - 1: logits, a workgroup an expert and TOKENS tokens, for
-// which its row is loaded once.  The others lay x out in pieces.
+// which its row is loaded once.  The others cut x into pieces (PX > 1).
 template <int DT, int PX, int TOKENS>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeLayer a, int routers) {
   if ((int)blockIdx.x >= routers) {
-    // with zeros behind the end of a row, as weights behind it are 0 and 0 times anything else might be NaN
-    constexpr int PH = moe_h_pieces(DT);
-    const int per_row = (int)moe_row(a.k, 1) / 8, more = (int)moe_row(a.f, 1) - a.f;
-    int h = (int)(blockIdx.x - routers) * 256 + threadIdx.x;
-    if (h >= a.tokens * per_row) {
-      h -= a.tokens * per_row;
-      if (more == 0 || h >= a.tokens * a.top_k * (more / 8)) return;
-      const int p = h / (more / 8), at = a.f + 8 * (h - p * (more / 8));
+    if constexpr (PX > 1) {
+      const int per_row = a.k / 8;
+      const int h = (int)(blockIdx.x - routers) * 256 + threadIdx.x;
+      if (h >= a.tokens * per_row) return;
+      const int t = h / per_row, at = 8 * (h - t * per_row);
+      float v[8];
+      load8x<DT>(a.x, h, v);
+      uint16_t p[8][PX];
 #pragma unroll
-      for (int j = 0; j < PH; ++j)
-        *reinterpret_cast<u32x4*>(a.h_pieces + p * moe_row(a.f, PH) + moe_place(at, PH) + 32 * j) = u32x4{0u, 0u, 0u, 0u};
-      return;
-    }
-    const int t = h / per_row, at = 8 * (h - t * per_row);
-    float v[8] = {};
-    if (at < a.k) load8x<DT>(a.x, (int64_t)t * (a.k / 8) + at / 8, v);
-    uint16_t p[8][PX];
+      for (int i = 0; i < 8; ++i) moe_pieces<PX>(v[i], p[i]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) moe_pieces<PX>(v[i], p[i]);
+      for (int j = 0; j < PX; ++j) {
+        u32x4 w;
 #pragma unroll
-    for (int j = 0; j < PX; ++j) {
-      u32x4 w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = p[2 * i][j] | (uint32_t)p[2 * i + 1][j] << 16;
-      *reinterpret_cast<u32x4*>(a.x_pieces + t * moe_row(a.k, PX) + moe_place(at, PX) + 32 * j) = w;
+        for (int i = 0; i < 4; ++i) w[i] = p[2 * i][j] | (uint32_t)p[2 * i + 1][j] << 16;
+        *reinterpret_cast<u32x4*>(a.x_pieces + t * moe_row(a.k, PX) + moe_place(at, PX) + kUnit * j) = w;
+      }
     }
     return;
   }
@@ -217,48 +207,117 @@ __device__ __forceinline__ int moe_pair(const MoeLayer& a, const MoeLists& s, in
 }
 
 // ----------------------------------------------------------------- products
+//
+// A wave's unit: 256 inner values of NR tiles of 16 weight rows, and of the
+// columns (x or h of a token) that meet them.  A product's operand is 8 values of
+// lane l's row l % 16 from value 8 (l / 16) on, so that neighbouring lanes read
+// different rows; loaded that way, every 16 bytes are a cache access of their
+// own, and accesses bound the kernels (0.82 a clock and CU, 16 tokens, 2 of 8
+// experts of 4096 x 14336: 141 us up, 140 us down).  So a wave loads whole lines,
+// 8 lanes a row's 128 bytes, and turns them round in LDS of its own, where no
+// other wave waits for it; chunks of 16 bytes lie at their number xor the row's,
+// which spreads both the writes and the reads over the banks.  The next unit's
+// loads are under way meanwhile.
 
-// 64 consecutive inner values of one row, as loaded: 4 groups of 16.  WHOLE: rows
-// are whole 64s; then a lane past a row's end loads the row's beginning, and no
-// branch stands between the loads.  Scales past the end are 0, and so are weights.
-struct MoeWeights {
-  uint32_t w[8], s;
+constexpr int kSlots = 8;  // columns in LDS at a time
+
+// In LDS, of one wave.
+template <int NR, int P>
+struct MoeStage {
+  u32x4 codes[NR][16][8];       // row, chunk of 32 values
+  uint32_t scales[NR][16][4];   // row, 4 groups of 16
+  u32x4 columns[P][kSlots][32]; // column, chunk of 8 values
 };
-template <bool WHOLE>
-__device__ __forceinline__ MoeWeights moe_load(const uint8_t* codes, const uint8_t* scales, int64_t row, int inner, int at) {
-  MoeWeights r;
-  const int from = WHOLE && at >= inner ? 0 : at;
-  const uint8_t* c = codes + row * (inner / 2) + from / 2;
-  const uint8_t* s = scales + row * (inner / 16) + from / 16;
-  if (WHOLE || at + 64 <= inner) {
-    const u32x4_8 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c));
-    const u32x4_8 y = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + 16));
+
+// One unit's weights on their way: lane l has chunk l % 8 of rows l / 8 and l / 8
+// + 8, and the scales of row l / 4, groups 4 (l % 4) ...  WHOLE: rows are whole
+// 64s and scales whole dwords.  Past the end of a row scales are 0, and so are its weights.
+template <int NR>
+struct MoeWeights {
+  u32x4 c[NR][2];
+  uint32_t s[NR];
+};
+template <int NR, bool WHOLE>
+__device__ __forceinline__ void moe_load(MoeWeights<NR>& w, const uint8_t* codes, const uint8_t* scales, const int64_t (&row0)[NR],
+                                         int inner, int unit) {
+  const int lane = threadIdx.x & 63;
+  const int from = unit * kUnit + 32 * (lane & 7), group = unit * (kUnit / 16) + 4 * (lane & 3), groups = inner / 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.w[i] = x[i];
-      r.w[4 + i] = y[i];
-    }
-    if constexpr (WHOLE) {
-      r.s = *reinterpret_cast<const uint32_t*>(s);
-      if (at >= inner) r.s = 0u;
-    } else {
-      __builtin_memcpy(&r.s, s, 4);
-    }
-  } else {
-    r.s = 0u;
+  for (int r = 0; r < NR; ++r) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      r.w[2 * g] = r.w[2 * g + 1] = 0u;
-      if (at + 16 * g < inner) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(c + 8 * g);
-        r.w[2 * g] = x.x;
-        r.w[2 * g + 1] = x.y;
-        r.s |= (uint32_t)s[g] << (8 * g);
+    for (int d = 0; d < 2; ++d) {
+      const uint8_t* p = codes + (row0[r] + (lane >> 3) + 8 * d) * (inner / 2) + from / 2;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (WHOLE ? from < inner : from + 32 <= inner) {
+        v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(p));
+      } else if (!WHOLE && from < inner) {
+        const u32x2 half = *reinterpret_cast<const u32x2*>(p);
+        v.x = half.x;
+        v.y = half.y;
       }
+      w.c[r][d] = v;
+    }
+    const uint8_t* p = scales + (row0[r] + (lane >> 2)) * groups + group;
+    w.s[r] = 0u;
+    if constexpr (WHOLE) {
+      if (group < groups) w.s[r] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (group + i < groups) w.s[r] |= (uint32_t)p[i] << (8 * i);
     }
   }
-  return r;
 }
+template <int NR, int P>
+__device__ __forceinline__ void moe_stage(MoeStage<NR, P>& l, const MoeWeights<NR>& w) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) l.codes[r][(lane >> 3) + 8 * d][(lane & 7) ^ (lane >> 3)] = w.c[r][d];
+    l.scales[r][lane >> 2][lane & 3] = w.s[r];
+  }
+}
+
+// kSlots columns of a unit on their way: lane l has chunk l % 32 of columns l / 32, l / 32 + 2 ..
+template <int P>
+struct MoeColumns {
+  u32x4 v[P][kSlots / 2];
+};
+// `at`: where this lane's columns begin; `count` of them are there, of `inner` values.
+template <int P>
+__device__ __forceinline__ void moe_load(MoeColumns<P>& x, const uint16_t* base, const int (&at)[kSlots / 2], int count, int inner,
+                                         int unit) {
+  const int lane = threadIdx.x & 63;
+  const bool there = unit * kUnit + 8 * (lane & 31) < inner;
+#pragma unroll
+  for (int i = 0; i < kSlots / 2; ++i)
+    if (2 * i < count) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        x.v[p][i] = u32x4{0u, 0u, 0u, 0u};
+        if (there) x.v[p][i] = *reinterpret_cast<const u32x4*>(base + at[i] + unit * kUnit * P + p * kUnit + 8 * (lane & 31));
+      }
+    }
+}
+template <int NR, int P>
+__device__ __forceinline__ void moe_stage(MoeStage<NR, P>& l, const MoeColumns<P>& x, int count) {
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < kSlots / 2; ++i)
+    if (2 * i < count) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) l.columns[p][2 * i + half][(lane & 31) ^ (2 * i + half)] = x.v[p][i];
+    }
+}
+
+// What a wave's lanes have written to its LDS, its other lanes may read.
+__device__ __forceinline__ void moe_settle() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 8 weights (a dword of codes) times their block scale, exact in bfloat16.
 __device__ __forceinline__ bf16x8 moe_decode8(uint32_t w, float s) {
   float v[8];
@@ -269,57 +328,73 @@ __device__ __forceinline__ bf16x8 moe_decode8(uint32_t w, float s) {
     r[i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1] * s), __float_as_uint(v[2 * i] * s), 0x07060302u);
   return __builtin_bit_cast(bf16x8, r);
 }
-__device__ __forceinline__ bf16x8 moe_values(const MoeWeights& r, int i) {
-  return moe_decode8(r.w[i], e4m3_decode(r.s >> (8 * (i >> 1))));
-}
 
-// One unit: NR tiles of 16 rows by MT tiles of 16 tokens.  Lane l has row l % 16
-// and inner values 64 (l / 16) .. of the unit on both sides.  `col`: this lane's
-// column of each tile, at its quarter's values of the unit's first step.
-//
-// `ahead` loads the weights of a later unit.  Loads come back in the order of
-// their issue, so it is called behind the unit's last loads of columns: ahead of
-// them, waiting for those (in a cache) would wait for weights from memory too.
-template <int NR, int MT, int P, typename F>
-__device__ __forceinline__ void moe_unit(const MoeWeights (&w)[NR], const uint16_t* const (&col)[MT], int unit,
-                                         f32x4 (&acc)[NR][MT], F ahead) {
-  constexpr int H = MT * P <= 2 ? 8 : MT * P <= 4 ? 4 : 2;  // steps whose columns are loaded at a time
+// The products of what is staged.  Lane l has row l % 16 and values 64 (l / 16) ..
+// + 63 of the unit on both sides.  slot[m]: this lane's column of tile m among
+// those staged, or -1: it meets zeros.  tiles: which tiles have any.
+template <int NR, int MT, int P>
+__device__ __forceinline__ void moe_products(const MoeStage<NR, P>& l, const int (&slot)[MT], uint32_t tiles,
+                                             f32x4 (&acc)[NR][MT]) {
+  const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
+  float scale[NR][4];
+  u32x4 codes[NR][2];
 #pragma unroll
-  for (int c = 0; c < 8 / H; ++c) {
-    bf16x8 b[H][MT][P];
+  for (int r = 0; r < NR; ++r) {
+    const uint32_t s = l.scales[r][row][quarter];
+    scale[r][0] = e4m3_decode_byte<0>(s);
+    scale[r][1] = e4m3_decode_byte<1>(s);
+    scale[r][2] = e4m3_decode_byte<2>(s);
+    scale[r][3] = e4m3_decode_byte<3>(s);
 #pragma unroll
-    for (int i = 0; i < H; ++i)
+    for (int j = 0; j < 2; ++j) codes[r][j] = l.codes[r][row][(2 * quarter + j) ^ (row & 7)];
+  }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int i = 0; i < 8; ++i) {
+    bf16x8 a[NR];
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          b[i][m][p] = *reinterpret_cast<const bf16x8*>(col[m] + (unit * 8 + c * H + i) * P * 32 + p * 32);
-    __builtin_amdgcn_sched_barrier(0);
-    if (c + 1 == 8 / H) {
-      ahead();
-      __builtin_amdgcn_sched_barrier(0);
+    for (int r = 0; r < NR; ++r) a[r] = moe_decode8(codes[r][i >> 2][i & 3], scale[r][i >> 1]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (MT > 1 && !(tiles >> m & 1u)) continue;
+#pragma unroll
+      for (int p = P - 1; p >= 0; --p) {  // the small pieces first
+        const int at = max(slot[m], 0);
+        u32x4 v = l.columns[p][at][(8 * quarter + i) ^ at];
+        if (slot[m] < 0) v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r], __builtin_bit_cast(bf16x8, v), acc[r][m], 0, 0, 0);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < H; ++i) {
-      bf16x8 a[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) a[r] = moe_values(w[r], c * H + i);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int p = P - 1; p >= 0; --p)  // the small pieces first
-#pragma unroll
-          for (int r = 0; r < NR; ++r) acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r], b[i][m][p], acc[r][m], 0, 0, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
-// The row that a column without a token reads instead: the first one that has
-// (no line more); its sums are not looked at.  0 if none has.
-__device__ __forceinline__ int moe_instead(int row, bool live) {
-  const uint64_t lanes = __ballot(live);
-  const int other = lanes ? __builtin_amdgcn_readlane(row, __builtin_ctzll(lanes)) : 0;
-  return live ? row : other;
+
+// The tokens of one expert.  Lane t < 64 has token t's first pair with it.
+struct MoeTokens {
+  uint64_t live;  // which tokens
+  int count;
+};
+__device__ __forceinline__ MoeTokens moe_tokens(int pair) {
+  MoeTokens r;
+  r.live = __ballot(pair >= 0);
+  r.count = __builtin_popcountll(r.live);
+  return r;
+}
+// Which of them token t is.
+__device__ __forceinline__ int moe_rank(const MoeTokens& k, int t) {
+  return __builtin_popcountll(k.live & ((1ull << t) - 1));
+}
+// This lane's column of each tile among those from `from` on, and the tiles that have any.
+template <int MT>
+__device__ __forceinline__ uint32_t moe_slots(const MoeTokens& k, int from, int (&slot)[MT]) {
+  uint32_t tiles = 0u;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int t = 16 * m + (threadIdx.x & 15), at = moe_rank(k, t) - from;
+    slot[m] = (k.live >> t & 1u) && at >= 0 && at < kSlots ? at : -1;
+    tiles |= __any(slot[m] >= 0) ? 1u << m : 0u;
+  }
+  return tiles;
 }
 
 constexpr int kUpWaves = 4;
@@ -327,54 +402,74 @@ constexpr int kUpWaves = 4;
 // 16 gate rows and the 16 up rows that go with them, of one expert: a workgroup,
 // its waves each a share of the inner values.
 template <int MT, int PX, int PH, bool WHOLE>
-__global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a) {
+__global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a, const uint16_t* x) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ MoeLists lists;
-  __shared__ f32x4 part[kUpWaves][2][MT][64];
+  __shared__ int row_of[kMoeMaxTokens];  // of the expert's tokens
   moe_lists(a, lists);
   const int tiles = a.f / 16;
   const int which = blockIdx.x / tiles, f0 = (blockIdx.x - which * tiles) * 16;
   if (which >= lists.count) return;
   const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, quarter = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int units = (a.k + kUnit - 1) / kUnit;
-  const int64_t row = (int64_t)expert * 2 * a.f + f0 + col;
-  MoeWeights w[2][2];
-  auto load = [&](int u, MoeWeights(&x)[2]) {
-    const int at = u * kUnit + 64 * quarter;
-    x[0] = moe_load<WHOLE>(a.up_codes, a.up_scales, row, a.k, at);
-    x[1] = moe_load<WHOLE>(a.up_codes, a.up_scales, row + a.f, a.k, at);
-  };
-  if (wave < units) load(wave, w[0]);
-  const uint16_t* at_x[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = 16 * m + col;
-    at_x[m] = a.x_pieces + moe_instead(t, moe_pair(a, lists, t, expert) >= 0) * moe_row(a.k, PX) + 8 * quarter;
-  }
+  const int64_t row0[2] = {(int64_t)expert * 2 * a.f + f0, (int64_t)expert * 2 * a.f + a.f + f0};
+  MoeWeights<2> w;
+  if (wave < units) moe_load<2, WHOLE>(w, a.up_codes, a.up_scales, row0, a.k, wave);
+  const int my_pair = moe_pair(a, lists, lane, expert);
+  const MoeTokens tokens = moe_tokens(my_pair);
+  if (wave == 0 && my_pair >= 0) row_of[moe_rank(tokens, lane)] = lane;
+  __syncthreads();
+  MoeStage<2, PX>& stage = reinterpret_cast<MoeStage<2, PX>*>(lds)[wave];
   f32x4 acc[2][MT] = {};
-  for (int u = wave; u < units;) {
+  MoeColumns<PX> columns;
+  auto place = [&](int from, int(&at)[kSlots / 2]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (u >= units) break;
-      moe_unit<2, MT, PX>(w[j], at_x, u, acc, [&]() {
-        if (u + kUpWaves < units) load(u + kUpWaves, w[1 - j]);
-      });
-      u += kUpWaves;
+    for (int i = 0; i < kSlots / 2; ++i)
+      at[i] = row_of[min(from + 2 * i + (lane >> 5), tokens.count - 1)] * (int)moe_row(a.k, PX);
+  };
+  int at[kSlots / 2], slot[MT];
+  place(0, at);
+  const uint32_t first = moe_slots<MT>(tokens, 0, slot);
+  if (wave < units) moe_load<PX>(columns, x, at, tokens.count, a.k, wave);
+  for (int u = wave; u < units; u += kUpWaves) {
+    moe_stage<2, PX>(stage, w);
+    moe_stage<2, PX>(stage, columns, tokens.count);
+    moe_settle();
+    if (u + kUpWaves < units) {
+      moe_load<PX>(columns, x, at, tokens.count, a.k, u + kUpWaves);
+      moe_load<2, WHOLE>(w, a.up_codes, a.up_scales, row0, a.k, u + kUpWaves);
     }
+    moe_products<2, MT, PX>(stage, slot, first, acc);
+    for (int from = kSlots; from < tokens.count; from += kSlots) {  // more tokens than have room
+      MoeColumns<PX> more;
+      int at2[kSlots / 2], slot2[MT];
+      place(from, at2);
+      moe_load<PX>(more, x, at2, tokens.count - from, a.k, u);
+      moe_settle();
+      moe_stage<2, PX>(stage, more, tokens.count - from);
+      moe_settle();
+      const uint32_t some = moe_slots<MT>(tokens, from, slot2);
+      moe_products<2, MT, PX>(stage, slot2, some, acc);
+    }
+    moe_settle();
   }
+  __syncthreads();
+  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [wave][2][MT][64]
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) part[wave][r][m][lane] = acc[r][m];
+    for (int m = 0; m < MT; ++m) part[((wave * 2 + r) * MT + m) * 64 + lane] = acc[r][m];
   __syncthreads();
   const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
+  const int quarter = lane >> 4;
   for (int m = wave; m < MT; m += kUpWaves) {
-    const int p = moe_pair(a, lists, 16 * m + col, expert);
-    f32x4 g = part[0][0][m][lane], v = part[0][1][m][lane];
+    const int p = moe_pair(a, lists, 16 * m + (lane & 15), expert);
+    f32x4 g = part[m * 64 + lane], v = part[(MT + m) * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) {
-      g += part[w][0][m][lane];
-      v += part[w][1][m][lane];
+    for (int i = 1; i < kUpWaves; ++i) {
+      g += part[((i * 2) * MT + m) * 64 + lane];
+      v += part[((i * 2 + 1) * MT + m) * 64 + lane];
     }
     if (p < 0) continue;
     uint16_t piece[4][PH];
@@ -385,37 +480,39 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeLayer a) {
     }
 #pragma unroll
     for (int j = 0; j < PH; ++j)
-      *reinterpret_cast<u32x2*>(a.h_pieces + p * moe_row(a.f, PH) + moe_place(f0 + 4 * quarter, PH) + 32 * j + 4 * (quarter & 1)) =
+      *reinterpret_cast<u32x2*>(a.h_pieces + p * moe_row(a.f, PH) + moe_place(f0 + 4 * quarter, PH) + kUnit * j) =
           u32x2{piece[0][j] | (uint32_t)piece[1][j] << 16, piece[2][j] | (uint32_t)piece[3][j] << 16};
   }
 }
 
-constexpr int kDownWaves = 16, kDownAhead = 2;
+// Waves of a workgroup of the down products: what has room in LDS, and in registers.
+constexpr int down_waves(int MT, int PH) { return PH == 3 || MT > 2 ? 8 : 12; }
 
 // 16 columns of the output for all tokens: a workgroup, its waves in turn the
 // units of all chosen experts' rows: what they read at a time lies together.
 template <int DT, int MT, int PH, bool WHOLE>
-__global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeLayer a) {
+__global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLayer a) {
+  constexpr int WAVES = down_waves(MT, PH);
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ MoeLists lists;
-  __shared__ f32x4 part[kDownWaves][MT][64];
+  __shared__ int rows_of[WAVES][kMoeMaxTokens];
   moe_lists(a, lists);
   const int n0 = blockIdx.x * 16;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, quarter = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int units = (a.f + kUnit - 1) / kUnit, all = lists.count * units;
+  int* const row_of = rows_of[wave];
   f32x4 total[MT] = {};
   if (wave < all) {
-    MoeWeights w[kDownAhead + 1][1];
-    // the unit that is loaded next, all of them, and of its expert
+    MoeWeights<1> w[2];
+    // the unit whose weights are loaded next: of all, and of its expert
     int next = wave, next_which = wave / units, next_u = wave - next_which * units;
-    int64_t next_row = 0;
-    auto seek = [&]() {
-      next_row = (int64_t)__builtin_amdgcn_readfirstlane(lists.list[next_which]) * a.k + n0 + col;
-    };
-    auto load = [&](MoeWeights& x) {
+    int64_t next_row[1];
+    auto seek = [&]() { next_row[0] = (int64_t)__builtin_amdgcn_readfirstlane(lists.list[next_which]) * a.k + n0; };
+    auto load = [&](MoeWeights<1>& x) {
       if (next >= all) return;
-      x = moe_load<WHOLE>(a.down_codes, a.down_scales, next_row, a.f, next_u * kUnit + 64 * quarter);
-      next += kDownWaves;
-      next_u += kDownWaves;
+      moe_load<1, WHOLE>(x, a.down_codes, a.down_scales, next_row, a.f, next_u);
+      next += WAVES;
+      next_u += WAVES;
       if (next_u >= units && next < all) {
         do {
           next_u -= units;
@@ -425,22 +522,35 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeLayer a) {
       }
     };
     seek();
-#pragma unroll
-    for (int j = 0; j < kDownAhead; ++j) load(w[j][0]);
+    load(w[0]);
 
-    const uint16_t* at_h[MT];
-    bool live[MT];
+    MoeStage<1, PH>& stage = reinterpret_cast<MoeStage<1, PH>*>(lds)[wave];
+    MoeColumns<PH> columns;
+    MoeTokens tokens;
+    int at[kSlots / 2], slot[MT];
+    uint32_t first = 0u;
     float weight[MT];
-    f32x4 acc[1][MT] = {};
-    int which = wave / units, u = wave - which * units, left = (all - wave + kDownWaves - 1) / kDownWaves;
+    f32x4 acc[1][MT];
+    int which = wave / units, u = wave - which * units, left = (all - wave + WAVES - 1) / WAVES;
+    auto place = [&](int from, int(&to)[kSlots / 2]) {
+#pragma unroll
+      for (int i = 0; i < kSlots / 2; ++i)
+        to[i] = row_of[min(from + 2 * i + (lane >> 5), tokens.count - 1)] * (int)moe_row(a.f, PH);
+    };
     auto begin = [&]() {  // the columns of expert `which`
       const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
+      const int pair = moe_pair(a, lists, lane, expert);
+      tokens = moe_tokens(pair);
+      moe_settle();
+      if (pair >= 0) row_of[moe_rank(tokens, lane)] = pair;
+      moe_settle();
+      place(0, at);
+      moe_load<PH>(columns, a.h_pieces, at, tokens.count, a.f, u);
+      first = moe_slots<MT>(tokens, 0, slot);
       const float factor = global_decode(a.down_global ? a.down_global + expert : nullptr);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int t = 16 * m + col, p = moe_pair(a, lists, t, expert);
-        live[m] = p >= 0;
-        at_h[m] = a.h_pieces + moe_instead(p, live[m]) * moe_row(a.f, PH) + 8 * quarter;
+        const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
         weight[m] = 0.0f;
         if (p >= 0)  // an expert may stand twice among a token's
           for (int q = p; q < (t + 1) * a.top_k; ++q)
@@ -451,19 +561,41 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeLayer a) {
     };
     auto end = [&]() {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        const bool live = tokens.live >> (16 * m + (lane & 15)) & 1u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) total[m][i] = live[m] ? total[m][i] + weight[m] * acc[0][m][i] : total[m][i];
+        for (int i = 0; i < 4; ++i) total[m][i] = live ? total[m][i] + weight[m] * acc[0][m][i] : total[m][i];
+      }
     };
     begin();
+    load(w[1]);
     while (left > 0) {
 #pragma unroll
-      for (int j = 0; j <= kDownAhead; ++j) {
+      for (int j = 0; j < 2; ++j) {
         if (left <= 0) break;
-        moe_unit<1, MT, PH>(w[j], at_h, u, acc, [&]() { load(w[(j + kDownAhead) % (kDownAhead + 1)][0]); });
+        moe_stage<1, PH>(stage, w[j]);
+        moe_stage<1, PH>(stage, columns, tokens.count);
+        moe_settle();
+        const int now = u;
         --left;
-        u += kDownWaves;
-        if (u >= units && left > 0) {
+        u += WAVES;
+        const bool over = u >= units;
+        if (!over && left > 0) moe_load<PH>(columns, a.h_pieces, at, tokens.count, a.f, u);
+        load(w[j]);
+        moe_products<1, MT, PH>(stage, slot, first, acc);
+        for (int from = kSlots; from < tokens.count; from += kSlots) {  // more tokens than have room
+          MoeColumns<PH> more;
+          int at2[kSlots / 2], slot2[MT];
+          place(from, at2);
+          moe_load<PH>(more, a.h_pieces, at2, tokens.count - from, a.f, now);
+          moe_settle();
+          moe_stage<1, PH>(stage, more, tokens.count - from);
+          moe_settle();
+          const uint32_t some = moe_slots<MT>(tokens, from, slot2);
+          moe_products<1, MT, PH>(stage, slot2, some, acc);
+        }
+        moe_settle();
+        if (over && left > 0) {
           end();
           do {
             u -= units;
@@ -475,20 +607,22 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeLayer a) {
     }
     end();
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) part[wave][m][lane] = total[m];
   __syncthreads();
-  for (int m = wave; m < MT; m += kDownWaves) {
-    const int t = 16 * m + col;
-    f32x4 v = part[0][m][lane];
+  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [wave][MT][64]
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) v += part[w][m][lane];
+  for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = total[m];
+  __syncthreads();
+  for (int m = wave; m < MT; m += WAVES) {
+    const int t = 16 * m + (lane & 15);
+    f32x4 v = part[m * 64 + lane];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) v += part[(i * MT + m) * 64 + lane];
     if (t >= a.tokens) continue;
-    const int64_t at = (int64_t)t * a.k + n0 + 4 * quarter;
+    const int64_t to = (int64_t)t * a.k + n0 + 4 * (lane >> 4);
     if constexpr (DT == kF32)
-      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at) = v;
+      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + to) = v;
     else
-      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + to) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
   }
 }
 
@@ -502,32 +636,63 @@ MoePlan moe_plan(int64_t tokens, int64_t top_k, int64_t experts, int64_t k, int6
   MoePlan p;
   p.logits = 0;
   p.x = up((size_t)tokens * experts * 8);
-  p.h = p.x + up((size_t)tokens * moe_row((int)k, moe_x_pieces(dt)) * 2);
+  p.h = p.x + (moe_x_pieces(dt) > 1 ? up((size_t)tokens * moe_row((int)k, moe_x_pieces(dt)) * 2) : 0);
   p.bytes = p.h + up((size_t)tokens * top_k * moe_row((int)f, moe_h_pieces(dt)) * 2);
   return p;
 }
 
+// Lets `kernel` have more than 64 KB of dynamic LDS; once per device (or twice,
+// by two threads at once).
+template <typename K>
+hipError_t moe_allow_lds(K* kernel, size_t bytes, std::atomic<bool> (&set)[64]) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) dev = 0;
+  if (dev < 0 || dev >= 64 || set[dev]) return hipSuccess;
+  const hipError_t e =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == hipSuccess) set[dev] = true;
+  return e;
+}
+
+template <int DT, int MT, bool WHOLE>
+hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
+  constexpr int PX = moe_x_pieces(DT), PH = moe_h_pieces(DT);
+  constexpr size_t staged = kUpWaves * sizeof(MoeStage<2, PX>), joined = kUpWaves * 2 * MT * 1024;
+  constexpr size_t bytes = staged > joined ? staged : joined;
+  static std::atomic<bool> set[64];
+  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, PX, PH, WHOLE>, bytes, set); e != hipSuccess) return e;
+  const int pairs = a.tokens * a.top_k, most = pairs < a.experts ? pairs : a.experts;
+  const uint16_t* x = PX > 1 ? a.x_pieces : reinterpret_cast<const uint16_t*>(a.x);
+  moe_up_kernel<MT, PX, PH, WHOLE><<<(unsigned)(most * (a.f / 16)), 64 * kUpWaves, bytes, s>>>(a, x);
+  return hipGetLastError();
+}
+
+template <int DT, int MT, bool WHOLE>
+hipError_t launch_down(const MoeLayer& a, hipStream_t s) {
+  constexpr int PH = moe_h_pieces(DT), WAVES = down_waves(MT, PH);
+  constexpr size_t staged = WAVES * sizeof(MoeStage<1, PH>), joined = WAVES * MT * 1024;
+  constexpr size_t bytes = staged > joined ? staged : joined;
+  static std::atomic<bool> set[64];
+  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, PH, WHOLE>, bytes, set); e != hipSuccess) return e;
+  moe_down_kernel<DT, MT, PH, WHOLE><<<(unsigned)(a.k / 16), 64 * WAVES, bytes, s>>>(a);
+  return hipGetLastError();
+}
+
 template <int DT, int MT>
 hipError_t launch_products(const MoeLayer& a, hipStream_t s) {
-  constexpr int PX = moe_x_pieces(DT), PH = moe_h_pieces(DT);
-  const int pairs = a.tokens * a.top_k, most = pairs < a.experts ? pairs : a.experts;
-  const unsigned up = (unsigned)(most * (a.f / 16)), down = (unsigned)(a.k / 16);
-  if (a.k % 64 == 0) moe_up_kernel<MT, PX, PH, true><<<up, 64 * kUpWaves, 0, s>>>(a);
-  else moe_up_kernel<MT, PX, PH, false><<<up, 64 * kUpWaves, 0, s>>>(a);
-  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  if (a.f % 64 == 0) moe_down_kernel<DT, MT, PH, true><<<down, 64 * kDownWaves, 0, s>>>(a);
-  else moe_down_kernel<DT, MT, PH, false><<<down, 64 * kDownWaves, 0, s>>>(a);
-  return hipGetLastError();
+  auto whole = [](int inner, const uint8_t* scales) { return inner % 64 == 0 && (reinterpret_cast<uintptr_t>(scales) & 3) == 0; };
+  const hipError_t e = whole(a.k, a.up_scales) ? launch_up<DT, MT, true>(a, s) : launch_up<DT, MT, false>(a, s);
+  if (e != hipSuccess) return e;
+  return whole(a.f, a.down_scales) ? launch_down<DT, MT, true>(a, s) : launch_down<DT, MT, false>(a, s);
 }
 
 template <int DT>
 hipError_t launch(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT);
-  const int64_t eights = a.tokens * (moe_row(a.k, 1) + a.top_k * (moe_row(a.f, 1) - a.f)) / 8;
-  const unsigned cuts = (unsigned)((eights + 255) / 256);
+  const unsigned cuts = PX > 1 ? (unsigned)((a.tokens * (a.k / 8) + 255) / 256) : 0u;
   // Few logits: a workgroup each, for the latency; many: four tokens each, for the traffic.
   if (!a.router) {
-    moe_logits_kernel<DT, PX, 1><<<cuts, 256, 0, s>>>(a, 0);
+    if (cuts > 0) moe_logits_kernel<DT, PX, 1><<<cuts, 256, 0, s>>>(a, 0);
   } else if (a.tokens * a.experts <= 1024) {
     const int routers = a.tokens * a.experts;
     moe_logits_kernel<DT, PX, 1><<<routers + cuts, 256, 0, s>>>(a, routers);
