@@ -650,9 +650,11 @@ nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* 
  *     g = x . gate_up_hat[e, i], u = x . gate_up_hat[e, f + i],
  *     h_i = g / (1 + exp(-g)) * u                                   (i < f)
  *     out[t] = T( sum_j expert_weights[t, j] * down_hat[e_j] h )
- * float32 sums of exact products before the global scales (float32 x loses
- * nothing, h 2^-16 of itself for 16-bit types), one rounding to T.  Sums in
- * front of the global scale must stay below float32's largest number.
+ * float32 sums of exact products before the global scales, one rounding to T.
+ * x and h enter the products as float16 times a power of two of their row: x of
+ * 16 bits exactly (what is below 2^-27 of its row's largest to within 2^-38 of
+ * that), x of float32 and h of float16 and float32 layers with 22 bits, h of
+ * bfloat16 layers with 11.  An infinity may come out as a NaN.
  *   x              device [t, k] of type dt, 16-byte aligned
  *   router         device [e, k] of type dt, 16-byte aligned; or NULL:
  *                  expert_idx and expert_weights are given, and an index

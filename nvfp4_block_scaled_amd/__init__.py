@@ -151,6 +151,13 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+# the current stream of a device, as an integer, and the current device: torch.cuda's own functions take several
+# times as long, which shows in calls of 10 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -767,6 +774,14 @@ def nvfp4_mx_qqmm_packed(x, w, out=None, workspace=None):
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _mx_pack_bytes(bits, rows, k):
+    """Shapes of the packed codes and scales."""
+    cb, sb = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load_library().nvfp4_mx_pack_size(bits, rows, k, ctypes.byref(cb), ctypes.byref(sb)))
+    return (cb.value,), (sb.value,)
+
+
 class MxNormed(typing.NamedTuple):
     """What nvfp4_mx_rms_norm gives: `quantized`, (codes, scales) or an
     MxPacked; `sum`, x + residual in x's type (x itself without a residual);
@@ -788,42 +803,42 @@ def nvfp4_mx_rms_norm(x, weight=None, mode="mxfp8", residual=None, eps=1e-6, pac
     L = load_library()
     bits = _mx_mode(mode)
     _dev(x, "x")
+    device, dtype, shape, index = x.device, x.dtype, x.shape, x.device.index
+    if index != _current_device():
+        with torch.cuda.device(device):
+            return nvfp4_mx_rms_norm(x, weight, mode, residual, eps, packed, normed, sum_out, out)
     code = _dtype_code(x, "x")
     rows, k = _rows_k(x)
-    for t, name, shape in ((residual, "residual", x.shape), (weight, "weight", (k,)), (sum_out, "sum_out", x.shape)):
-        if t is None:
-            continue
-        if t.dtype is not x.dtype or t.shape != shape or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {x.dtype} {tuple(shape)} on x's device")
-    if x.device.index != torch.cuda.current_device():
-        with torch.cuda.device(x.device):
-            return nvfp4_mx_rms_norm(x, weight, mode, residual, eps, packed, normed, sum_out, out)
-    if packed:
-        cb, sb = ctypes.c_size_t(0), ctypes.c_size_t(0)
-        _check(L.nvfp4_mx_pack_size(bits, rows, k, ctypes.byref(cb), ctypes.byref(sb)))
-        if out is None:
-            out = MxPacked(torch.empty(cb.value, dtype=torch.uint8, device=x.device),
-                           torch.empty(sb.value, dtype=torch.uint8, device=x.device), (rows, k), mode)
-        elif not isinstance(out, MxPacked) or out.mode != mode or out.shape != (rows, k):
-            raise ValueError("out must be an MxPacked of this shape and mode")
-        codes, scales = out.codes, out.scales
-        sizes = ((cb.value,), (sb.value,))
-    else:
-        sizes = (tuple(x.shape[:-1]) + (_mx_code_cols(k, mode),), tuple(x.shape[:-1]) + (k // 32,))
-        if out is None:
-            out = tuple(torch.empty(s, dtype=torch.uint8, device=x.device) for s in sizes)
-        codes, scales = out
-    for t, s in zip((codes, scales), sizes):
-        if t.dtype is not torch.uint8 or t.shape != s or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"out's codes and scales must be contiguous uint8 {sizes} on x's device")
     total = sum_out
+    for t, name in ((residual, "residual"), (weight, "weight"), (total, "sum_out")):
+        if t is not None and (t.dtype is not dtype or t.shape != (shape if t is not weight else (k,)) or t.device != device
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape) if t is not weight else (k,)} on x's device")
+    if packed:
+        sizes = _mx_pack_bytes(bits, rows, k)
+    else:
+        sizes = (*shape[:-1], _mx_code_cols(k, mode)), (*shape[:-1], k // 32)
+    if out is None:
+        codes = torch.empty(sizes[0], dtype=torch.uint8, device=device)
+        scales = torch.empty(sizes[1], dtype=torch.uint8, device=device)
+        out = MxPacked(codes, scales, (rows, k), mode) if packed else (codes, scales)
+    else:
+        if packed:
+            if not isinstance(out, MxPacked) or out.mode != mode or out.shape != (rows, k):
+                raise ValueError("out must be an MxPacked of this shape and mode")
+            codes, scales = out.codes, out.scales
+        else:
+            codes, scales = out
+        for t, size in ((codes, sizes[0]), (scales, sizes[1])):
+            if t.dtype is not torch.uint8 or t.shape != size or t.device != device or not t.is_contiguous():
+                raise ValueError(f"out's codes and scales must be contiguous uint8 {sizes} on x's device")
     if total is None and residual is not None:
         total = torch.empty_like(x)
     y = torch.empty_like(x) if normed else None
     _check(L.nvfp4_mx_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
-                               None if weight is None else weight.data_ptr(), code, bits, rows, k, eps, int(bool(packed)),
+                               None if weight is None else weight.data_ptr(), code, bits, rows, k, eps, 1 if packed else 0,
                                None if total is None else total.data_ptr(), None if y is None else y.data_ptr(),
-                               codes.data_ptr(), scales.data_ptr(), torch.cuda.current_stream().cuda_stream))
+                               codes.data_ptr(), scales.data_ptr(), _raw_stream(index)))
     return MxNormed(out, x if total is None else total, y)
 
 
@@ -857,8 +872,8 @@ def nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router=
     _dev(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [t, k]")
-    code, device = _dtype_code(x, "x"), x.device
-    if device.index != torch.cuda.current_device():
+    code, device, dtype = _dtype_code(x, "x"), x.device, x.dtype
+    if device.index != _current_device():
         with torch.cuda.device(device):
             return nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router, top_k, global_scale_gate_up,
                              global_scale_down, normalize, expert_idx, expert_weights, out, workspace)
@@ -872,10 +887,10 @@ def nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router=
         if w.dtype is not torch.uint8 or w.shape != want or w.device != device or not w.is_contiguous():
             raise ValueError(f"{name} must be a contiguous uint8 {want} on x's device, not {w.dtype} {tuple(w.shape)}")
     g_up, g_down = _gscale(global_scale_gate_up, "global_scale_gate_up", e), _gscale(global_scale_down, "global_scale_down", e)
-    if any(g is not None and g.device != device for g in (g_up, g_down)):
+    if (g_up is not None and g_up.device != device) or (g_down is not None and g_down.device != device):
         raise ValueError("the global scales must be on x's device")
     if router is not None:
-        if router.dtype is not x.dtype or router.shape != (e, k) or router.device != device or not router.is_contiguous():
+        if router.dtype is not dtype or router.shape != (e, k) or router.device != device or not router.is_contiguous():
             raise ValueError(f"router must be a contiguous {x.dtype} {(e, k)} on x's device")
         if top_k is None:
             if expert_idx is None:
@@ -888,26 +903,30 @@ def nvfp4_moe(x, gate_up_codes, gate_up_scales, down_codes, down_scales, router=
             top_k = expert_idx.shape[-1]
     if expert_idx is None:
         expert_idx = torch.empty((t, top_k), dtype=torch.int32, device=device)
+    elif expert_idx.dtype is not torch.int32 or expert_idx.shape != (t, top_k) or expert_idx.device != device \
+            or not expert_idx.is_contiguous():
+        raise ValueError(f"expert_idx must be a contiguous int32 {(t, top_k)} on x's device")
     if expert_weights is None:
         expert_weights = torch.empty((t, top_k), dtype=torch.float32, device=device)
-    for w, name, dtype in ((expert_idx, "expert_idx", torch.int32), (expert_weights, "expert_weights", torch.float32)):
-        if w.dtype is not dtype or w.shape != (t, top_k) or w.device != device or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} {(t, top_k)} on x's device")
+    elif expert_weights.dtype is not torch.float32 or expert_weights.shape != (t, top_k) or expert_weights.device != device \
+            or not expert_weights.is_contiguous():
+        raise ValueError(f"expert_weights must be a contiguous float32 {(t, top_k)} on x's device")
     if out is None:
         out = torch.empty_like(x)
-    elif out.dtype is not x.dtype or out.shape != x.shape or out.device != device or not out.is_contiguous():
+    elif out.dtype is not dtype or out.shape != x.shape or out.device != device or not out.is_contiguous():
         raise ValueError("out must be contiguous and have x's shape, dtype and device")
     if workspace is None:
-        workspace, nbytes = moe_workspace(t, top_k, e, k, f, x.dtype, device)
+        nbytes = _moe_bytes(code, t, top_k, e, k, f)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
     else:
         nbytes = workspace.numel() * workspace.element_size()
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on x's device")
     _check(L.nvfp4_moe(x.data_ptr(), code, None if router is None else router.data_ptr(), expert_idx.data_ptr(),
-                       expert_weights.data_ptr(), int(bool(normalize)), gate_up_codes.data_ptr(), gate_up_scales.data_ptr(),
+                       expert_weights.data_ptr(), 1 if normalize else 0, gate_up_codes.data_ptr(), gate_up_scales.data_ptr(),
                        None if g_up is None else g_up.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(),
                        None if g_down is None else g_down.data_ptr(), t, top_k, e, k, f, out.data_ptr(), workspace.data_ptr(),
-                       nbytes, torch.cuda.current_stream().cuda_stream))
+                       nbytes, _raw_stream(device.index)))
     return out, expert_idx, expert_weights
 
 
@@ -975,13 +994,6 @@ def kv_cache(pages, page_size, heads, dim, global_scale_k=None, global_scale_v=N
         return torch.zeros(pages, heads, page_size, dim // per, dtype=torch.uint8, device=device)
 
     return KVCache(held(2), held(16), held(2), held(16), global_scale_k, global_scale_v)
-
-
-# the current stream of a device, as an integer, and the current device: torch.cuda's own functions take several
-# times as long, which shows in calls of 10 us
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _kv_stream(cache):

@@ -49,8 +49,11 @@ struct MoeLayer {
   void* out;                                // [tokens, k]
   int tokens, top_k, experts, k, f, normalize;  // k and f multiples of 16, below 2^20
   // in the workspace, set by the launch
-  double* logits;                 // [tokens, experts]
-  uint16_t *x_pieces, *h_pieces;  // of tokens (float32, float16), of pairs: moe_row, moe_place
+  double* logits;        // [tokens, experts]
+  int* x_exponent;       // [tokens]: x_pieces times 2^this is x; null: float16 x is used as it lies
+  uint32_t* h_top;       // [tokens * top_k]: bits of the largest |h|
+  uint16_t* x_pieces;    // float16 [pieces][tokens, k]
+  float* hidden;         // [tokens * top_k, f]
 };
 size_t moe_workspace(int64_t tokens, int64_t top_k, int64_t experts, int64_t k, int64_t f, int dt);
 hipError_t launch_moe(MoeLayer a, int dt, void* workspace, hipStream_t s);

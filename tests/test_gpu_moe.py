@@ -5,11 +5,17 @@ sum can change unless two lie within 2^-45 of their terms' sizes of each other
 (asserted not to happen): indices must be equal.  Bounds (u: the output type's
 unit roundoff, K and F the inner sizes):
     weights   float64 arithmetic rounded once: 2^-23 of the value
+    x         as float16 pieces times a power of two that brings the row's largest
+              X to 2^13 .. 2^14: below the smallest normal number a step is
+              2^-24, so at most 2^-25 2^-13 X = 2^-38 X is lost; bfloat16's 8 bits
+              fit the 11, float16 is used as it lies, and float32's two pieces
+              leave 2^-11 2^-11 / 2 of a value: dx = 2^-38 X, 0, 2^-23 |x| + 2^-38 X
     g, u      float32 sums of exact products, in any order, and one factor:
-              e_g = (K + 8) 2^-24 (|x| . |w|) 2^-r, r = 0
+              e_g = (K + 8) 2^-24 (|x| . |w|) + dx . |w|
     h         = g s(g) u, s the logistic: |dh| <= 1.1 |u| e_g + |g s(g)| e_u (the
               slope of g s(g) is below 1.1) + 2^-20 |h| (exponential, division,
-              products) + 2^-16 |h| for 16-bit types (its pieces)
+              products) + its pieces, H the pair's largest: 2^-11 |h| + 2^-38 H
+              (bfloat16: one), 2^-22 |h| + 2^-38 H (two)
     out       sum_j p_j (|W_d| . dh + (F + 8) 2^-24 |W_d| . |h|) + 2^-22 of
               sum_j p_j |W_d| . |h|, and u |out| for the last rounding."""
 import pytest
@@ -82,11 +88,13 @@ def reference(x, w, index, p):
         for i, j in (index == e).nonzero().tolist():
             both, size = up @ x[i], up.abs() @ x[i].abs()
             g, v = both[:w.f], both[w.f:]
-            e_both = (k + 8) * 2.0 ** -24 * size
+            dx = (0.0 if dtype == torch.float16 else 2.0 ** -38 * x[i].abs().max()) + \
+                (2.0 ** -23 * x[i].abs() if dtype == torch.float32 else torch.zeros(k, dtype=torch.float64))
+            e_both = (k + 8) * 2.0 ** -24 * size + up.abs() @ dx
             s = torch.sigmoid(g)
             h = g * s * v
             dh = 1.1 * v.abs() * e_both[:w.f] + (g * s).abs() * e_both[w.f:] + 1.1 * e_both[:w.f] * e_both[w.f:] + \
-                2.0 ** -20 * h.abs() + (2.0 ** -16 * h.abs() if dtype != torch.float32 else 0.0) + 2.0 ** -126
+                (2.0 ** -20 + (2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22)) * h.abs() + 2.0 ** -38 * h.abs().max() + 2.0 ** -126
             out[i] += p[i, j] * (down @ h)
             sizes = down.abs() @ h.abs()
             bound[i] += p[i, j].abs() * (down.abs() @ dh + ((w.f + 8) * 2.0 ** -24 + 2.0 ** -22) * sizes)
