@@ -27,6 +27,7 @@
 
 #include "layer_internal.h"
 #include "nvfp4_device.h"
+#include "nvfp4_internal.h"
 
 namespace nvfp4 {
 
@@ -211,12 +212,18 @@ constexpr bool moe_choose_inside(int tokens, int experts) {
 struct MoeLists {
   int *idx, *first, *list;
   int* count;
+  int* exponent;  // of each token's x (kMoeMaxTokens, up products) or each pair's h (down products)
+  float* weight;  // of each pair (down products)
 };
-constexpr int moe_list_words(int pairs, int experts) { return (pairs + 2 * experts + 1 + 3) / 4 * 4; }
+constexpr int moe_list_words(int pairs, int experts) {
+  return (pairs + 2 * experts + 1 + (pairs > kMoeMaxTokens ? pairs : kMoeMaxTokens) + pairs + 3) / 4 * 4;
+}
 __device__ __forceinline__ MoeLists moe_lists_at(const MoeLayer& a, void* lds) {
   int* w = reinterpret_cast<int*>(lds);
   const int pairs = a.tokens * a.top_k;
-  return MoeLists{w, w + pairs, w + pairs + a.experts, w + pairs + 2 * a.experts};
+  int* const exponent = w + pairs + 2 * a.experts + 1;
+  return MoeLists{w,        w + pairs, w + pairs + a.experts, w + pairs + 2 * a.experts,
+                  exponent, reinterpret_cast<float*>(exponent + (pairs > kMoeMaxTokens ? pairs : kMoeMaxTokens))};
 }
 // CHOOSE: from the logits (scratch: tokens * experts words of 64 bits in LDS).
 template <bool CHOOSE>
@@ -262,23 +269,27 @@ __device__ __forceinline__ int moe_pair(const MoeLayer& a, const MoeLists& s, in
 // own, and accesses bound the kernels (0.82 a clock and CU, 16 tokens, 2 of 8
 // experts of 4096 x 14336: 141 us up, 140 us down).  So a wave loads whole lines,
 // 8 lanes a row's 128 bytes, and turns them round in LDS of its own, where no
-// other wave waits for it; chunks of 16 bytes lie at their number xor the row's,
-// which spreads both the writes and the reads over the banks.  The next unit's
-// loads are under way meanwhile.
+// other wave waits for it; rows are padded by 16 bytes, which spreads the reads of
+// 8 rows over the banks.  The next units' loads are under way meanwhile.
 
-constexpr int kSlots = 8;  // columns in LDS at a time
-
-// In LDS, of one wave.
-template <int NR, int P>
+// In LDS, of one wave.  NS: columns in LDS at a time.
+template <int NR, int NS, int P>
 struct MoeStage {
-  u32x4 codes[NR][16][8];       // row, chunk of 32 values
-  uint32_t scales[NR][16][4];   // row, 4 groups of 16
-  u32x4 columns[P][kSlots][32]; // column, chunk of 8 values
+  u32x4 codes[NR][16][8 + 1];       // row, chunk of 32 values
+  uint32_t scales[NR][16][4];       // row, 4 groups of 16
+  u32x4 columns[P][NS][32 + 1]; // column, chunk of 8 values
 };
 
 // One unit's weights on their way: lane l has chunk l % 8 of rows l / 8 and l / 8
-// + 8, and the scales of row l / 4, groups 4 (l % 4) ...  WHOLE: rows are whole
-// 64s and scales whole dwords.  Past the end of a row scales are 0, and so are its weights.
+// + 8, and the scales of row l / 4, groups 4 (l % 4) ..  WHOLE: rows are whole
+// 64s and scales whole dwords.
+//
+// No branch stands between a wave's loads, here and below: behind one the compiler
+// cannot count what is on its way, and waits for all of it.  So a lane past a
+// row's end loads the row's beginning; its weights become 0 by their scales when
+// they are staged (MoeStage's columns may hold anything there that is in their row
+// anyway), and columns that are too many are the last one again.  Addresses are
+// one of the wave and 32 bits of the lane.
 template <int NR>
 struct MoeWeights {
   u32x4 c[NR][2];
@@ -288,104 +299,108 @@ template <int NR, bool WHOLE>
 __device__ __forceinline__ void moe_load(MoeWeights<NR>& w, const uint8_t* codes, const uint8_t* scales, const int64_t (&row0)[NR],
                                          int inner, int unit) {
   const int lane = threadIdx.x & 63;
-  const int from = unit * kUnit + 32 * (lane & 7), group = unit * (kUnit / 16) + 4 * (lane & 3), groups = inner / 16;
+  const uint32_t row_bytes = inner / 2, groups = inner / 16;
+  const int from = unit * kUnit + 32 * (lane & 7), group = unit * (kUnit / 16) + 4 * (lane & 3);
+  if constexpr (WHOLE) {
+    const uint32_t code_at = (lane >> 3) * row_bytes + (from < inner ? 16 * (lane & 7) : 0);
+    const uint32_t code_at2 = code_at + 8 * row_bytes;
+    const uint32_t scale_at = (lane >> 2) * groups + (group < (int)groups ? 4 * (lane & 3) : 0);
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const uint8_t* p = codes + (row0[r] + (lane >> 3) + 8 * d) * (inner / 2) + from / 2;
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (WHOLE ? from < inner : from + 32 <= inner) {
-        v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(p));
-      } else if (!WHOLE && from < inner) {
-        const u32x2 half = *reinterpret_cast<const u32x2*>(p);
-        v.x = half.x;
-        v.y = half.y;
-      }
-      w.c[r][d] = v;
+    for (int r = 0; r < NR; ++r) {
+      const uint8_t* c = codes + row0[r] * row_bytes + unit * (kUnit / 2);
+      const uint8_t* s = scales + row0[r] * groups + unit * (kUnit / 16);
+      w.c[r][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + code_at));
+      w.c[r][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + code_at2));
+      w.s[r] = *reinterpret_cast<const uint32_t*>(s + scale_at);  // 8 units share a line: kept
     }
-    const uint8_t* p = scales + (row0[r] + (lane >> 2)) * groups + group;
-    w.s[r] = 0u;
-    if constexpr (WHOLE) {
-      if (group < groups) w.s[r] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
-    } else {
+  } else {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const uint8_t* s = scales + (row0[r] + (lane >> 2)) * groups + group;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const uint8_t* p = codes + (row0[r] + (lane >> 3) + 8 * d) * row_bytes + from / 2;
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (from + 32 <= inner) {
+          v = *reinterpret_cast<const u32x4_8*>(p);
+        } else if (from < inner) {
+          const u32x2 half = *reinterpret_cast<const u32x2*>(p);
+          v.x = half.x;
+          v.y = half.y;
+        }
+        w.c[r][d] = v;
+      }
+      w.s[r] = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (group + i < groups) w.s[r] |= (uint32_t)p[i] << (8 * i);
+        if (group + i < (int)groups) w.s[r] |= (uint32_t)s[i] << (8 * i);
     }
   }
 }
-template <int NR, int P>
-__device__ __forceinline__ void moe_stage(MoeStage<NR, P>& l, const MoeWeights<NR>& w) {
+template <bool WHOLE, int NR, int NS, int P>
+__device__ __forceinline__ void moe_stage(MoeStage<NR, NS, P>& l, const MoeWeights<NR>& w, int inner, int unit) {
   const int lane = threadIdx.x & 63;
+  const bool there = !WHOLE || unit * kUnit + 64 * (lane & 3) < inner;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
 #pragma unroll
-    for (int d = 0; d < 2; ++d) l.codes[r][(lane >> 3) + 8 * d][(lane & 7) ^ (lane >> 3)] = w.c[r][d];
-    l.scales[r][lane >> 2][lane & 3] = w.s[r];
+    for (int d = 0; d < 2; ++d) l.codes[r][(lane >> 3) + 8 * d][lane & 7] = w.c[r][d];
+    l.scales[r][lane >> 2][lane & 3] = there ? w.s[r] : 0u;
   }
 }
 
-// kSlots columns of x pieces of a unit on their way: lane l has chunk l % 32 of
+// NS columns of x pieces of a unit on their way: lane l has chunk l % 32 of
 // columns l / 32, l / 32 + 2 ..
-template <int P>
+template <int NS, int P>
 struct MoeColumns {
-  u32x4 v[P][kSlots / 2];
+  u32x4 v[P][NS / 2];
 };
-// `at`: where this lane's columns begin; `count` of them are there, of `inner`
-// values, a piece `plane` behind the other.
-template <int P>
-__device__ __forceinline__ void moe_load(MoeColumns<P>& x, const uint16_t* base, int64_t plane, const int (&at)[kSlots / 2], int count,
-                                         int inner, int unit) {
-  const int from = unit * kUnit + 8 * (threadIdx.x & 31);
-  const bool there = from < inner;
+// `at`: where this lane's columns begin, of `inner` values; a piece is `plane` behind the other.
+template <int NS, int P>
+__device__ __forceinline__ void moe_load(MoeColumns<NS, P>& x, const uint16_t* base, int64_t plane, const int (&at)[NS / 2], int inner,
+                                         int unit) {
+  const uint32_t chunk = threadIdx.x & 31;
+  const uint32_t from = unit * kUnit + 8 * (int)chunk < inner ? 8 * chunk : 0;
 #pragma unroll
-  for (int i = 0; i < kSlots / 2; ++i)
-    if (2 * i < count) {
+  for (int p = 0; p < P; ++p) {
+    const uint16_t* b = base + p * plane + unit * kUnit;
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        x.v[p][i] = u32x4{0u, 0u, 0u, 0u};
-        if (there) x.v[p][i] = *reinterpret_cast<const u32x4*>(base + p * plane + at[i] + from);
-      }
-    }
+    for (int i = 0; i < NS / 2; ++i) x.v[p][i] = *reinterpret_cast<const u32x4*>(b + (uint32_t)(at[i] + from));
+  }
 }
-template <int NR, int P>
-__device__ __forceinline__ void moe_stage(MoeStage<NR, P>& l, const MoeColumns<P>& x, int count) {
+template <int NR, int NS, int P>
+__device__ __forceinline__ void moe_stage(MoeStage<NR, NS, P>& l, const MoeColumns<NS, P>& x) {
   const int lane = threadIdx.x & 63, half = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < kSlots / 2; ++i)
-    if (2 * i < count) {
+  for (int i = 0; i < NS / 2; ++i)
 #pragma unroll
-      for (int p = 0; p < P; ++p) l.columns[p][2 * i + half][(lane & 31) ^ (2 * i + half)] = x.v[p][i];
-    }
+    for (int p = 0; p < P; ++p) l.columns[p][2 * i + half][lane & 31] = x.v[p][i];
 }
 
-// kSlots columns of h on their way, float32: lane l has values 4 l .. 4 l + 3 of
-// each.  They become pieces when they are staged.  row: slot i's pair, in lane i.
+// NS columns of h on their way, float32: lane l has values 4 l .. 4 l + 3 of each.
+// They become pieces when they are staged.  row, exponent: of slot i, in lane i.
+template <int NS>
 struct MoeHidden {
-  f32x4 v[kSlots];
+  f32x4 v[NS];
 };
-__device__ __forceinline__ void moe_load(MoeHidden& x, const float* base, int row, int count, int inner, int unit) {
-  const int from = unit * kUnit + 4 * (threadIdx.x & 63);
-  const bool there = from < inner;
+template <int NS>
+__device__ __forceinline__ void moe_load(MoeHidden<NS>& x, const float* base, int row, int inner, int unit) {
+  const int from = 4 * (threadIdx.x & 63);
+  const uint32_t at = unit * kUnit + from < inner ? from : 0;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i)
-    if (i < count) {
-      x.v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      const float* p = base + (int64_t)__builtin_amdgcn_readlane(row, i) * inner;
-      if (there) x.v[i] = *reinterpret_cast<const f32x4*>(p + from);
-    }
+  for (int i = 0; i < NS; ++i)
+    x.v[i] = *reinterpret_cast<const f32x4*>(base + (int64_t)__builtin_amdgcn_readlane(row, i) * inner + unit * kUnit + at);
 }
-template <int P>
-__device__ __forceinline__ void moe_stage(MoeStage<1, P>& l, const MoeHidden& x, int exponent, int count) {
+template <int NS, int P>
+__device__ __forceinline__ void moe_stage(MoeStage<1, NS, P>& l, const MoeHidden<NS>& x, int exponent, int count) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i)
+  for (int i = 0; i < NS; ++i)
     if (i < count) {
       u32x2 piece[P];
       moe_pieces<P>({x.v[i][0], x.v[i][1], x.v[i][2], x.v[i][3]}, __builtin_amdgcn_readlane(exponent, i), piece);
 #pragma unroll
-      for (int p = 0; p < P; ++p) reinterpret_cast<u32x2*>(&l.columns[p][i][(lane >> 1) ^ i])[lane & 1] = piece[p];
+      for (int p = 0; p < P; ++p) reinterpret_cast<u32x2*>(l.columns[p][i])[lane] = piece[p];
     }
 }
 
@@ -407,8 +422,8 @@ __device__ __forceinline__ f16x8 moe_decode8(uint32_t w, _Float16 s) {
 // The products of what is staged.  Lane l has row l % 16 and values 64 (l / 16) ..
 // + 63 of the unit on both sides.  slot[m]: this lane's column of tile m among
 // those staged, or -1: it meets zeros.  tiles: which tiles have any.
-template <int NR, int MT, int P>
-__device__ __forceinline__ void moe_products(const MoeStage<NR, P>& l, const int (&slot)[MT], uint32_t tiles,
+template <int NR, int MT, int NS, int P>
+__device__ __forceinline__ void moe_products(const MoeStage<NR, NS, P>& l, const int (&slot)[MT], uint32_t tiles,
                                              f32x4 (&acc)[NR][MT]) {
   const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
   f16x2 scale[NR][2];
@@ -419,10 +434,25 @@ __device__ __forceinline__ void moe_products(const MoeStage<NR, P>& l, const int
     scale[r][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)s, 1.0f, false);
     scale[r][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)s, 1.0f, true);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) codes[r][j] = l.codes[r][row][(2 * quarter + j) ^ (row & 7)];
+    for (int j = 0; j < 2; ++j) codes[r][j] = l.codes[r][row][2 * quarter + j];
   }
+  // The columns of the next step are read while this one's are multiplied; the
+  // order is fixed, as all eight steps' would be read at once otherwise, for a
+  // third of the registers.
+  u32x4 b[2][MT][P];
+  auto read = [&](int i) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        b[i & 1][m][p] = l.columns[p][max(slot[m], 0)][8 * quarter + i];
+      }
+  };
+  read(0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    if (i < 7) read(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
     f16x8 a[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) a[r] = moe_decode8(codes[r][i >> 2][i & 3], (i & 2) ? scale[r][i >> 2].y : scale[r][i >> 2].x);
@@ -431,14 +461,14 @@ __device__ __forceinline__ void moe_products(const MoeStage<NR, P>& l, const int
       if (MT > 1 && !(tiles >> m & 1u)) continue;
 #pragma unroll
       for (int p = P - 1; p >= 0; --p) {  // the small pieces first
-        const int at = max(slot[m], 0);
-        u32x4 v = l.columns[p][at][(8 * quarter + i) ^ at];
+        u32x4 v = b[i & 1][m][p];
         if (slot[m] < 0) v = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int r = 0; r < NR; ++r)
           acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r], __builtin_bit_cast(f16x8, v), acc[r][m], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -458,238 +488,332 @@ __device__ __forceinline__ int moe_rank(const MoeTokens& k, int t) {
   return __builtin_popcountll(k.live & ((1ull << t) - 1));
 }
 // This lane's column of each tile among those from `from` on, and the tiles that have any.
-template <int MT>
+template <int NS, int MT>
 __device__ __forceinline__ uint32_t moe_slots(const MoeTokens& k, int from, int (&slot)[MT]) {
   uint32_t tiles = 0u;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int t = 16 * m + (threadIdx.x & 15), at = moe_rank(k, t) - from;
-    slot[m] = (k.live >> t & 1u) && at >= 0 && at < kSlots ? at : -1;
+    slot[m] = (k.live >> t & 1u) && at >= 0 && at < NS ? at : -1;
     tiles |= __any(slot[m] >= 0) ? 1u << m : 0u;
   }
   return tiles;
 }
 
-constexpr int kUpWaves = 4;
+constexpr int kUpWaves = 4, kUpAhead = 2, kUpSlots = 8;
 
-// 16 gate rows and the 16 up rows that go with them, of one expert: a workgroup,
-// its waves each a share of the inner values.  CHOOSE: moe_choose_inside, and the
-// last workgroup writes the choice.  PX: pieces of x here (1 or 2).
+// 16 gate rows and the 16 up rows that go with them, of one expert, are a job; a
+// workgroup takes every so many of them, its waves each a share of the inner
+// values.  Weights are on their way two units ahead, columns one, over the jobs'
+// ends; at a job's end one wave in turn joins the four sums while the others go
+// on.  CHOOSE: moe_choose_inside, and the last workgroup writes the
+// choice.  PX: pieces of x here (1 or 2).
 template <int MT, int PX, bool WHOLE, bool CHOOSE>
-__global__ void __launch_bounds__(64 * kUpWaves, MT * PX == 1 ? 4 : MT * PX == 2 ? 3 : 2) moe_up_kernel(MoeLayer a, const uint16_t* x) {
+__global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_kernel(MoeLayer a, const uint16_t* x) {
+  constexpr int NS = kUpSlots;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ int row_of[kMoeMaxTokens];  // of the expert's tokens
+  __shared__ int rows_of[kUpWaves][2][kMoeMaxTokens];  // of this job's expert and the next one's: its tokens
   const MoeLists lists = moe_lists_at(a, lds);
   uint8_t* const mine = lds + 4 * moe_list_words(a.tokens * a.top_k, a.experts);
+  if (threadIdx.x < a.tokens) lists.exponent[threadIdx.x] = a.x_exponent ? a.x_exponent[threadIdx.x] : 0;
   moe_lists<CHOOSE>(a, lists, reinterpret_cast<uint64_t*>(mine));
-  if (CHOOSE && blockIdx.x == gridDim.x - 1) {
+  const int groups = (int)gridDim.x - (CHOOSE ? 1 : 0);
+  if (CHOOSE && (int)blockIdx.x == groups) {
     moe_weigh(a, 0, a.tokens, lists.idx);
     return;
   }
-  const int tiles = a.f / 16;
-  const int which = blockIdx.x / tiles, f0 = (blockIdx.x - which * tiles) * 16;
-  if (which >= *lists.count) return;
-  const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = a.f / 16, jobs = __builtin_amdgcn_readfirstlane(*lists.count) * tiles;
   const int units = (a.k + kUnit - 1) / kUnit;
-  const int64_t row0[2] = {(int64_t)expert * 2 * a.f + f0, (int64_t)expert * 2 * a.f + a.f + f0};
-  MoeWeights<2> w;
-  if (wave < units) moe_load<2, WHOLE>(w, a.up_codes, a.up_scales, row0, a.k, wave);
-  const int my_pair = moe_pair(a, lists, lane, expert);
-  const MoeTokens tokens = moe_tokens(my_pair);
-  if (wave == 0 && my_pair >= 0) row_of[moe_rank(tokens, lane)] = lane;
-  __syncthreads();
-  MoeStage<2, PX>& stage = reinterpret_cast<MoeStage<2, PX>*>(mine)[wave];
-  f32x4 acc[2][MT] = {};
-  MoeColumns<PX> columns;
   const int64_t plane = (int64_t)a.tokens * a.k;
-  auto place = [&](int from, int(&at)[kSlots / 2]) {
-#pragma unroll
-    for (int i = 0; i < kSlots / 2; ++i) at[i] = row_of[min(from + 2 * i + (lane >> 5), tokens.count - 1)] * a.k;
+  using Stage = MoeStage<2, NS, PX>;
+  Stage& stage = reinterpret_cast<Stage*>(mine)[wave];
+  f32x4* const parts = reinterpret_cast<f32x4*>(mine + kUpWaves * sizeof(Stage));  // [wave][2][MT][64]
+  // A job: tile `tile` of the which-th expert.  (All of it in scalar registers.)
+  struct Job {
+    int at, which, tile;
   };
-  int at[kSlots / 2], slot[MT];
-  place(0, at);
-  const uint32_t first = moe_slots<MT>(tokens, 0, slot);
-  if (wave < units) moe_load<PX>(columns, x, plane, at, tokens.count, a.k, wave);
-  for (int u = wave; u < units; u += kUpWaves) {
-    moe_stage<2, PX>(stage, w);
-    moe_stage<2, PX>(stage, columns, tokens.count);
-    moe_settle();
-    if (u + kUpWaves < units) {
-      moe_load<PX>(columns, x, plane, at, tokens.count, a.k, u + kUpWaves);
-      moe_load<2, WHOLE>(w, a.up_codes, a.up_scales, row0, a.k, u + kUpWaves);
+  const int step_which = __builtin_amdgcn_readfirstlane(groups / tiles), step_tile = groups - step_which * tiles;
+  auto advance = [&](Job& j) {
+    j.at += groups;
+    j.which += step_which;
+    j.tile += step_tile;
+    if (j.tile >= tiles) {
+      j.tile -= tiles;
+      ++j.which;
     }
-    moe_products<2, MT, PX>(stage, slot, first, acc);
-    for (int from = kSlots; from < tokens.count; from += kSlots) {  // more tokens than have room
-      MoeColumns<PX> more;
-      int at2[kSlots / 2], slot2[MT];
-      place(from, at2);
-      moe_load<PX>(more, x, plane, at2, tokens.count - from, a.k, u);
-      moe_settle();
-      moe_stage<2, PX>(stage, more, tokens.count - from);
-      moe_settle();
-      const uint32_t some = moe_slots<MT>(tokens, from, slot2);
-      moe_products<2, MT, PX>(stage, slot2, some, acc);
+  };
+  auto expert_of = [&](const Job& j) { return __builtin_amdgcn_readfirstlane(lists.list[j.which]); };
+
+  // The sums of a job, number `n` of this workgroup's.
+  auto finish = [&](const Job& job, int n, const f32x4(&acc)[2][MT]) {
+    f32x4* const part = parts;
+    if (n > 0) lds_barrier();  // the last job's are read
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) part[((wave * 2 + r) * MT + m) * 64 + lane] = acc[r][m];
+    lds_barrier();
+    const int expert = expert_of(job), f0 = job.tile * 16;
+    for (int m = (wave + n) % kUpWaves; m < MT; m += kUpWaves) {
+      const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
+      const int e = lists.exponent[min(t, a.tokens - 1)];
+      const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
+      f32x4 g = part[m * 64 + lane], v = part[(MT + m) * 64 + lane];
+#pragma unroll
+      for (int i = 1; i < kUpWaves; ++i) {
+        g += part[((i * 2) * MT + m) * 64 + lane];
+        v += part[((i * 2 + 1) * MT + m) * 64 + lane];
+      }
+      f32x4 h;
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x1 = __builtin_ldexpf(g[i] * factor, e), x2 = __builtin_ldexpf(v[i] * factor, e);
+        h[i] = x1 / (1.0f + expf(-x1)) * x2;
+        top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+      }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      if (p < 0) continue;
+      *reinterpret_cast<f32x4*>(a.hidden + (int64_t)p * a.f + f0 + 4 * (lane >> 4)) = h;
+      if (lane < 16) atomicMax(a.h_top + p, top);  // (in any order the same)
     }
-    moe_settle();
+  };
+
+  if ((int)blockIdx.x >= jobs) return;
+  Job job;
+  job.at = blockIdx.x;
+  job.which = __builtin_amdgcn_readfirstlane(job.at / tiles);
+  job.tile = job.at - job.which * tiles;
+  if (wave >= units) {  // fewer units than waves
+    const f32x4 none[2][MT] = {};
+    for (int n = 0; job.at < jobs; advance(job), ++n) finish(job, n, none);
+    return;
   }
-  __syncthreads();
-  f32x4* part = reinterpret_cast<f32x4*>(mine);  // [wave][2][MT][64]
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) part[((wave * 2 + r) * MT + m) * 64 + lane] = acc[r][m];
-  __syncthreads();
-  const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
-  for (int m = wave; m < MT; m += kUpWaves) {
-    const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
-    const int e = a.x_exponent && t < a.tokens ? a.x_exponent[t] : 0;
-    f32x4 g = part[m * 64 + lane], v = part[(MT + m) * 64 + lane];
-#pragma unroll
-    for (int i = 1; i < kUpWaves; ++i) {
-      g += part[((i * 2) * MT + m) * 64 + lane];
-      v += part[((i * 2 + 1) * MT + m) * 64 + lane];
+
+  // The unit whose weights are loaded next; the last one again when all are.
+  Job w_job = job;
+  int w_unit = wave;
+  int64_t w_row = (int64_t)expert_of(job) * 2 * a.f + job.tile * 16;
+  auto load_weights = [&](MoeWeights<2>& to) {
+    moe_load<2, WHOLE>(to, a.up_codes, a.up_scales, {w_row, w_row + a.f}, a.k, w_unit);
+    if (w_unit + kUpWaves < units) {
+      w_unit += kUpWaves;
+    } else if (w_job.at + groups < jobs) {
+      w_unit = wave;
+      advance(w_job);
+      w_row = (int64_t)expert_of(w_job) * 2 * a.f + w_job.tile * 16;
     }
-    f32x4 h;
-    uint32_t top = 0u;
+  };
+
+  // The tokens of a job's expert, and where this lane's columns of x begin.
+  MoeTokens tokens, next_tokens;
+  int at[NS / 2];
+  auto place = [&](const MoeTokens& k, const int* row_of, int from, int(&to)[NS / 2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x1 = __builtin_ldexpf(g[i] * factor, e), x2 = __builtin_ldexpf(v[i] * factor, e);
-      h[i] = x1 / (1.0f + expf(-x1)) * x2;
-      top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < NS / 2; ++i) to[i] = row_of[min(from + 2 * i + (lane >> 5), k.count - 1)] * a.k;
+  };
+  auto open = [&](const Job& j, MoeTokens& k, int* row_of) {
+    const int pair = moe_pair(a, lists, lane, expert_of(j));
+    k = moe_tokens(pair);
+    moe_settle();
+    if (pair >= 0) row_of[moe_rank(k, lane)] = lane;
+    moe_settle();
+    place(k, row_of, 0, at);
+  };
+  MoeWeights<2> w[kUpAhead];
+  MoeColumns<NS, PX> columns;
+  int u = wave, n = 0;
+  load_weights(w[0]);
+  open(job, tokens, rows_of[wave][0]);
+  moe_load<NS, PX>(columns, x, plane, at, a.k, u);
+  load_weights(w[1]);
+  int slot[MT];
+  uint32_t first = moe_slots<NS, MT>(tokens, 0, slot);
+  f32x4 acc[2][MT] = {};
+  for (;;) {
+#pragma unroll
+    for (int j = 0; j < kUpAhead; ++j) {
+      moe_stage<WHOLE>(stage, w[j], a.k, u);
+      moe_stage(stage, columns);
+      moe_settle();
+      const bool last = u + kUpWaves >= units, more_jobs = job.at + groups < jobs;
+      if (last && more_jobs) {
+        Job next = job;
+        advance(next);
+        open(next, next_tokens, rows_of[wave][(n + 1) & 1]);
+      }
+      moe_load<NS, PX>(columns, x, plane, at, a.k, last ? wave : u + kUpWaves);
+      load_weights(w[j]);
+      moe_products<2, MT>(stage, slot, first, acc);
+      for (int from = NS; from < tokens.count; from += NS) {  // more tokens than have room
+        MoeColumns<NS, PX> more;
+        int at2[NS / 2], slot2[MT];
+        place(tokens, rows_of[wave][n & 1], from, at2);
+        moe_load<NS, PX>(more, x, plane, at2, a.k, u);
+        moe_settle();
+        moe_stage(stage, more);
+        moe_settle();
+        const uint32_t some = moe_slots<NS, MT>(tokens, from, slot2);
+        moe_products<2, MT>(stage, slot2, some, acc);
+      }
+      moe_settle();
+      u += kUpWaves;
+      if (last) {
+        finish(job, n, acc);
+        if (!more_jobs) return;
+        advance(job);
+        ++n;
+        u = wave;
+        tokens = next_tokens;
+        first = moe_slots<NS, MT>(tokens, 0, slot);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
     }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    if (p < 0) continue;
-    *reinterpret_cast<f32x4*>(a.hidden + (int64_t)p * a.f + f0 + 4 * (lane >> 4)) = h;
-    if (lane < 16) atomicMax(a.h_top + p, top);  // (in any order the same)
   }
 }
 
 // Waves of a workgroup of the down products: what has room in LDS, and in registers.
 constexpr int down_waves(int MT, int PH) { return MT > 2 || (MT == 2 && PH == 2) ? 8 : 12; }
+constexpr int kDownAhead = 3;
 
 // 16 columns of the output for all tokens: a workgroup, its waves in turn the
 // units of all chosen experts' rows: what they read at a time lies together.
-template <int DT, int MT, int PH, bool WHOLE>
+// Weights are on their way three units ahead, columns one, over the experts' ends.
+template <int DT, int MT, int NS, int PH, bool WHOLE>
 __global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLayer a) {
   constexpr int WAVES = down_waves(MT, PH);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ int rows_of[WAVES][kMoeMaxTokens];
+  __shared__ int rows_of[WAVES][2][kMoeMaxTokens];  // of this expert and the next one: its pairs
   const MoeLists lists = moe_lists_at(a, lds);
   uint8_t* const mine = lds + 4 * moe_list_words(a.tokens * a.top_k, a.experts);
+  for (int p = threadIdx.x; p < a.tokens * a.top_k; p += 64 * WAVES) {
+    lists.exponent[p] = moe_exponent(a.h_top[p]);
+    lists.weight[p] = a.expert_weights[p];
+  }
   moe_lists<false>(a, lists, nullptr);
   const int n0 = blockIdx.x * 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int units = (a.f + kUnit - 1) / kUnit, all = *lists.count * units;
-  int* const row_of = rows_of[wave];
+  const int units = (a.f + kUnit - 1) / kUnit, all = __builtin_amdgcn_readfirstlane(*lists.count) * units;
   f32x4 total[MT] = {};
   if (wave < all) {
-    MoeWeights<1> w[2];
-    // the unit whose weights are loaded next: of all, and of its expert
-    int next = wave, next_which = wave / units, next_u = wave - next_which * units;
-    int64_t next_row[1];
-    auto seek = [&]() { next_row[0] = (int64_t)__builtin_amdgcn_readfirstlane(lists.list[next_which]) * a.k + n0; };
-    auto load = [&](MoeWeights<1>& x) {
-      if (next >= all) return;
-      moe_load<1, WHOLE>(x, a.down_codes, a.down_scales, next_row, a.f, next_u);
-      next += WAVES;
-      next_u += WAVES;
-      if (next_u >= units && next < all) {
-        do {
-          next_u -= units;
-          ++next_which;
-        } while (next_u >= units);
-        seek();
+    auto expert_of = [&](int which) { return __builtin_amdgcn_readfirstlane(lists.list[which]); };
+    int which = __builtin_amdgcn_readfirstlane(wave / units), u = wave - which * units;
+    // the unit whose weights are loaded next, of all and of its expert; the last one again when all are
+    int w_next = wave, w_which = which, w_unit = u;
+    int64_t w_row = (int64_t)expert_of(which) * a.k + n0;
+    auto load_weights = [&](MoeWeights<1>& to) {
+      moe_load<1, WHOLE>(to, a.down_codes, a.down_scales, {w_row}, a.f, w_unit);
+      if (w_next + WAVES < all) {
+        w_next += WAVES;
+        w_unit += WAVES;
+        if (w_unit >= units) {
+          do {
+            w_unit -= units;
+            ++w_which;
+          } while (w_unit >= units);
+          w_row = (int64_t)expert_of(w_which) * a.k + n0;
+        }
       }
     };
-    seek();
-    load(w[0]);
+    MoeWeights<1> w[kDownAhead];
+    load_weights(w[0]);
 
-    MoeStage<1, PH>& stage = reinterpret_cast<MoeStage<1, PH>*>(mine)[wave];
-    MoeHidden hidden;
-    MoeTokens tokens;
-    int slot[MT], row = 0, exponent = 0;  // lane i: slot i's pair and its power of two
+    using Stage = MoeStage<1, NS, PH>;
+    Stage& stage = reinterpret_cast<Stage*>(mine)[wave];
+    MoeHidden<NS> hidden;
+    MoeTokens tokens, next_tokens;
+    int slot[MT], row = 0, exponent = 0, next_exponent = 0, n = 0;  // lane i: slot i's pair and its power of two
     uint32_t first = 0u;
-    float weight[MT];
     f32x4 acc[1][MT];
-    int which = wave / units, u = wave - which * units, left = (all - wave + WAVES - 1) / WAVES;
-    auto place = [&](int from, int& to, int& e) {
-      to = row_of[min(from + (lane & (kSlots - 1)), tokens.count - 1)];
-      e = moe_exponent(a.h_top[to]);
+    int left = __builtin_amdgcn_readfirstlane((all - wave + WAVES - 1) / WAVES);
+    auto place = [&](const MoeTokens& k, const int* row_of, int from, int& to, int& e) {
+      to = row_of[min(from + (lane & 7), k.count - 1)];
+      e = lists.exponent[to];
     };
-    auto begin = [&]() {  // the columns of expert `which`
-      const int expert = __builtin_amdgcn_readfirstlane(lists.list[which]);
+    auto open = [&](int expert, MoeTokens& k, int* row_of, int& e) {
       const int pair = moe_pair(a, lists, lane, expert);
-      tokens = moe_tokens(pair);
+      k = moe_tokens(pair);
       moe_settle();
-      if (pair >= 0) row_of[moe_rank(tokens, lane)] = pair;
+      if (pair >= 0) row_of[moe_rank(k, lane)] = pair;
       moe_settle();
-      place(0, row, exponent);
-      moe_load(hidden, a.hidden, row, tokens.count, a.f, u);
-      first = moe_slots<MT>(tokens, 0, slot);
+      place(k, row_of, 0, row, e);
+    };
+    auto begin = [&]() {
+      first = moe_slots<NS, MT>(tokens, 0, slot);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[0][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    auto end = [&]() {  // adds the sums of expert `which`
+      const int expert = expert_of(which);
       const float factor = global_decode(a.down_global ? a.down_global + expert : nullptr);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
-        weight[m] = 0.0f;
-        if (p >= 0)  // an expert may stand twice among a token's
-          for (int q = p; q < (t + 1) * a.top_k; ++q)
-            if (lists.idx[q] == expert) weight[m] += a.expert_weights[q];
-        weight[m] *= factor;
-        acc[0][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-    };
-    auto end = [&]() {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
         const int t = 16 * m + (lane & 15);
-        const bool live = tokens.live >> t & 1u;
-        const int e = live ? moe_exponent(a.h_top[row_of[moe_rank(tokens, t)]]) : 0;
+        if (!(tokens.live >> t & 1u)) continue;
+        const int p = rows_of[wave][n & 1][moe_rank(tokens, t)];
+        float weight = 0.0f;
+        for (int q = p; q < (t + 1) * a.top_k; ++q)  // an expert may stand twice among a token's
+          if (lists.idx[q] == expert) weight += lists.weight[q];
+        weight *= factor;
+        const int e = lists.exponent[p];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          total[m][i] = live ? total[m][i] + weight[m] * __builtin_ldexpf(acc[0][m][i], e) : total[m][i];
+        for (int i = 0; i < 4; ++i) total[m][i] += weight * __builtin_ldexpf(acc[0][m][i], e);
       }
     };
-    begin();
-    load(w[1]);
-    while (left > 0) {
+    open(expert_of(which), tokens, rows_of[wave][0], exponent);
+    moe_load(hidden, a.hidden, row, a.f, u);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (left <= 0) break;
-        moe_stage<1, PH>(stage, w[j]);
-        moe_stage<PH>(stage, hidden, exponent, tokens.count);
+    for (int j = 1; j < kDownAhead; ++j) load_weights(w[j]);
+    begin();
+    for (;;) {
+#pragma unroll
+      for (int j = 0; j < kDownAhead; ++j) {
+        moe_stage<WHOLE>(stage, w[j], a.f, u);
+        moe_stage(stage, hidden, exponent, tokens.count);
         moe_settle();
         const int now = u;
-        --left;
-        u += WAVES;
-        const bool over = u >= units;
-        if (!over && left > 0) moe_load(hidden, a.hidden, row, tokens.count, a.f, u);
-        load(w[j]);
-        moe_products<1, MT, PH>(stage, slot, first, acc);
-        for (int from = kSlots; from < tokens.count; from += kSlots) {  // more tokens than have room
-          MoeHidden more;
+        const bool more = --left > 0;
+        int next = which;
+        if (more) {
+          u += WAVES;
+          while (u >= units) {
+            u -= units;
+            ++next;
+          }
+          if (next != which) open(expert_of(next), next_tokens, rows_of[wave][(n + 1) & 1], next_exponent);
+        }
+        moe_load(hidden, a.hidden, row, a.f, u);
+        load_weights(w[j]);
+        moe_products<1, MT>(stage, slot, first, acc);
+        for (int from = NS; from < tokens.count; from += NS) {  // more tokens than have room
+          MoeHidden<NS> some;
           int row2, e2, slot2[MT];
-          place(from, row2, e2);
-          moe_load(more, a.hidden, row2, tokens.count - from, a.f, now);
+          place(tokens, rows_of[wave][n & 1], from, row2, e2);
+          moe_load(some, a.hidden, row2, a.f, now);
           moe_settle();
-          moe_stage<PH>(stage, more, e2, tokens.count - from);
+          moe_stage(stage, some, e2, tokens.count - from);
           moe_settle();
-          const uint32_t some = moe_slots<MT>(tokens, from, slot2);
-          moe_products<1, MT, PH>(stage, slot2, some, acc);
+          const uint32_t tiles = moe_slots<NS, MT>(tokens, from, slot2);
+          moe_products<1, MT>(stage, slot2, tiles, acc);
         }
         moe_settle();
-        if (over && left > 0) {
-          end();
-          do {
-            u -= units;
-            ++which;
-          } while (u >= units);
+        if (!more || next != which) end();
+        if (!more) goto done;
+        if (next != which) {
+          which = next;
+          ++n;
+          tokens = next_tokens;
+          exponent = next_exponent;
           begin();
         }
       }
     }
-    end();
+  done:;
   }
   __syncthreads();
   f32x4* part = reinterpret_cast<f32x4*>(mine);  // [wave][MT][64]
@@ -741,34 +865,35 @@ hipError_t moe_allow_lds(K* kernel, size_t bytes, std::atomic<bool> (&set)[64]) 
 }
 
 size_t moe_lists_bytes(const MoeLayer& a) { return 4 * (size_t)moe_list_words(a.tokens * a.top_k, a.experts); }
-constexpr size_t kMoeMaxListBytes = 4 * moe_list_words(kMoeMaxPairs, kMoeMaxExperts);
+constexpr size_t moe_most_list_bytes(int MT) { return 4 * (size_t)moe_list_words(16 * MT * kMoeMaxTopK, kMoeMaxExperts); }
 
 template <int DT, int MT, bool WHOLE, bool CHOOSE>
 hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT) > 0 ? moe_x_pieces(DT) : 1;
-  constexpr size_t staged = kUpWaves * sizeof(MoeStage<2, PX>), joined = kUpWaves * 2 * MT * 1024;
-  constexpr size_t bytes = staged > joined ? staged : joined;
+  constexpr size_t bytes = kUpWaves * (sizeof(MoeStage<2, kUpSlots, PX>) + 2 * MT * 1024);
   static_assert(bytes >= 1024 * 8, "the order of the logits fits");
   static std::atomic<bool> set[64];
-  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, PX, WHOLE, CHOOSE>, bytes + kMoeMaxListBytes, set); e != hipSuccess)
+  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, PX, WHOLE, CHOOSE>, bytes + moe_most_list_bytes(MT), set); e != hipSuccess)
     return e;
   const int pairs = a.tokens * a.top_k, most = pairs < a.experts ? pairs : a.experts;
   const uint16_t* x = moe_x_pieces(DT) > 0 ? a.x_pieces : reinterpret_cast<const uint16_t*>(a.x);
-  moe_up_kernel<MT, PX, WHOLE, CHOOSE>
-      <<<(unsigned)(most * (a.f / 16) + (CHOOSE ? 1 : 0)), 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
+  // as many workgroups as run at once
+  const int jobs = most * (a.f / 16), resident = device_cu_count() * (MT * PX <= 2 ? 3 : 2);
+  const int groups = (jobs < resident ? jobs : resident) + (CHOOSE ? 1 : 0);
+  moe_up_kernel<MT, PX, WHOLE, CHOOSE><<<groups, 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
   return hipGetLastError();
 }
 
-template <int DT, int MT, bool WHOLE>
+template <int DT, int MT, int NS, bool WHOLE>
 hipError_t launch_down(const MoeLayer& a, hipStream_t s) {
   constexpr int PH = moe_h_pieces(DT), WAVES = down_waves(MT, PH);
-  constexpr size_t staged = WAVES * sizeof(MoeStage<1, PH>), joined = WAVES * MT * 1024;
+  constexpr size_t staged = WAVES * sizeof(MoeStage<1, NS, PH>), joined = WAVES * MT * 1024;
   constexpr size_t bytes = staged > joined ? staged : joined;
-  static_assert(bytes + kMoeMaxListBytes + WAVES * kMoeMaxTokens * 4 <= 160 * 1024, "LDS");
+  static_assert(bytes + moe_most_list_bytes(MT) + WAVES * kMoeMaxTokens * 8 <= 160 * 1024, "LDS");
   static std::atomic<bool> set[64];
-  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, PH, WHOLE>, bytes + kMoeMaxListBytes, set); e != hipSuccess)
+  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, NS, PH, WHOLE>, bytes + moe_most_list_bytes(MT), set); e != hipSuccess)
     return e;
-  moe_down_kernel<DT, MT, PH, WHOLE><<<(unsigned)(a.k / 16), 64 * WAVES, bytes + moe_lists_bytes(a), s>>>(a);
+  moe_down_kernel<DT, MT, NS, PH, WHOLE><<<(unsigned)(a.k / 16), 64 * WAVES, bytes + moe_lists_bytes(a), s>>>(a);
   return hipGetLastError();
 }
 
@@ -782,7 +907,10 @@ hipError_t launch_products(const MoeLayer& a, hipStream_t s) {
   }
   if (!inside) e = whole(a.k, a.up_scales) ? launch_up<DT, MT, true, false>(a, s) : launch_up<DT, MT, false, false>(a, s);
   if (e != hipSuccess) return e;
-  return whole(a.f, a.down_scales) ? launch_down<DT, MT, true>(a, s) : launch_down<DT, MT, false>(a, s);
+  if constexpr (MT == 1) {
+    if (a.tokens <= 2) return whole(a.f, a.down_scales) ? launch_down<DT, 1, 2, true>(a, s) : launch_down<DT, 1, 2, false>(a, s);
+  }
+  return whole(a.f, a.down_scales) ? launch_down<DT, MT, 8, true>(a, s) : launch_down<DT, MT, 8, false>(a, s);
 }
 
 template <int DT>
