@@ -847,12 +847,15 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
  *   tree_words  at least max_queries / 64, rounded up
  *   positions   device int32 [tokens], or NULL without a window; taken as at
  *               least L - n and at most L - 1
+ *   workspace   nvfp4_kv_tree_attention_workspace_size() bytes
  *   the other arguments, the numbers and the errors as nvfp4_kv_attention with
- *   query_starts, which must not be NULL here; the workspace is
- *   nvfp4_kv_attention_workspace_size() of the same sizes.
+ *   query_starts, which must not be NULL here.
  * Errors besides: tree_words too small (or of 2^25 or more), NULL or
  * misaligned tree or positions.
  */
+size_t nvfp4_kv_tree_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
+                                              int64_t seqs, int64_t max_queries, int64_t max_context,
+                                              int64_t window);
 nvfp4_status nvfp4_kv_tree_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype dt, int64_t tokens,
                                      int64_t query_heads, int64_t q_token_stride, int64_t q_head_stride,
                                      const int32_t* page_table, int64_t seqs, int64_t table_pages,

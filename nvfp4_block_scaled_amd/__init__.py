@@ -128,6 +128,7 @@ def load_library():
         "nvfp4_kv_attention_workspace_size": (SZ, [C, I64, I64, I64, I64, I64, I64]),
         "nvfp4_kv_attention": (I, [C, P, I, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, ctypes.c_float,
                                    I, I64, P, P, P, SZ, P]),
+        "nvfp4_kv_tree_attention_workspace_size": (SZ, [C, I64, I64, I64, I64, I64, I64]),
         "nvfp4_kv_tree_attention": (I, [C, P, I, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, ctypes.c_float,
                                         P, I64, P, I64, P, P, P, SZ, P]),
     }
@@ -1230,6 +1231,21 @@ def kv_trees(parents):
     return (torch.tensor(rows, dtype=torch.int64).reshape(len(rows), words), torch.tensor(depths, dtype=torch.int32))
 
 
+@functools.lru_cache(maxsize=4096)
+def _kv_tree_bytes(device, pages, page_size, heads, dim, *sizes):
+    """As _kv_attention_bytes."""
+    s = _KVCacheStruct(256, 256, 256, 256, None, None, pages, page_size, heads, dim)
+    with torch.cuda.device(device):
+        return load_library().nvfp4_kv_tree_attention_workspace_size(s, *sizes)
+
+
+def kv_tree_attention_workspace(cache, tokens, query_heads, seqs, max_queries, max_context, window=0):
+    """(workspace, bytes) for nvfp4_kv_tree_attention calls of these sizes."""
+    nbytes = _kv_tree_bytes(cache._gpu, cache.pages, cache.page_size, cache.heads, cache.dim, tokens, query_heads, seqs,
+                            max_queries, max_context, window)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device), nbytes
+
+
 def nvfp4_kv_tree_attention(q, cache, page_table, context_lens, query_starts, tree, max_queries=None, max_context=None,
                             scale=None, positions=None, window=0, return_lse=False, out=None, workspace=None):
     """nvfp4_kv_attention for drafted tokens that form trees.  A sequence's queries are the last n tokens of its
@@ -1272,8 +1288,8 @@ def nvfp4_kv_tree_attention(q, cache, page_table, context_lens, query_starts, tr
         raise ValueError("out must be contiguous and have q's shape, dtype and device")
     lse = torch.empty((tokens, query_heads), dtype=torch.float32, device=cache.device) if return_lse else None
     if workspace is None:
-        nbytes = _kv_attention_bytes(cache._gpu, cache.pages, cache.page_size, cache.heads, cache.dim, tokens,
-                                     query_heads, seqs, max_queries, max_context, window)
+        nbytes = _kv_tree_bytes(cache._gpu, cache.pages, cache.page_size, cache.heads, cache.dim, tokens, query_heads,
+                                seqs, max_queries, max_context, window)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     else:
@@ -1388,5 +1404,6 @@ __all__ = [
     "nvfp4_mx_pack", "mx_qqmm_workspace", "nvfp4_mx_qqmm", "nvfp4_mx_qqmm_packed",
     "nvfp4_mx_quantize_packed", "nvfp4_mx_mm_packed", "MxNormed", "nvfp4_mx_rms_norm", "moe_workspace", "nvfp4_moe", "nvfp4_gather_qmm_indexed",
     "nvfp4_mx_gather_qmm", "KVCache", "kv_cache", "nvfp4_kv_write", "rotation_table", "nvfp4_kv_write_rotated", "nvfp4_kv_read",
-    "kv_attention_workspace", "nvfp4_kv_attention", "kv_trees", "nvfp4_kv_tree_attention",
+    "kv_attention_workspace", "nvfp4_kv_attention", "kv_trees", "kv_tree_attention_workspace",
+    "nvfp4_kv_tree_attention",
 ]

@@ -1481,16 +1481,29 @@ static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, 
   return NVFP4_OK;
 }
 
-size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
-                                         int64_t seqs, int64_t max_queries, int64_t max_context,
-                                         int64_t window) {
-  const char* op = "kv_attention_workspace_size";
+static size_t attend_workspace(const char* op, const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
+                               int64_t seqs, int64_t max_queries, int64_t max_context, int64_t window, bool tree) {
   nvfp4::KvCache c;
   nvfp4::KvAttention a{};
   if (check_kv(op, cache, NVFP4_BF16, tokens, &c) ||
       check_kv_attention(op, c, tokens, query_heads, seqs, max_queries, max_context, window, &a))
     return 0;
-  return tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
+  if (tokens == 0 || seqs == 0) return 0;
+  return tree ? nvfp4::kv_tree_attention_workspace(c, a) : nvfp4::kv_attention_workspace(c, a);
+}
+
+size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
+                                         int64_t seqs, int64_t max_queries, int64_t max_context,
+                                         int64_t window) {
+  return attend_workspace("kv_attention_workspace_size", cache, tokens, query_heads, seqs, max_queries, max_context,
+                          window, false);
+}
+
+size_t nvfp4_kv_tree_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
+                                              int64_t seqs, int64_t max_queries, int64_t max_context,
+                                              int64_t window) {
+  return attend_workspace("kv_tree_attention_workspace_size", cache, tokens, query_heads, seqs, max_queries,
+                          max_context, window, true);
 }
 
 // Both attention calls; `tree` is null for queries at consecutive positions.
@@ -1536,7 +1549,9 @@ static nvfp4_status attend(const char* op, const nvfp4_kv_cache* cache, const vo
       return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tree must be 8-byte, positions 4-byte aligned.", op);
   }
   const StreamDevice on(stream);
-  const size_t need = tokens == 0 || seqs == 0 ? 0 : nvfp4::kv_attention_workspace(c, a);
+  const size_t need = tokens == 0 || seqs == 0 ? 0
+                      : tree                   ? nvfp4::kv_tree_attention_workspace(c, a)
+                                               : nvfp4::kv_attention_workspace(c, a);
   if (tokens > 0 && seqs > 0) {
     if (!q || !out || !context_lens || (max_context > 0 && !page_table))
       return fail(NVFP4_ERR_INVALID_ARGUMENT,

@@ -1034,37 +1034,30 @@ struct KvChunks {
   float* stats;       // [tokens][query_heads][splits][2]: maximum (log2), sum
 };
 
+// 128 rows of sequence b and kv head `head` from row0 on, past the keys [begin,
+// end).  split: which chunk; base: of a tree's part, its first row.
 template <int NG, int SPLIT, bool EXACT, bool TREE>
-__global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1))
-kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
+__device__ __forceinline__ void kv_many_rows(const KvCache& c, const KvAttention& a, const KvChunks& sp, int dt, bool q_vec,
+                                             uint8_t* lds, int b, int head, int row0, const KvRange& rg, int begin, int end,
+                                             int split, bool whole, int64_t base_row) {
   constexpr int DP = 64 * NG, TILE = many_tile(NG), SUB = TILE / 32, STEPS = DP / 16, DB = DP / 32;
   constexpr int KROW = many_k_row(NG), VROW = many_v_row(NG), BUF = TILE * (KROW + VROW);
   constexpr int NEAR = NG * SPLIT <= 4 ? kNearBands : 1;  // (more registers would be spilled)
   constexpr bool BOTH = TILE == 64;  // every thread decodes keys and values; else half of them each
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // four lanes a key: which keys of a buffer exist, with values that are
   // numbers; where some do not, also which exist and which have other values
   __shared__ uint64_t fine[2][4], exists[2][4], odd[2][4];
   __shared__ uint32_t odd_groups[2][256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t thread_of = threadIdx.x;
+  if constexpr (TREE) asm volatile("" : "+v"(thread_of));  // (nothing of it is kept over the runs)
+  const int lane = thread_of & 63, wave = thread_of >> 6;
   const int col = lane & 31, half = lane >> 5;
-  const int b = blockIdx.y;
-  int x = blockIdx.x;
-  const int split = x % sp.splits;
-  x /= sp.splits;
-  const int head = x % c.heads;
-  const int row0 = (sp.row_tiles - 1 - x / c.heads) * kManyRows;  // the longest ranges first
-  const KvRange rg = kv_range<TREE>(a, b, row0, kManyRows);
   const int rows = rg.n * a.groups;
-  if (row0 >= rows) return;
-  const int keys = max(0, rg.hi - rg.lo), before = min(keys, split * sp.chunk);
-  const int begin = rg.lo + before, end = begin + min(keys - before, sp.chunk);
-  if (begin >= end && split > 0) return;  // the first chunk's workgroup answers for rows that see nothing
 
   // what this thread decodes: NG groups of one key (and of its value)
-  const int key_of = BOTH ? threadIdx.x >> 2 : (threadIdx.x & 127) >> 2;
-  const bool second = !BOTH && threadIdx.x >= 128;
-  const int g0 = NG * (threadIdx.x & 3);
+  const int key_of = BOTH ? thread_of >> 2 : (thread_of & 127) >> 2;
+  const bool second = !BOTH && thread_of >= 128;
+  const int g0 = NG * (thread_of & 3);
   // The page number of this thread's key, as it stands in the table (checked
   // when it is used, a tile later: nothing may wait for it here).  Past the
   // end the last key's.
@@ -1118,7 +1111,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         exists[buf][wave] = there;
         odd[buf][wave] = others;
       }
-      odd_groups[buf][opaque((int)threadIdx.x)] = bad;
+      odd_groups[buf][opaque((int)thread_of)] = bad;
       if constexpr (BOTH) kv_drop(vt, bad);
       else kv_drop(kt, bad);
     }
@@ -1469,7 +1462,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
   l_run += __shfl_xor(l_run, 32, 64);
   if (!row_live) return;
   const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + qh;
-  if (sp.splits == 1) {
+  if (TREE ? whole : sp.splits == 1) {
     const float by = l_run == 0.0f ? 0.0f : global_decode(c.global_v) / l_run;  // a NaN stays one
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -1481,7 +1474,7 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
       }
     if (a.lse && half == 0) a.lse[row] = l_run == 0.0f ? kNone : (m_run - kBias + __builtin_log2f(l_run)) * kLn2;
   } else {
-    const int64_t part = row * sp.splits + split;
+    const int64_t part = TREE ? base_row + r - row0 : row * sp.splits + split;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -1491,6 +1484,134 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
         if (at < c.dim) kv_store4<kF32>(sp.sums, part * c.dim + at, v);
       }
     if (half == 0) *reinterpret_cast<f32x2*>(sp.stats + 2 * part) = f32x2{m_run, l_run};
+  }
+}
+
+// A workgroup a (sequence, kv head), 128 rows and a chunk of the keys.
+template <int NG, int SPLIT, bool EXACT>
+__global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1))
+kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int b = blockIdx.y;
+  int x = blockIdx.x;
+  const int split = x % sp.splits;
+  x /= sp.splits;
+  const int head = x % c.heads;
+  const int row0 = (sp.row_tiles - 1 - x / c.heads) * kManyRows;  // the longest ranges first
+  const KvRange rg = kv_range<false>(a, b, row0, kManyRows);
+  if (row0 >= rg.n * a.groups) return;
+  const int keys = max(0, rg.hi - rg.lo), before = min(keys, split * sp.chunk);
+  const int begin = rg.lo + before, end = begin + min(keys - before, sp.chunk);
+  if (begin >= end && split > 0) return;  // the first chunk's workgroup answers for rows that see nothing
+  kv_many_rows<NG, SPLIT, EXACT, false>(c, a, sp, dt, q_vec, lds, b, head, row0, rg, begin, end, split, true, 0);
+}
+
+// Trees: all rows of a sequence see the same keys but the last ones, and a batch's
+// contexts and trees differ, so the workgroups share the work out as those of few
+// rows do: the keys of every (sequence, kv head, 128 rows) are cut into units of
+// kManyStep, and each workgroup takes an equal run of all units.  (In chunks of a
+// fixed length, as many as fill the GPU if every sequence is of the largest size,
+// 16 sequences of up to 16384 keys and 64 drafts took 343 us, as long as the
+// longest chunk; 8 heads of 128, 4 queries a head.)
+constexpr int kManyStep = 256;
+
+struct KvTreeShare {
+  int groups;     // workgroups of the launch
+  int row_tiles;  // of a sequence and kv head, at most
+  float* sums;    // [groups + seqs * heads * row_tiles][128][dim], times 2^kBias; null: units are whole
+  float* stats;   // .. [2]: maximum (log2), sum
+};
+// Sequences 64 at a time, one per lane, and the units before them: as KvScan.
+struct KvTreeScan {
+  KvRange range;
+  int tiles;  // (kv head, 128 rows) of this sequence
+  int units;  // of one of them; 0 past the last sequence and without queries
+  int first, after;
+};
+__device__ __forceinline__ void tree_scan(const KvCache& c, const KvAttention& a, int base, int before, KvTreeScan& s) {
+  const int lane = threadIdx.x & 63, b = base + lane;
+  s.units = s.tiles = 0;
+  s.range = KvRange{0, 0, 0, 0, 0};
+  if (b < a.seqs) {
+    s.range = kv_range<true>(a, b, 0, kManyRows);
+    s.tiles = c.heads * ((s.range.n * a.groups + kManyRows - 1) / kManyRows);
+    if (s.range.n > 0) s.units = max(1, (s.range.hi - s.range.lo + kManyStep - 1) / kManyStep);
+  }
+  int sum = s.units * s.tiles;
+  const int own = sum;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int up = __shfl_up(sum, off, 64);
+    if (lane >= off) sum += up;
+  }
+  s.first = before + sum - own;
+  s.after = before + __builtin_amdgcn_readlane(sum, 63);
+}
+__device__ __forceinline__ int tree_units_each(const KvCache& c, const KvAttention& a, int groups, KvTreeScan& s) {
+  int total = 0;
+  for (int base = 0; base < a.seqs; base += 64) {
+    tree_scan(c, a, base, total, s);
+    total = s.after;
+  }
+  return (total + groups - 1) / groups;
+}
+
+struct KvTreeArgs {
+  KvCache c;
+  KvAttention a;
+  KvTreeShare sh;
+  int dt;
+  bool q_vec;
+};
+
+// The arguments are read anew for each run, where they lie: held over the runs,
+// they and what follows from them cost the loop over the keys 36 spilled registers.
+template <int NG, int SPLIT, bool EXACT>
+__global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1)) kv_tree_kernel(KvTreeArgs) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  typedef const __attribute__((address_space(4))) KvTreeArgs* ArgsPtr;
+  auto arguments = []() {
+    ArgsPtr p = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return (const KvTreeArgs*)p;
+  };
+  int unit, last, base = 0, before = 0;
+  {
+    const KvTreeArgs& args = *arguments();
+    KvTreeScan scan;
+    const int each = __builtin_amdgcn_readfirstlane(tree_units_each(args.c, args.a, args.sh.groups, scan));
+    unit = __builtin_amdgcn_readfirstlane((int)blockIdx.x * each);
+    last = unit + each;
+  }
+  while (unit < last) {
+    const KvTreeArgs& args = *arguments();
+    const KvCache& c = args.c;
+    const KvAttention& a = args.a;
+    const KvChunks sp{0, 1, 0, args.sh.sums, args.sh.stats};
+    KvTreeScan scan;  // (anew for each run: kept, it would cost the loop's registers)
+    tree_scan(c, a, base, before, scan);
+    while (unit >= scan.after) {
+      base += 64;
+      before = scan.after;
+      if (base >= a.seqs) return;  // past the last unit
+      tree_scan(c, a, base, before, scan);
+    }
+    const int lane = __builtin_amdgcn_readfirstlane(63 - __builtin_clzll(__ballot(scan.units > 0 && scan.first <= unit)));
+    const int b = base + lane;
+    const KvRange rg{__builtin_amdgcn_readlane(scan.range.first, lane), __builtin_amdgcn_readlane(scan.range.n, lane),
+                     __builtin_amdgcn_readlane(scan.range.context, lane), __builtin_amdgcn_readlane(scan.range.lo, lane),
+                     __builtin_amdgcn_readlane(scan.range.hi, lane)};
+    const int units = __builtin_amdgcn_readlane(scan.units, lane);
+    const int inside = unit - __builtin_amdgcn_readlane(scan.first, lane);
+    const int tile = __builtin_amdgcn_readfirstlane(inside / units), off = inside - tile * units;
+    const int take = min(units - off, last - unit);
+    const int row_tile = __builtin_amdgcn_readfirstlane(tile / c.heads), head = tile - row_tile * c.heads;
+    const int begin = rg.lo + off * kManyStep, end = min(rg.hi, begin + take * kManyStep);
+    // Part number: of this workgroup and of the tile, which no other part has both.
+    const int64_t part = (int64_t)blockIdx.x + ((int64_t)b * args.sh.row_tiles * c.heads + tile);
+    kv_many_rows<NG, SPLIT, EXACT, true>(c, a, sp, args.dt, args.q_vec, lds, b, head, row_tile * kManyRows, rg, begin, end, 0,
+                                         take == units, part * kManyRows);
+    unit += take;
   }
 }
 
@@ -1582,12 +1703,37 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention
   kv_join<kFewWaves>(c, a, dt, sh.sums, sh.stats, at, sh.rows, parts, (int64_t)(rg.first + qi) * a.query_heads + qh);
 }
 
-template <bool TREE>
-__global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt) {
+// A wave a row of a tree.
+[[maybe_unused]] __global__ void __launch_bounds__(256) kv_join_tree_kernel(KvCache c, KvAttention a, KvTreeShare sh, int dt) {
+  const int b = blockIdx.y, row_of = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int qi = row_of / a.query_heads, qh = row_of - qi * a.query_heads;
+  const int head = qh / a.groups, r = qi * a.groups + qh - head * a.groups;
+  KvTreeScan scan;
+  const int each = tree_units_each(c, a, sh.groups, scan);
+  int base = 0;
+  if (a.seqs > 64) {
+    tree_scan(c, a, 0, 0, scan);
+    while (b >= base + 64) {
+      base += 64;
+      tree_scan(c, a, base, scan.after, scan);
+    }
+  }
+  const int first = __builtin_amdgcn_readlane(scan.range.first, b - base);
+  if (qi >= __builtin_amdgcn_readlane(scan.range.n, b - base)) return;
+  const int units = __builtin_amdgcn_readlane(scan.units, b - base);
+  const int tile = r / kManyRows * c.heads + head;
+  const int u0 = __builtin_amdgcn_readlane(scan.first, b - base) + tile * units;
+  const int g0 = u0 / each, g1 = (u0 + units - 1) / each;
+  if (g0 == g1) return;  // one workgroup had it all
+  const int64_t at = ((int64_t)g0 + (int64_t)b * sh.row_tiles * c.heads + tile) * kManyRows + r % kManyRows;
+  kv_join<1>(c, a, dt, sh.sums, sh.stats, at, kManyRows, g1 - g0 + 1, (int64_t)(first + qi) * a.query_heads + qh);
+}
+
+[[maybe_unused]] __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt) {
   const int row_of = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int qi = row_of / a.query_heads, qh = row_of - qi * a.query_heads;
   const int r = qi * a.groups + qh % a.groups;  // its row among those of its kv head
-  const KvRange rg = kv_range<TREE>(a, blockIdx.y, r / kManyRows * kManyRows, kManyRows);
+  const KvRange rg = kv_range<false>(a, blockIdx.y, r / kManyRows * kManyRows, kManyRows);
   if (qi >= rg.n) return;
   const int parts = rg.hi > rg.lo ? (rg.hi - rg.lo - 1) / sp.chunk + 1 : 1;
   const int64_t row = (int64_t)(rg.first + qi) * a.query_heads + qh;
@@ -1626,7 +1772,8 @@ constexpr int few_groups(int dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : dim 
 // them; more rows are matrix work.  32 rows, 8 x 30000 keys, 4 heads, few
 // against many, us: dim 128 76 / 90, float32 92 / 175; dim 256 128 / 254,
 // float32 282 / 317 (48 rows of dim 128 on the many-rows kernel: 92, 96 rows 105).
-KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
+// tree: for drafted tokens.
+KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split, bool tree) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_queries * a.groups;
   int64_t keys = a.max_keys;
@@ -1642,6 +1789,14 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split) {
     const bool alone = keys <= few_alone(pairs);
     p.groups = (int)(alone ? pairs : units < most ? units : most);
     parts = alone ? 0 : (size_t)(p.groups + pairs) * 16 * p.mt;
+  } else if (tree) {
+    p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
+    // as many workgroups as run at once, but no more than there can be units
+    const int64_t tiles = pairs * p.row_tiles, most = (int64_t)device_cu_count() * (few_groups(c.dim) * split <= 2 ? 2 : 1);
+    const int64_t each = keys > kManyStep ? (keys + kManyStep - 1) / kManyStep : 1;
+    const int64_t units = tiles > most ? most : tiles * each;  // (without overflow)
+    p.groups = (int)(each == 1 ? tiles : units < most ? units : most);
+    parts = each == 1 ? 0 : (size_t)(p.groups + tiles) * kManyRows;
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
     const int64_t tiles = pairs * p.row_tiles;
@@ -1698,17 +1853,30 @@ hipError_t launch_few(const KvCache& c, const KvAttention& a, const KvShare& sh,
   return hipGetLastError();
 }
 
-template <int NG, bool EXACT, bool TREE>
+template <int NG, bool EXACT>
 hipError_t launch_many(const KvCache& c, const KvAttention& a, const KvChunks& sp, int dt, bool q_vec, hipStream_t s) {
   const dim3 grid((unsigned)(sp.row_tiles * c.heads * sp.splits), a.seqs);
 #define KV_MANY(SPLIT)                                                                            \
   do {                                                                                            \
     static std::atomic<bool> set[64];                                                             \
-    if (hipError_t e = allow_lds(&kv_many_kernel<NG, SPLIT, EXACT, TREE>, set)) return e;               \
-    kv_many_kernel<NG, SPLIT, EXACT, TREE><<<grid, 256, many_lds(NG), s>>>(c, a, sp, dt, q_vec);        \
+    if (hipError_t e = allow_lds(&kv_many_kernel<NG, SPLIT, EXACT>, set)) return e;               \
+    kv_many_kernel<NG, SPLIT, EXACT><<<grid, 256, many_lds(NG), s>>>(c, a, sp, dt, q_vec);        \
   } while (0)
   if (dt == kF32) KV_MANY(2); else KV_MANY(1);
 #undef KV_MANY
+  return hipGetLastError();
+}
+
+template <int NG, bool EXACT>
+hipError_t launch_tree(const KvCache& c, const KvAttention& a, const KvTreeShare& sh, int dt, bool q_vec, hipStream_t s) {
+#define KV_TREE(SPLIT)                                                                            \
+  do {                                                                                            \
+    static std::atomic<bool> set[64];                                                             \
+    if (hipError_t e = allow_lds(&kv_tree_kernel<NG, SPLIT, EXACT>, set)) return e;               \
+    kv_tree_kernel<NG, SPLIT, EXACT><<<sh.groups, 256, many_lds(NG), s>>>(KvTreeArgs{c, a, sh, dt, q_vec}); \
+  } while (0)
+  if (dt == kF32) KV_TREE(2); else KV_TREE(1);
+#undef KV_TREE
   return hipGetLastError();
 }
 
@@ -1721,19 +1889,30 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const KvPlan& p, int d
     const hipError_t e = launch_few<NG, EXACT, TREE>(c, a, sh, p, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
     kv_join_few_kernel<TREE><<<rows, 256, 0, s>>>(c, a, sh, dt);
+  } else if constexpr (TREE) {
+    const KvTreeShare sh{p.groups, p.row_tiles, sums, stats};
+    const hipError_t e = launch_tree<NG, EXACT>(c, a, sh, dt, q_vec, s);
+    if (e != hipSuccess || p.bytes == 0) return e;
+    kv_join_tree_kernel<<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sh, dt);
   } else {
     const KvChunks sp{p.chunk, p.splits, p.row_tiles, sums, stats};
-    const hipError_t e = launch_many<NG, EXACT, TREE>(c, a, sp, dt, q_vec, s);
+    const hipError_t e = launch_many<NG, EXACT>(c, a, sp, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
-    kv_join_many_kernel<TREE><<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sp, dt);
+    kv_join_many_kernel<<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sp, dt);
   }
   return hipGetLastError();
+}
+
+template <bool TREE>
+size_t attention_workspace(const KvCache& c, const KvAttention& a) {
+  const size_t one = kv_plan(c, a, 1, TREE).bytes, two = kv_plan(c, a, 2, TREE).bytes;
+  return one > two ? one : two;
 }
 
 // The whole call: queries, workspace and launch by type and size.
 template <bool TREE>
 hipError_t launch_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s) {
-  const KvPlan p = kv_plan(c, a, dt == kF32 ? 2 : 1);
+  const KvPlan p = kv_plan(c, a, dt == kF32 ? 2 : 1, TREE);
   float* sums = reinterpret_cast<float*>(workspace);
   float* stats = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + p.sums_bytes);
   const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && (a.q_token | a.q_head) % 8 == 0;

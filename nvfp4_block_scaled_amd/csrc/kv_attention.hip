@@ -4,10 +4,7 @@
 
 namespace nvfp4 {
 
-size_t kv_attention_workspace(const KvCache& c, const KvAttention& a) {
-  const size_t one = kv_plan(c, a, 1).bytes, two = kv_plan(c, a, 2).bytes;
-  return one > two ? one : two;
-}
+size_t kv_attention_workspace(const KvCache& c, const KvAttention& a) { return attention_workspace<false>(c, a); }
 
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s) {
   return launch_attention<false>(c, a, dt, workspace, s);

@@ -48,6 +48,7 @@ struct KvAttention {
 };
 size_t kv_attention_workspace(const KvCache& c, const KvAttention& a);
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s);
+size_t kv_tree_attention_workspace(const KvCache& c, const KvAttention& a);
 hipError_t launch_kv_tree_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s);
 
 }  // namespace nvfp4

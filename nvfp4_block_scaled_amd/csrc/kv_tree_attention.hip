@@ -4,6 +4,8 @@
 
 namespace nvfp4 {
 
+size_t kv_tree_attention_workspace(const KvCache& c, const KvAttention& a) { return attention_workspace<true>(c, a); }
+
 hipError_t launch_kv_tree_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s) {
   return launch_attention<true>(c, a, dt, workspace, s);
 }

@@ -27,7 +27,7 @@ def cache(pages=10, page_size=16, heads=2, dim=128):
 
 def attend(L, c, q=A, dt=2, tokens=12, query_heads=8, qt=1024, qh=128, table=B, seqs=4, table_pages=8, lens=C, starts=E,
            max_queries=5, max_context=100, scale=0.1, tree=F, words=1, positions=None, window=0, out=D, lse=None, nbytes=None):
-    need = L.nvfp4_kv_attention_workspace_size(c, tokens, query_heads, seqs, max_queries, max_context, window)
+    need = L.nvfp4_kv_tree_attention_workspace_size(c, tokens, query_heads, seqs, max_queries, max_context, window)
     return L.nvfp4_kv_tree_attention(c, q, dt, tokens, query_heads, qt, qh, table, seqs, table_pages, lens, starts, max_queries,
                                      max_context, scale, tree, words, positions, window, out, lse, 0x70000,
                                      need if nbytes is None else nbytes, None)
