@@ -1183,6 +1183,18 @@ __device__ __forceinline__ void kv_many_rows(const KvCache& c, const KvAttention
     lds_barrier();
   }
   int buf = 0;
+  if (TREE && row0 + 32 * __builtin_amdgcn_readfirstlane(wave) >= rows) {  // no rows: decodes its share for the others
+    for (int tile = begin; tile < end; tile += TILE, buf ^= 1) {
+      store_flags(buf ^ 1);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) store_piece(buf ^ 1, i);
+      load(tile + 2 * TILE, page);
+      page = page2;
+      page2 = lookup();
+      lds_barrier();
+    }
+    return;
+  }
   for (int tile = begin; tile < end; tile += TILE, buf ^= 1) {
     const uint8_t* kb = lds + buf * BUF;
     const uint8_t* vb = kb + TILE * KROW;
