@@ -500,17 +500,18 @@ __device__ __forceinline__ uint32_t moe_slots(const MoeTokens& k, int from, int 
   return tiles;
 }
 
-constexpr int kUpWaves = 4, kUpAhead = 2, kUpSlots = 8;
+constexpr int kUpWaves = 4, kUpAhead = 2;
 
-// 16 gate rows and the 16 up rows that go with them, of one expert, are a job; a
-// workgroup takes every so many of them, its waves each a share of the inner
-// values.  Weights are on their way two units ahead, columns one, over the jobs'
-// ends; at a job's end one wave in turn joins the four sums while the others go
-// on.  CHOOSE: moe_choose_inside, and the last workgroup writes the
+// 16 gate rows and the 16 up rows that go with them, of one expert, are a job; KW
+// waves (all four of a workgroup, or one) take a job, each a share of the inner
+// values, and go on to every so many-th.  Weights are on their way two units ahead,
+// columns one, over the jobs' ends; at a job's end one wave in turn joins the four
+// sums while the others go on.  CHOOSE: moe_choose_inside, and the last workgroup writes the
 // choice.  PX: pieces of x here (1 or 2).
-template <int MT, int PX, bool WHOLE, bool CHOOSE>
-__global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_kernel(MoeLayer a, const uint16_t* x) {
-  constexpr int NS = kUpSlots;
+constexpr int up_groups_a_cu(int MT, int NS, int PX) { return MT * PX <= 2 && NS <= 8 ? 3 : 2; }
+
+template <int MT, int NS, int PX, int KW, bool WHOLE, bool CHOOSE>
+__global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe_up_kernel(MoeLayer a, const uint16_t* x) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int rows_of[kUpWaves][2][kMoeMaxTokens];  // of this job's expert and the next one's: its tokens
   const MoeLists lists = moe_lists_at(a, lds);
@@ -522,7 +523,9 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
     moe_weigh(a, 0, a.tokens, lists.idx);
     return;
   }
+  constexpr int kJobs = kUpWaves / KW;  // of a workgroup at a time
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int share = wave % KW, stride = groups * kJobs;
   const int tiles = a.f / 16, jobs = __builtin_amdgcn_readfirstlane(*lists.count) * tiles;
   const int units = (a.k + kUnit - 1) / kUnit;
   const int64_t plane = (int64_t)a.tokens * a.k;
@@ -533,9 +536,9 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
   struct Job {
     int at, which, tile;
   };
-  const int step_which = __builtin_amdgcn_readfirstlane(groups / tiles), step_tile = groups - step_which * tiles;
+  const int step_which = __builtin_amdgcn_readfirstlane(stride / tiles), step_tile = stride - step_which * tiles;
   auto advance = [&](Job& j) {
-    j.at += groups;
+    j.at += stride;
     j.which += step_which;
     j.tile += step_tile;
     if (j.tile >= tiles) {
@@ -545,48 +548,57 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
   };
   auto expert_of = [&](const Job& j) { return __builtin_amdgcn_readfirstlane(lists.list[j.which]); };
 
+  // h of tile m of a job's tokens from its gate and up sums.
+  auto hidden = [&](const Job& job, int m, const f32x4& g, const f32x4& v) {
+    const int expert = expert_of(job), f0 = job.tile * 16;
+    const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
+    const int e = lists.exponent[min(t, a.tokens - 1)];
+    const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
+    f32x4 h;
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x1 = __builtin_ldexpf(g[i] * factor, e), x2 = __builtin_ldexpf(v[i] * factor, e);
+      h[i] = x1 / (1.0f + expf(-x1)) * x2;
+      top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    if (p < 0) return;
+    *reinterpret_cast<f32x4*>(a.hidden + (int64_t)p * a.f + f0 + 4 * (lane >> 4)) = h;
+    if (lane < 16) atomicMax(a.h_top + p, top);  // (in any order the same)
+  };
   // The sums of a job, number `n` of this workgroup's.
   auto finish = [&](const Job& job, int n, const f32x4(&acc)[2][MT]) {
-    f32x4* const part = parts;
-    if (n > 0) lds_barrier();  // the last job's are read
+    if constexpr (KW == 1) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+      for (int m = 0; m < MT; ++m) hidden(job, m, acc[0][m], acc[1][m]);
+    } else {
+      f32x4* const part = parts;
+      if (n > 0) lds_barrier();  // the last job's are read
 #pragma unroll
-      for (int m = 0; m < MT; ++m) part[((wave * 2 + r) * MT + m) * 64 + lane] = acc[r][m];
-    lds_barrier();
-    const int expert = expert_of(job), f0 = job.tile * 16;
-    for (int m = (wave + n) % kUpWaves; m < MT; m += kUpWaves) {
-      const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
-      const int e = lists.exponent[min(t, a.tokens - 1)];
-      const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
-      f32x4 g = part[m * 64 + lane], v = part[(MT + m) * 64 + lane];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int i = 1; i < kUpWaves; ++i) {
-        g += part[((i * 2) * MT + m) * 64 + lane];
-        v += part[((i * 2 + 1) * MT + m) * 64 + lane];
+        for (int m = 0; m < MT; ++m) part[((wave * 2 + r) * MT + m) * 64 + lane] = acc[r][m];
+      lds_barrier();
+      for (int m = (wave + n) % kUpWaves; m < MT; m += kUpWaves) {
+        f32x4 g = part[m * 64 + lane], v = part[(MT + m) * 64 + lane];
+#pragma unroll
+        for (int i = 1; i < kUpWaves; ++i) {
+          g += part[((i * 2) * MT + m) * 64 + lane];
+          v += part[((i * 2 + 1) * MT + m) * 64 + lane];
+        }
+        hidden(job, m, g, v);
       }
-      f32x4 h;
-      uint32_t top = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x1 = __builtin_ldexpf(g[i] * factor, e), x2 = __builtin_ldexpf(v[i] * factor, e);
-        h[i] = x1 / (1.0f + expf(-x1)) * x2;
-        top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-      }
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      if (p < 0) continue;
-      *reinterpret_cast<f32x4*>(a.hidden + (int64_t)p * a.f + f0 + 4 * (lane >> 4)) = h;
-      if (lane < 16) atomicMax(a.h_top + p, top);  // (in any order the same)
     }
   };
 
-  if ((int)blockIdx.x >= jobs) return;
   Job job;
-  job.at = blockIdx.x;
+  job.at = (int)blockIdx.x * kJobs + wave / KW;
+  if (job.at >= jobs) return;
   job.which = __builtin_amdgcn_readfirstlane(job.at / tiles);
   job.tile = job.at - job.which * tiles;
-  if (wave >= units) {  // fewer units than waves
+  if (KW > 1 && share >= units) {  // fewer units than waves
     const f32x4 none[2][MT] = {};
     for (int n = 0; job.at < jobs; advance(job), ++n) finish(job, n, none);
     return;
@@ -594,14 +606,14 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
 
   // The unit whose weights are loaded next; the last one again when all are.
   Job w_job = job;
-  int w_unit = wave;
+  int w_unit = share;
   int64_t w_row = (int64_t)expert_of(job) * 2 * a.f + job.tile * 16;
   auto load_weights = [&](MoeWeights<2>& to) {
     moe_load<2, WHOLE>(to, a.up_codes, a.up_scales, {w_row, w_row + a.f}, a.k, w_unit);
-    if (w_unit + kUpWaves < units) {
-      w_unit += kUpWaves;
-    } else if (w_job.at + groups < jobs) {
-      w_unit = wave;
+    if (w_unit + KW < units) {
+      w_unit += KW;
+    } else if (w_job.at + stride < jobs) {
+      w_unit = share;
       advance(w_job);
       w_row = (int64_t)expert_of(w_job) * 2 * a.f + w_job.tile * 16;
     }
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
   };
   MoeWeights<2> w[kUpAhead];
   MoeColumns<NS, PX> columns;
-  int u = wave, n = 0;
+  int u = share, n = 0;
   load_weights(w[0]);
   open(job, tokens, rows_of[wave][0]);
   moe_load<NS, PX>(columns, x, plane, at, a.k, u);
@@ -638,13 +650,13 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
       moe_stage<WHOLE>(stage, w[j], a.k, u);
       moe_stage(stage, columns);
       moe_settle();
-      const bool last = u + kUpWaves >= units, more_jobs = job.at + groups < jobs;
+      const bool last = u + KW >= units, more_jobs = job.at + stride < jobs;
       if (last && more_jobs) {
         Job next = job;
         advance(next);
         open(next, next_tokens, rows_of[wave][(n + 1) & 1]);
       }
-      moe_load<NS, PX>(columns, x, plane, at, a.k, last ? wave : u + kUpWaves);
+      moe_load<NS, PX>(columns, x, plane, at, a.k, last ? share : u + KW);
       load_weights(w[j]);
       moe_products<2, MT>(stage, slot, first, acc);
       for (int from = NS; from < tokens.count; from += NS) {  // more tokens than have room
@@ -659,13 +671,13 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
         moe_products<2, MT>(stage, slot2, some, acc);
       }
       moe_settle();
-      u += kUpWaves;
+      u += KW;
       if (last) {
         finish(job, n, acc);
         if (!more_jobs) return;
         advance(job);
         ++n;
-        u = wave;
+        u = share;
         tokens = next_tokens;
         first = moe_slots<NS, MT>(tokens, 0, slot);
 #pragma unroll
@@ -677,16 +689,31 @@ __global__ void __launch_bounds__(64 * kUpWaves, MT * PX <= 2 ? 3 : 2) moe_up_ke
   }
 }
 
+template <int DT>
+__device__ __forceinline__ void moe_store(void* out, int64_t to, const f32x4& v) {
+  if constexpr (DT == kF32)
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + to) = v;
+  else
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + to) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+
 // Waves of a workgroup of the down products: what has room in LDS, and in registers.
-constexpr int down_waves(int MT, int PH) { return MT > 2 || (MT == 2 && PH == 2) ? 8 : 12; }
+constexpr int down_waves(int MT, int NS, int PH) {
+  return NS > 8 && PH == 2 ? 6 : MT > 2 || NS > 8 || (MT == 2 && PH == 2) ? 8 : 12;
+}
 constexpr int kDownAhead = 3;
 
-// 16 columns of the output for all tokens: a workgroup, its waves in turn the
-// units of all chosen experts' rows: what they read at a time lies together.
-// Weights are on their way three units ahead, columns one, over the experts' ends.
+// 16 columns of the output for all tokens: a workgroup, its waves the units of all
+// chosen experts' rows, in turn, so that what they read at a time lies together;
+// or, where an expert's units are few, a run of them each, so that they do not
+// change experts with every unit (16 tokens bfloat16, runs against turns: 8 of 64
+// experts of 2048 x 1024, 4 units each, 103 against 121 us of the whole layer; 4 of
+// 16 of 2048 x 4096, 16 units, 120 against 125; 4 of 32 of 2048 x 5760, 23 units,
+// 232 against 229, and there the rule ends).  Weights are on their way three units
+// ahead, columns one, over the experts' ends.
 template <int DT, int MT, int NS, int PH, bool WHOLE>
-__global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLayer a) {
-  constexpr int WAVES = down_waves(MT, PH);
+__global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(MoeLayer a) {
+  constexpr int WAVES = down_waves(MT, NS, PH);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int rows_of[WAVES][2][kMoeMaxTokens];  // of this expert and the next one: its pairs
   const MoeLists lists = moe_lists_at(a, lds);
@@ -699,18 +726,22 @@ __global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLa
   const int n0 = blockIdx.x * 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int units = (a.f + kUnit - 1) / kUnit, all = __builtin_amdgcn_readfirstlane(*lists.count) * units;
+  // this wave's units: begin, begin + stride ..
+  const bool runs = units < 2 * WAVES;
+  const int each = __builtin_amdgcn_readfirstlane((all + WAVES - 1) / WAVES);
+  const int stride = runs ? 1 : WAVES, begin_at = runs ? wave * each : wave, end_at = runs ? min(all, begin_at + each) : all;
   f32x4 total[MT] = {};
-  if (wave < all) {
+  if (begin_at < end_at) {
     auto expert_of = [&](int which) { return __builtin_amdgcn_readfirstlane(lists.list[which]); };
-    int which = __builtin_amdgcn_readfirstlane(wave / units), u = wave - which * units;
+    int which = __builtin_amdgcn_readfirstlane(begin_at / units), u = begin_at - which * units;
     // the unit whose weights are loaded next, of all and of its expert; the last one again when all are
-    int w_next = wave, w_which = which, w_unit = u;
+    int w_next = begin_at, w_which = which, w_unit = u;
     int64_t w_row = (int64_t)expert_of(which) * a.k + n0;
     auto load_weights = [&](MoeWeights<1>& to) {
       moe_load<1, WHOLE>(to, a.down_codes, a.down_scales, {w_row}, a.f, w_unit);
-      if (w_next + WAVES < all) {
-        w_next += WAVES;
-        w_unit += WAVES;
+      if (w_next + stride < end_at) {
+        w_next += stride;
+        w_unit += stride;
         if (w_unit >= units) {
           do {
             w_unit -= units;
@@ -730,9 +761,9 @@ __global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLa
     int slot[MT], row = 0, exponent = 0, next_exponent = 0, n = 0;  // lane i: slot i's pair and its power of two
     uint32_t first = 0u;
     f32x4 acc[1][MT];
-    int left = __builtin_amdgcn_readfirstlane((all - wave + WAVES - 1) / WAVES);
+    int left = __builtin_amdgcn_readfirstlane((end_at - begin_at + stride - 1) / stride);
     auto place = [&](const MoeTokens& k, const int* row_of, int from, int& to, int& e) {
-      to = row_of[min(from + (lane & 7), k.count - 1)];
+      to = row_of[min(from + (lane & 15), k.count - 1)];
       e = lists.exponent[to];
     };
     auto open = [&](int expert, MoeTokens& k, int* row_of, int& e) {
@@ -780,7 +811,7 @@ __global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLa
         const bool more = --left > 0;
         int next = which;
         if (more) {
-          u += WAVES;
+          u += stride;
           while (u >= units) {
             u -= units;
             ++next;
@@ -826,11 +857,7 @@ __global__ void __launch_bounds__(64 * down_waves(MT, PH)) moe_down_kernel(MoeLa
 #pragma unroll
     for (int i = 1; i < WAVES; ++i) v += part[(i * MT + m) * 64 + lane];
     if (t >= a.tokens) continue;
-    const int64_t to = (int64_t)t * a.k + n0 + 4 * (lane >> 4);
-    if constexpr (DT == kF32)
-      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + to) = v;
-    else
-      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + to) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    moe_store<DT>(a.out, (int64_t)t * a.k + n0 + 4 * (lane >> 4), v);
   }
 }
 
@@ -867,50 +894,64 @@ hipError_t moe_allow_lds(K* kernel, size_t bytes, std::atomic<bool> (&set)[64]) 
 size_t moe_lists_bytes(const MoeLayer& a) { return 4 * (size_t)moe_list_words(a.tokens * a.top_k, a.experts); }
 constexpr size_t moe_most_list_bytes(int MT) { return 4 * (size_t)moe_list_words(16 * MT * kMoeMaxTopK, kMoeMaxExperts); }
 
-template <int DT, int MT, bool WHOLE, bool CHOOSE>
+template <int DT, int MT, int NS, int KW, bool WHOLE, bool CHOOSE>
 hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT) > 0 ? moe_x_pieces(DT) : 1;
-  constexpr size_t bytes = kUpWaves * (sizeof(MoeStage<2, kUpSlots, PX>) + 2 * MT * 1024);
+  constexpr size_t bytes = kUpWaves * (sizeof(MoeStage<2, NS, PX>) + (KW > 1 ? 2 * MT * 1024 : 0));
   static_assert(bytes >= 1024 * 8, "the order of the logits fits");
   static std::atomic<bool> set[64];
-  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, PX, WHOLE, CHOOSE>, bytes + moe_most_list_bytes(MT), set); e != hipSuccess)
+  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, NS, PX, KW, WHOLE, CHOOSE>, bytes + moe_most_list_bytes(MT), set);
+      e != hipSuccess)
     return e;
   const int pairs = a.tokens * a.top_k, most = pairs < a.experts ? pairs : a.experts;
   const uint16_t* x = moe_x_pieces(DT) > 0 ? a.x_pieces : reinterpret_cast<const uint16_t*>(a.x);
   // as many workgroups as run at once
-  const int jobs = most * (a.f / 16), resident = device_cu_count() * (MT * PX <= 2 ? 3 : 2);
+  const int jobs = (most * (a.f / 16) + kUpWaves / KW - 1) / (kUpWaves / KW);
+  const int resident = device_cu_count() * up_groups_a_cu(MT, NS, PX);
   const int groups = (jobs < resident ? jobs : resident) + (CHOOSE ? 1 : 0);
-  moe_up_kernel<MT, PX, WHOLE, CHOOSE><<<groups, 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
+  moe_up_kernel<MT, NS, PX, KW, WHOLE, CHOOSE><<<groups, 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
   return hipGetLastError();
 }
 
 template <int DT, int MT, int NS, bool WHOLE>
 hipError_t launch_down(const MoeLayer& a, hipStream_t s) {
-  constexpr int PH = moe_h_pieces(DT), WAVES = down_waves(MT, PH);
+  constexpr int PH = moe_h_pieces(DT), WAVES = down_waves(MT, NS, PH);
   constexpr size_t staged = WAVES * sizeof(MoeStage<1, NS, PH>), joined = WAVES * MT * 1024;
   constexpr size_t bytes = staged > joined ? staged : joined;
-  static_assert(bytes + moe_most_list_bytes(MT) + WAVES * kMoeMaxTokens * 8 <= 160 * 1024, "LDS");
+  static_assert(bytes + moe_most_list_bytes(MT) + WAVES * kMoeMaxTokens * 8 + 16 <= 160 * 1024, "LDS");
   static std::atomic<bool> set[64];
-  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, NS, PH, WHOLE>, bytes + moe_most_list_bytes(MT), set); e != hipSuccess)
+  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, NS, PH, WHOLE>, bytes + moe_most_list_bytes(MT), set);
+      e != hipSuccess)
     return e;
   moe_down_kernel<DT, MT, NS, PH, WHOLE><<<(unsigned)(a.k / 16), 64 * WAVES, bytes + moe_lists_bytes(a), s>>>(a);
   return hipGetLastError();
 }
 
-template <int DT, int MT>
+template <int DT, int MT, int NS>
 hipError_t launch_products(const MoeLayer& a, hipStream_t s) {
   auto whole = [](int inner, const uint8_t* scales) { return inner % 64 == 0 && (reinterpret_cast<uintptr_t>(scales) & 3) == 0; };
   const bool inside = MT <= 2 && a.router && moe_choose_inside(a.tokens, a.experts);  // (most tokens of MT 4 pass it)
+  // Up to three units are one wave's, without a join: 20 tokens float16, 3 of 9
+  // experts of 128 x 1376 58 us against 65, of 768 x 1376 60 against 65.
+  const bool alone = a.k <= 3 * kUnit;
   hipError_t e;
+#define MOE_UP(CHOOSE)                                                                                            \
+  do {                                                                                                            \
+    if (alone) e = whole(a.k, a.up_scales) ? launch_up<DT, MT, NS, 1, true, CHOOSE>(a, s)                         \
+                                           : launch_up<DT, MT, NS, 1, false, CHOOSE>(a, s);                       \
+    else e = whole(a.k, a.up_scales) ? launch_up<DT, MT, NS, kUpWaves, true, CHOOSE>(a, s)                        \
+                                     : launch_up<DT, MT, NS, kUpWaves, false, CHOOSE>(a, s);                      \
+  } while (0)
   if constexpr (MT <= 2) {
-    if (inside) e = whole(a.k, a.up_scales) ? launch_up<DT, MT, true, true>(a, s) : launch_up<DT, MT, false, true>(a, s);
+    if (inside) MOE_UP(true);
   }
-  if (!inside) e = whole(a.k, a.up_scales) ? launch_up<DT, MT, true, false>(a, s) : launch_up<DT, MT, false, false>(a, s);
+  if (!inside) MOE_UP(false);
+#undef MOE_UP
   if (e != hipSuccess) return e;
   if constexpr (MT == 1) {
     if (a.tokens <= 2) return whole(a.f, a.down_scales) ? launch_down<DT, 1, 2, true>(a, s) : launch_down<DT, 1, 2, false>(a, s);
   }
-  return whole(a.f, a.down_scales) ? launch_down<DT, MT, 8, true>(a, s) : launch_down<DT, MT, 8, false>(a, s);
+  return whole(a.f, a.down_scales) ? launch_down<DT, MT, NS, true>(a, s) : launch_down<DT, MT, NS, false>(a, s);
 }
 
 template <int DT>
@@ -932,9 +973,15 @@ hipError_t launch(const MoeLayer& a, hipStream_t s) {
     moe_choose_kernel<<<(unsigned)a.tokens, 256, 0, s>>>(a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (a.tokens <= 16) return launch_products<DT, 1>(a, s);
-  if (a.tokens <= 32) return launch_products<DT, 2>(a, s);
-  return launch_products<DT, 4>(a, s);
+  // Columns at a time, about as many as an expert has tokens (an expert's weights
+  // are staged again for those that are left): 16 where there are more than 5 an
+  // expert.  32 tokens, 2 of 8 of 4096 x 14336 bfloat16: 300 us, with 8 at a time
+  // 345.  They cost registers, and with them a workgroup a CU: 16 tokens there, 4 an
+  // expert, 210 us with 8.  (float32 above 32 tokens would spill with 16.)
+  const bool wide = 5 * a.experts < a.tokens * a.top_k;
+  if (a.tokens <= 16) return wide ? launch_products<DT, 1, 16>(a, s) : launch_products<DT, 1, 8>(a, s);
+  if (a.tokens <= 32) return wide ? launch_products<DT, 2, 16>(a, s) : launch_products<DT, 2, 8>(a, s);
+  return wide && DT != kF32 ? launch_products<DT, 4, DT == kF32 ? 8 : 16>(a, s) : launch_products<DT, 4, 8>(a, s);
 }
 
 }  // namespace
