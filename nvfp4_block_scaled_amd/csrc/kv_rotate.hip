@@ -27,16 +27,37 @@ namespace {
 
 constexpr int kTokens = 4;  // of a workgroup, one a wave
 
+// 8 values as they are loaded, on their way while those before them are encoded.
 template <int DT, bool VEC>
-__device__ __forceinline__ void rotate_load(const void* base, int64_t e, float (&v)[8]) {
-  if constexpr (VEC) {
-    load8x<DT>(base, e >> 3, v);
-  } else {
+struct Eight {
+  u32x4 w[DT == kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t e) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const typename Elem<DT>::T*>(base) + e);
+#pragma unroll
+    for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) w[i] = p[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (DT == kF32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i / 4][i % 4]);
+    } else {
+      unpack8<DT>(w[0], v);
+    }
+  }
+};
+template <int DT>
+struct Eight<DT, false> {  // (rows that start anywhere)
+  typename Elem<DT>::T x[8];
+  __device__ __forceinline__ void load(const void* base, int64_t e) {
     const typename Elem<DT>::T* p = reinterpret_cast<const typename Elem<DT>::T*>(base) + e;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(p[i]);
+    for (int i = 0; i < 8; ++i) x[i] = p[i];
   }
-}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(x[i]);
+  }
+};
 
 // Where the 8 values of lane piece u find their pairs.
 struct Rotation {
@@ -108,23 +129,31 @@ kv_rotate_kernel(KvCache c, KvRotate a) {
   const float enc_k = global_encode(c.global_k), enc_v = global_encode(c.global_v);
   const int page = held ? (int)kv_div((uint32_t)slot, c.page_div) : 0;
   const int off = held ? (int)slot - page * c.page_size : 0;
+  // A turn's values and their pairs are on their way a turn ahead; lanes without a
+  // head load a head that there is.
+  auto load = [&](int turn, Eight<DT, VEC>& v, Eight<DT, VEC>& o) {
+    const bool of_q = turn < nq, of_v = turn >= nq + nk;
+    const int head = (of_q ? turn : of_v ? turn - nq - nk : turn - nq) * each + sub;
+    const void* x = of_q ? a.q : of_v ? a.v : a.k;
+    const int64_t at = token * (of_q ? a.q_token : of_v ? a.v_token : a.k_token) +
+                       min(head, (of_q ? a.query_heads : c.heads) - 1) * (of_q ? a.q_head : of_v ? a.v_head : a.k_head) + d;
+    v.load(x, at);
+    o.load(x, at + r.shift);
+  };
+  Eight<DT, VEC> next_v, next_o;
+  load(from, next_v, next_o);
   for (int turn = from; turn < to; ++turn) {
     const bool of_q = turn < nq, of_v = turn >= nq + nk;
     const int head = (of_q ? turn : of_v ? turn - nq - nk : turn - nq) * each + sub;
     const bool live = in && head < (of_q ? a.query_heads : c.heads);
-    const void* x = of_q ? a.q : of_v ? a.v : a.k;
-    const int64_t at = token * (of_q ? a.q_token : of_v ? a.v_token : a.k_token) +
-                       head * (of_q ? a.q_head : of_v ? a.v_head : a.k_head) + d;
+    const Eight<DT, VEC> now_v = next_v, now_o = next_o;
+    load(min(turn + 1, to - 1), next_v, next_o);
     float v[8], o[8];
+    now_v.get(v);
+    now_o.get(o);
+    if (!of_v) rotate(r, v, o);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = o[i] = 0.0f;
-    if (live && there) {
-      rotate_load<DT, VEC>(x, at, v);
-      if (!of_v) {
-        if (r.shift != 0) rotate_load<DT, VEC>(x, at + r.shift, o);
-        rotate(r, v, o);
-      }
-    }
+    for (int i = 0; i < 8; ++i) v[i] = live && there ? v[i] : 0.0f;
     if (of_q) {
       if (live) store8<DT>(a.q_out, ((token * a.query_heads + head) * c.dim + d) >> 3, v);
     } else {

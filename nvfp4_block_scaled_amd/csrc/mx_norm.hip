@@ -53,6 +53,27 @@ __device__ __forceinline__ u32x2 mx_pack8(const float (&v)[8], float by) {
   return w;
 }
 
+// 8 values as they are loaded: converted at once, each load would be waited for
+// before the next is issued.
+template <int DT>
+struct Eight {
+  u32x4 w[DT == kF32 ? 2 : 1];
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(base) + (DT == kF32 ? 2 : 1) * at;
+#pragma unroll
+    for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) w[i] = STREAM ? __builtin_nontemporal_load(p + i) : p[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (DT == kF32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i / 4][i % 4]);
+    } else {
+      unpack8<DT>(w[0], v);
+    }
+  }
+};
+
 // LANES lanes (a wave, or the whole workgroup) take a row, NP pieces a lane;
 // LOOP: rows longer than that, whose rest is read twice.
 template <int DT, int BITS, int LANES, int NP, bool LOOP>
@@ -78,24 +99,36 @@ mx_norm_kernel(MxNorm p, int tiles) {
   const int pieces = (int)(p.k / 8);
   const int quads = (int)((p.k + 255) / 256);
   const int all = p.packed ? 32 * quads : pieces;  // with the padding behind the row
-  const int64_t first = row * pieces;
+  const int64_t first = (real ? row : 0) * pieces;
 
+  // No branch stands between the loads: lanes behind the row's end load its last
+  // piece again, and what is not there becomes 0.
   float h[NP][8];
-  auto load = [&](int from) {
+  Eight<DT> weight[NP];
+  auto load = [&](int from, bool weights) {
+    Eight<DT> x[NP], y[NP];
+    auto take = [&](Eight<DT>(&into)[NP], const void* base) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) into[j].template load<true>(base, first + min(from + j * LANES + lane, pieces - 1));
+    };
+    take(x, p.x);
+    if (p.residual) take(y, p.residual);
+    if (weights && p.weight) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) weight[j].template load<false>(p.weight, min(from + j * LANES + lane, pieces - 1));
+    }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int at = from + j * LANES + lane;
+      const bool in = real && from + j * LANES + lane < pieces;
+      x[j].get(h[j]);
+      if (p.residual) {
+        float v[8];
+        y[j].get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
-      if (real && at < pieces) {
-        load8<DT>(p.x, first + at, h[j]);
-        if (p.residual) {
-          float v[8];
-          load8<DT>(p.residual, first + at, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[j][i] = to_f32<DT>(from_f32<DT>(h[j][i] + v[i]));
-        }
+        for (int i = 0; i < 8; ++i) h[j][i] = to_f32<DT>(from_f32<DT>(h[j][i] + v[i]));
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = in ? h[j][i] : 0.0f;
     }
   };
   double squares = 0.0;
@@ -105,14 +138,14 @@ mx_norm_kernel(MxNorm p, int tiles) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) squares = __builtin_fma((double)h[j][i], (double)h[j][i], squares);
   };
-  load(0);
+  load(0, !LOOP);
   add();
   if constexpr (LOOP) {
     for (int from = kChunk; from < pieces; from += kChunk) {
-      load(from);
+      load(from, false);
       add();
     }
-    load(0);
+    load(0, true);
   }
   squares = wave_sum_f64(squares);
   if constexpr (LANES > 64) {
@@ -135,7 +168,7 @@ mx_norm_kernel(MxNorm p, int tiles) {
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = 1.0f;
-      if (live && p.weight) load8x<DT>(p.weight, at, y);
+      if (p.weight) weight[j].get(y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
 #pragma clang fp contract(off)
@@ -172,7 +205,7 @@ mx_norm_kernel(MxNorm p, int tiles) {
   encode(0);
   if constexpr (LOOP) {
     for (int from = kChunk; from < all; from += kChunk) {
-      load(from);
+      load(from, true);
       encode(from);
     }
   }
