@@ -44,27 +44,23 @@ constexpr int moe_x_pieces(int dt) { return dt == kF32 ? 2 : dt == kF16 ? 0 : 1;
 constexpr int moe_h_pieces(int dt) { return dt == kBF16 ? 1 : 2; }
 
 // e such that 2^-e brings a row of largest magnitude `top` (its bits) to 2^13 ..
-// 2^14.  Rows of zeros, infinities and NaN stay as they are.
+// 2^14.  Rows of zeros, infinities and NaN stay as they are, and 2^126 is as far as
+// it goes: float16's smallest step is then below float32's, and nothing is lost.
 __device__ __forceinline__ int moe_exponent(uint32_t top) {
   const int field = (int)(top >> 23);
-  return top == 0u || field == 255 ? 0 : field - 140;
+  return top == 0u || field == 255 ? 0 : max(field - 140, -126);
 }
-// Four values times 2^-e as P float16 pieces, two to a dword.
+// Four values times 2^-e as P float16 pieces, two to a dword: each piece is one
+// rounding of what those before it leave, and one instruction.
 template <int P>
 __device__ __forceinline__ void moe_pieces(const float (&v)[4], int e, u32x2 (&p)[P]) {
-  float y[4];
-  f16x2 a, b;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = __builtin_ldexpf(v[i], -e);
+  const float by = __uint_as_float((uint32_t)(127 - e) << 23);
+  _Float16 y[4];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    a = f16x2{(_Float16)y[0], (_Float16)y[1]};
-    b = f16x2{(_Float16)y[2], (_Float16)y[3]};
-    p[j] = u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
-    y[0] -= (float)a.x;
-    y[1] -= (float)a.y;
-    y[2] -= (float)b.x;
-    y[3] -= (float)b.y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = j == 0 ? (_Float16)(v[i] * by) : (_Float16)__builtin_fmaf(v[i], by, -(float)y[i]);
+    p[j] = u32x2{__builtin_bit_cast(uint32_t, f16x2{y[0], y[1]}), __builtin_bit_cast(uint32_t, f16x2{y[2], y[3]})};
   }
 }
 
@@ -272,12 +268,18 @@ __device__ __forceinline__ int moe_pair(const MoeLayer& a, const MoeLists& s, in
 // other wave waits for it; rows are padded by 16 bytes, which spreads the reads of
 // 8 rows over the banks.  The next units' loads are under way meanwhile.
 
-// In LDS, of one wave.  NS: columns in LDS at a time.
+// In LDS, of one wave.  NS: columns in LDS at a time; a last one holds zeros, for
+// the lanes whose token has no column among them.
 template <int NR, int NS, int P>
 struct MoeStage {
   u32x4 codes[NR][16][8 + 1];       // row, chunk of 32 values
   uint32_t scales[NR][16][4];       // row, 4 groups of 16
-  u32x4 columns[P][NS][32 + 1]; // column, chunk of 8 values
+  u32x4 columns[P][NS + 1][32 + 1]; // column, chunk of 8 values
+  __device__ __forceinline__ void clear() {
+    if ((threadIdx.x & 63) < 32)
+#pragma unroll
+      for (int p = 0; p < P; ++p) columns[p][NS][threadIdx.x & 63] = u32x4{0u, 0u, 0u, 0u};
+  }
 };
 
 // One unit's weights on their way: lane l has chunk l % 8 of rows l / 8 and l / 8
@@ -421,7 +423,7 @@ __device__ __forceinline__ f16x8 moe_decode8(uint32_t w, _Float16 s) {
 
 // The products of what is staged.  Lane l has row l % 16 and values 64 (l / 16) ..
 // + 63 of the unit on both sides.  slot[m]: this lane's column of tile m among
-// those staged, or -1: it meets zeros.  tiles: which tiles have any.
+// those staged, or NS.  tiles: which tiles have any.
 template <int NR, int MT, int NS, int P>
 __device__ __forceinline__ void moe_products(const MoeStage<NR, NS, P>& l, const int (&slot)[MT], uint32_t tiles,
                                              f32x4 (&acc)[NR][MT]) {
@@ -445,7 +447,7 @@ __device__ __forceinline__ void moe_products(const MoeStage<NR, NS, P>& l, const
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        b[i & 1][m][p] = l.columns[p][max(slot[m], 0)][8 * quarter + i];
+        b[i & 1][m][p] = l.columns[p][slot[m]][8 * quarter + i];
       }
   };
   read(0);
@@ -461,11 +463,9 @@ __device__ __forceinline__ void moe_products(const MoeStage<NR, NS, P>& l, const
       if (MT > 1 && !(tiles >> m & 1u)) continue;
 #pragma unroll
       for (int p = P - 1; p >= 0; --p) {  // the small pieces first
-        u32x4 v = b[i & 1][m][p];
-        if (slot[m] < 0) v = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-          acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r], __builtin_bit_cast(f16x8, v), acc[r][m], 0, 0, 0);
+          acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r], __builtin_bit_cast(f16x8, b[i & 1][m][p]), acc[r][m], 0, 0, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -494,8 +494,8 @@ __device__ __forceinline__ uint32_t moe_slots(const MoeTokens& k, int from, int 
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int t = 16 * m + (threadIdx.x & 15), at = moe_rank(k, t) - from;
-    slot[m] = (k.live >> t & 1u) && at >= 0 && at < NS ? at : -1;
-    tiles |= __any(slot[m] >= 0) ? 1u << m : 0u;
+    slot[m] = (k.live >> t & 1u) && at >= 0 && at < NS ? at : NS;
+    tiles |= __any(slot[m] < NS) ? 1u << m : 0u;
   }
   return tiles;
 }
@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe
   const int64_t plane = (int64_t)a.tokens * a.k;
   using Stage = MoeStage<2, NS, PX>;
   Stage& stage = reinterpret_cast<Stage*>(mine)[wave];
+  stage.clear();
   f32x4* const parts = reinterpret_cast<f32x4*>(mine + kUpWaves * sizeof(Stage));  // [wave][2][MT][64]
   // A job: tile `tile` of the which-th expert.  (All of it in scalar registers.)
   struct Job {
@@ -715,7 +716,7 @@ template <int DT, int MT, int NS, int PH, bool WHOLE>
 __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(MoeLayer a) {
   constexpr int WAVES = down_waves(MT, NS, PH);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ int rows_of[WAVES][2][kMoeMaxTokens];  // of this expert and the next one: its pairs
+  __shared__ uint16_t rows_of[WAVES][2][kMoeMaxTokens];  // of this expert and the next one: its pairs
   const MoeLists lists = moe_lists_at(a, lds);
   uint8_t* const mine = lds + 4 * moe_list_words(a.tokens * a.top_k, a.experts);
   for (int p = threadIdx.x; p < a.tokens * a.top_k; p += 64 * WAVES) {
@@ -756,21 +757,22 @@ __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(M
 
     using Stage = MoeStage<1, NS, PH>;
     Stage& stage = reinterpret_cast<Stage*>(mine)[wave];
+    stage.clear();
     MoeHidden<NS> hidden;
     MoeTokens tokens, next_tokens;
     int slot[MT], row = 0, exponent = 0, next_exponent = 0, n = 0;  // lane i: slot i's pair and its power of two
     uint32_t first = 0u;
     f32x4 acc[1][MT];
     int left = __builtin_amdgcn_readfirstlane((end_at - begin_at + stride - 1) / stride);
-    auto place = [&](const MoeTokens& k, const int* row_of, int from, int& to, int& e) {
+    auto place = [&](const MoeTokens& k, const uint16_t* row_of, int from, int& to, int& e) {
       to = row_of[min(from + (lane & 15), k.count - 1)];
       e = lists.exponent[to];
     };
-    auto open = [&](int expert, MoeTokens& k, int* row_of, int& e) {
+    auto open = [&](int expert, MoeTokens& k, uint16_t* row_of, int& e) {
       const int pair = moe_pair(a, lists, lane, expert);
       k = moe_tokens(pair);
       moe_settle();
-      if (pair >= 0) row_of[moe_rank(k, lane)] = pair;
+      if (pair >= 0) row_of[moe_rank(k, lane)] = (uint16_t)pair;
       moe_settle();
       place(k, row_of, 0, row, e);
     };
@@ -918,7 +920,7 @@ hipError_t launch_down(const MoeLayer& a, hipStream_t s) {
   constexpr int PH = moe_h_pieces(DT), WAVES = down_waves(MT, NS, PH);
   constexpr size_t staged = WAVES * sizeof(MoeStage<1, NS, PH>), joined = WAVES * MT * 1024;
   constexpr size_t bytes = staged > joined ? staged : joined;
-  static_assert(bytes + moe_most_list_bytes(MT) + WAVES * kMoeMaxTokens * 8 + 16 <= 160 * 1024, "LDS");
+  static_assert(bytes + moe_most_list_bytes(MT) + WAVES * kMoeMaxTokens * 4 + 16 <= 160 * 1024, "LDS");
   static std::atomic<bool> set[64];
   if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, NS, PH, WHOLE>, bytes + moe_most_list_bytes(MT), set);
       e != hipSuccess)
@@ -977,11 +979,11 @@ hipError_t launch(const MoeLayer& a, hipStream_t s) {
   // are staged again for those that are left): 16 where there are more than 5 an
   // expert.  32 tokens, 2 of 8 of 4096 x 14336 bfloat16: 300 us, with 8 at a time
   // 345.  They cost registers, and with them a workgroup a CU: 16 tokens there, 4 an
-  // expert, 210 us with 8.  (float32 above 32 tokens would spill with 16.)
+  // expert, 210 us with 8.  (Two pieces and more than 32 tokens would spill with 16.)
   const bool wide = 5 * a.experts < a.tokens * a.top_k;
   if (a.tokens <= 16) return wide ? launch_products<DT, 1, 16>(a, s) : launch_products<DT, 1, 8>(a, s);
   if (a.tokens <= 32) return wide ? launch_products<DT, 2, 16>(a, s) : launch_products<DT, 2, 8>(a, s);
-  return wide && DT != kF32 ? launch_products<DT, 4, DT == kF32 ? 8 : 16>(a, s) : launch_products<DT, 4, 8>(a, s);
+  return wide && DT == kBF16 ? launch_products<DT, 4, DT == kBF16 ? 16 : 8>(a, s) : launch_products<DT, 4, 8>(a, s);
 }
 
 }  // namespace
