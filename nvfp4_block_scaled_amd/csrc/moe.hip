@@ -42,6 +42,7 @@ namespace nvfp4 {
 namespace {
 
 typedef uint32_t u32x4_8 __attribute__((ext_vector_type(4), aligned(8)));
+typedef uint32_t u32_1 __attribute__((aligned(1)));
 
 constexpr int kUnit = 256;  // inner values of a row that a wave takes at a time: 64 a lane
 
@@ -293,9 +294,12 @@ struct MoeStage {
   }
 };
 
+// Rows of weights: whole 64s with their scales at whole dwords; any from 64 values
+// on; and shorter ones, whose every piece is tested.
+enum { kWhole, kAny, kShort };
+
 // One unit's weights on their way: lane l has chunk l % 8 of rows l / 8 and l / 8
-// + 8, and the scales of row l / 4, groups 4 (l % 4) ..  WHOLE: rows are whole
-// 64s and scales whole dwords.
+// + 8, and the scales of row l / 4, groups 4 (l % 4) ..
 //
 // No branch stands between a wave's loads, here and below: behind one the compiler
 // cannot count what is on its way, and waits for all of it.  So a lane past a
@@ -308,13 +312,13 @@ struct MoeWeights {
   u32x4 c[NR][2];
   uint32_t s[NR];
 };
-template <int NR, bool WHOLE>
+template <int NR, int ROWS>
 __device__ __forceinline__ void moe_load(MoeWeights<NR>& w, const uint8_t* codes, const uint8_t* scales, const int64_t (&row0)[NR],
                                          int inner, int unit) {
   const int lane = threadIdx.x & 63;
   const uint32_t row_bytes = inner / 2, groups = inner / 16;
   const int from = unit * kUnit + 32 * (lane & 7), group = unit * (kUnit / 16) + 4 * (lane & 3);
-  if constexpr (WHOLE) {
+  if constexpr (ROWS == kWhole) {
     const uint32_t code_at = (lane >> 3) * row_bytes + (from < inner ? 16 * (lane & 7) : 0);
     const uint32_t code_at2 = code_at + 8 * row_bytes;
     const uint32_t scale_at = (lane >> 2) * groups + (group < (int)groups ? 4 * (lane & 3) : 0);
@@ -325,6 +329,19 @@ __device__ __forceinline__ void moe_load(MoeWeights<NR>& w, const uint8_t* codes
       w.c[r][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + code_at));
       w.c[r][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + code_at2));
       w.s[r] = *reinterpret_cast<const uint32_t*>(s + scale_at);  // 8 units share a line: kept
+    }
+  } else if constexpr (ROWS == kAny) {
+    // A chunk or a dword of scales that would pass its row's end ends there with it
+    // (moe_stage moves it to its place).  Scales lie anywhere, and so do the loads.
+    const uint32_t code_at = (lane >> 3) * row_bytes + min(from, inner - 32) / 2;
+    const uint32_t scale_at = (lane >> 2) * groups + min(group, (int)groups - 4);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const uint8_t* c = codes + row0[r] * row_bytes;
+      const uint8_t* s = scales + row0[r] * groups;
+      w.c[r][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + code_at));
+      w.c[r][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_8*>(c + code_at + 8 * row_bytes));
+      w.s[r] = *reinterpret_cast<const u32_1*>(s + scale_at);
     }
   } else {
 #pragma unroll
@@ -350,15 +367,24 @@ __device__ __forceinline__ void moe_load(MoeWeights<NR>& w, const uint8_t* codes
     }
   }
 }
-template <bool WHOLE, int NR, int NS, int P>
+template <int ROWS, int NR, int NS, int P>
 __device__ __forceinline__ void moe_stage(MoeStage<NR, NS, P>& l, const MoeWeights<NR>& w, int inner, int unit) {
   const int lane = threadIdx.x & 63;
-  const bool there = !WHOLE || unit * kUnit + 64 * (lane & 3) < inner;
+  const bool there = unit * kUnit + 64 * (lane & 3) < inner;
+  const bool half = unit * kUnit + 32 * (lane & 7) == inner - 16;
+  const int over = max(unit * (kUnit / 16) + 4 * (lane & 3) - (inner / 16 - 4), 0);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
 #pragma unroll
-    for (int d = 0; d < 2; ++d) l.codes[r][(lane >> 3) + 8 * d][lane & 7] = w.c[r][d];
-    l.scales[r][lane >> 2][lane & 3] = there ? w.s[r] : 0u;
+    for (int d = 0; d < 2; ++d) {
+      u32x4 c = w.c[r][d];
+      if (ROWS == kAny && half) c = u32x4{c.z, c.w, 0u, 0u};
+      l.codes[r][(lane >> 3) + 8 * d][lane & 7] = c;
+    }
+    uint32_t scales = w.s[r];
+    if constexpr (ROWS == kWhole) scales = there ? scales : 0u;
+    if constexpr (ROWS == kAny) scales = over < 4 ? scales >> (8 * over) : 0u;
+    l.scales[r][lane >> 2][lane & 3] = scales;
   }
 }
 
@@ -521,7 +547,7 @@ constexpr int kUpWaves = 4, kUpAhead = 2;  // (3 ahead: 126 us for 124, 16 token
 // choice.  PX: pieces of x here (1 or 2).
 constexpr int up_groups_a_cu(int MT, int NS, int PX) { return MT * PX <= 2 && NS <= 8 ? 3 : 2; }
 
-template <int MT, int NS, int PX, int KW, bool WHOLE, bool CHOOSE>
+template <int MT, int NS, int PX, int KW, int ROWS, bool CHOOSE>
 __global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe_up_kernel(MoeLayer a, const uint16_t* x) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int rows_of[kUpWaves][2][kMoeMaxTokens];  // of this job's expert and the next one's: its tokens
@@ -621,7 +647,7 @@ __global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe
   int w_unit = share;
   int64_t w_row = (int64_t)expert_of(job) * 2 * a.f + job.tile * 16;
   auto load_weights = [&](MoeWeights<2>& to) {
-    moe_load<2, WHOLE>(to, a.up_codes, a.up_scales, {w_row, w_row + a.f}, a.k, w_unit);
+    moe_load<2, ROWS>(to, a.up_codes, a.up_scales, {w_row, w_row + a.f}, a.k, w_unit);
     if (w_unit + KW < units) {
       w_unit += KW;
     } else if (w_job.at + stride < jobs) {
@@ -659,7 +685,7 @@ __global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe
   for (;;) {
 #pragma unroll
     for (int j = 0; j < kUpAhead; ++j) {
-      moe_stage<WHOLE>(stage, w[j], a.k, u);
+      moe_stage<ROWS>(stage, w[j], a.k, u);
       moe_stage(stage, columns);
       moe_settle();
       const bool last = u + KW >= units, more_jobs = job.at + stride < jobs;
@@ -723,7 +749,7 @@ constexpr int kDownAhead = 3;  // (4: the same within 1 %)
 // 16 of 2048 x 4096, 16 units, 120 against 125; 4 of 32 of 2048 x 5760, 23 units,
 // 232 against 229, and there the rule ends).  Weights are on their way three units
 // ahead, columns one, over the experts' ends.
-template <int DT, int MT, int NS, int PH, bool WHOLE>
+template <int DT, int MT, int NS, int PH, int ROWS>
 __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(MoeLayer a) {
   constexpr int WAVES = down_waves(MT, NS, PH);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -750,7 +776,7 @@ __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(M
     int w_next = begin_at, w_which = which, w_unit = u;
     int64_t w_row = (int64_t)expert_of(which) * a.k + n0;
     auto load_weights = [&](MoeWeights<1>& to) {
-      moe_load<1, WHOLE>(to, a.down_codes, a.down_scales, {w_row}, a.f, w_unit);
+      moe_load<1, ROWS>(to, a.down_codes, a.down_scales, {w_row}, a.f, w_unit);
       if (w_next + stride < end_at) {
         w_next += stride;
         w_unit += stride;
@@ -817,7 +843,7 @@ __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(M
     for (;;) {
 #pragma unroll
       for (int j = 0; j < kDownAhead; ++j) {
-        moe_stage<WHOLE>(stage, w[j], a.f, u);
+        moe_stage<ROWS>(stage, w[j], a.f, u);
         moe_stage(stage, hidden, exponent, tokens.count);
         moe_settle();
         const int now = u;
@@ -907,13 +933,13 @@ hipError_t moe_allow_lds(K* kernel, size_t bytes, std::atomic<bool> (&set)[64]) 
 size_t moe_lists_bytes(const MoeLayer& a) { return 4 * (size_t)moe_list_words(a.tokens * a.top_k, a.experts); }
 constexpr size_t moe_most_list_bytes(int MT) { return 4 * (size_t)moe_list_words(16 * MT * kMoeMaxTopK, kMoeMaxExperts); }
 
-template <int DT, int MT, int NS, int KW, bool WHOLE, bool CHOOSE>
+template <int DT, int MT, int NS, int KW, int ROWS, bool CHOOSE>
 hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT) > 0 ? moe_x_pieces(DT) : 1;
   constexpr size_t bytes = kUpWaves * (sizeof(MoeStage<2, NS, PX>) + (KW > 1 ? 2 * MT * 1024 : 0));
   static_assert(bytes >= kChooseMost * 8, "the order of the logits fits");
   static std::atomic<bool> set[64];
-  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, NS, PX, KW, WHOLE, CHOOSE>, bytes + moe_most_list_bytes(MT), set);
+  if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, NS, PX, KW, ROWS, CHOOSE>, bytes + moe_most_list_bytes(MT), set);
       e != hipSuccess)
     return e;
   const int pairs = a.tokens * a.top_k, most = pairs < a.experts ? pairs : a.experts;
@@ -922,38 +948,42 @@ hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
   const int jobs = (most * (a.f / 16) + kUpWaves / KW - 1) / (kUpWaves / KW);
   const int resident = device_cu_count() * up_groups_a_cu(MT, NS, PX);
   const int groups = (jobs < resident ? jobs : resident) + (CHOOSE ? 1 : 0);
-  moe_up_kernel<MT, NS, PX, KW, WHOLE, CHOOSE><<<groups, 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
+  moe_up_kernel<MT, NS, PX, KW, ROWS, CHOOSE><<<groups, 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
   return hipGetLastError();
 }
 
-template <int DT, int MT, int NS, bool WHOLE>
+template <int DT, int MT, int NS, int ROWS>
 hipError_t launch_down(const MoeLayer& a, hipStream_t s) {
   constexpr int PH = moe_h_pieces(DT), WAVES = down_waves(MT, NS, PH);
   constexpr size_t staged = WAVES * sizeof(MoeStage<1, NS, PH>), joined = WAVES * MT * 1024;
   constexpr size_t bytes = staged > joined ? staged : joined;
   static_assert(bytes + moe_most_list_bytes(MT) + WAVES * kMoeMaxTokens * 4 + 16 <= 160 * 1024, "LDS");
   static std::atomic<bool> set[64];
-  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, NS, PH, WHOLE>, bytes + moe_most_list_bytes(MT), set);
+  if (const hipError_t e = moe_allow_lds(&moe_down_kernel<DT, MT, NS, PH, ROWS>, bytes + moe_most_list_bytes(MT), set);
       e != hipSuccess)
     return e;
-  moe_down_kernel<DT, MT, NS, PH, WHOLE><<<(unsigned)(a.k / 16), 64 * WAVES, bytes + moe_lists_bytes(a), s>>>(a);
+  moe_down_kernel<DT, MT, NS, PH, ROWS><<<(unsigned)(a.k / 16), 64 * WAVES, bytes + moe_lists_bytes(a), s>>>(a);
   return hipGetLastError();
 }
 
 template <int DT, int MT, int NS>
 hipError_t launch_products(const MoeLayer& a, hipStream_t s) {
-  auto whole = [](int inner, const uint8_t* scales) { return inner % 64 == 0 && (reinterpret_cast<uintptr_t>(scales) & 3) == 0; };
+  auto rows = [](int inner, const uint8_t* scales) {
+    return inner < 64 ? kShort : inner % 64 == 0 && (reinterpret_cast<uintptr_t>(scales) & 3) == 0 ? kWhole : kAny;
+  };
+  const int up = rows(a.k, a.up_scales), down = rows(a.f, a.down_scales);
   const bool inside = MT <= 2 && a.router && moe_choose_inside(a.tokens, a.experts);  // (most tokens of MT 4 pass it)
   // Up to three units are one wave's, without a join: 20 tokens float16, 3 of 9
   // experts of 128 x 1376 58 us against 65, of 768 x 1376 60 against 65.
   const bool alone = a.k <= 3 * kUnit;
   hipError_t e;
-#define MOE_UP(CHOOSE)                                                                                            \
-  do {                                                                                                            \
-    if (alone) e = whole(a.k, a.up_scales) ? launch_up<DT, MT, NS, 1, true, CHOOSE>(a, s)                         \
-                                           : launch_up<DT, MT, NS, 1, false, CHOOSE>(a, s);                       \
-    else e = whole(a.k, a.up_scales) ? launch_up<DT, MT, NS, kUpWaves, true, CHOOSE>(a, s)                        \
-                                     : launch_up<DT, MT, NS, kUpWaves, false, CHOOSE>(a, s);                      \
+#define MOE_UP(CHOOSE)                                                                                     \
+  do {                                                                                                     \
+    if (up == kShort) e = launch_up<DT, MT, 8, 1, kShort, CHOOSE>(a, s);                                   \
+    else if (alone) e = up == kWhole ? launch_up<DT, MT, NS, 1, kWhole, CHOOSE>(a, s)                      \
+                                     : launch_up<DT, MT, NS, 1, kAny, CHOOSE>(a, s);                       \
+    else e = up == kWhole ? launch_up<DT, MT, NS, kUpWaves, kWhole, CHOOSE>(a, s)                          \
+                          : launch_up<DT, MT, NS, kUpWaves, kAny, CHOOSE>(a, s);                           \
   } while (0)
   if constexpr (MT <= 2) {
     if (inside) MOE_UP(true);
@@ -961,12 +991,13 @@ hipError_t launch_products(const MoeLayer& a, hipStream_t s) {
   if (!inside) MOE_UP(false);
 #undef MOE_UP
   if (e != hipSuccess) return e;
+  if (down == kShort) return launch_down<DT, MT, 8, kShort>(a, s);
   if constexpr (MT == 1) {
     // Fewer columns to load and convert: 1 token, 2 of 8 of 4096 x 14336 17.0 us for
     // 21.1 with 8, 2 tokens, 8 of 64 of 2048 x 1024 12.6 for 13.9.
-    if (a.tokens <= 2) return whole(a.f, a.down_scales) ? launch_down<DT, 1, 2, true>(a, s) : launch_down<DT, 1, 2, false>(a, s);
+    if (a.tokens <= 2) return down == kWhole ? launch_down<DT, 1, 2, kWhole>(a, s) : launch_down<DT, 1, 2, kAny>(a, s);
   }
-  return whole(a.f, a.down_scales) ? launch_down<DT, MT, NS, true>(a, s) : launch_down<DT, MT, NS, false>(a, s);
+  return down == kWhole ? launch_down<DT, MT, NS, kWhole>(a, s) : launch_down<DT, MT, NS, kAny>(a, s);
 }
 
 template <int DT>
