@@ -160,6 +160,42 @@ def test_ties_and_equal_rows():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,e,top_k,k,f", [
+    (16, 2, 2, 1040, 144), (31, 3, 2, 832, 6160), (9, 2, 1, 64, 6400), (2, 4, 2, 1024, 6208), (40, 2, 1, 784, 4112),
+    (64, 1, 1, 1088, 112), (13, 3, 3, 784, 32)])
+def test_many_tokens_an_expert(dtype, t, e, top_k, k, f):
+    """More tokens of an expert than are met at a time, by long and short rows of either product."""
+    say(f"moe {dtype} {t} tokens, {top_k} of {e}, {k} x {f}")
+    run(t, e, top_k, k, f, dtype, 300 + t + e, normalize=(t + e) % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,k,f", [(3, 128, 64), (12, 1024, 832), (1, 192, 128)])
+def test_scales_anywhere(dtype, t, k, f):
+    """Scales that begin at any byte, before rows of whole 64s: as those that begin at a dword."""
+    e, top_k = 4, 2
+    x, router = inputs(t, e, k, dtype, 21)
+    w = Weights(e, k, f, 21)
+    (uc, us, dc, ds), more = w.args()
+
+    def moved(s, by):
+        room = torch.zeros(s.numel() + 8, dtype=torch.uint8, device="cuda")
+        there = room[by:by + s.numel()].view(s.shape)
+        there.copy_(s)
+        return there
+
+    want = nv.nvfp4_moe(x.cuda(), uc, us, dc, ds, router=router.cuda(), top_k=top_k, **more)
+    index, p = choose(x, router, top_k, True)
+    ref = reference(x, w, index, p)
+    check(want[0], ref, "at dwords")
+    for by in (1, 2, 3):
+        got = nv.nvfp4_moe(x.cuda(), uc, moved(us, by), dc, moved(ds, by), router=router.cuda(), top_k=top_k, **more)
+        torch.cuda.synchronize()
+        check(got[0], ref, f"{by} behind")
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_given_experts(dtype):
     """Without a router: indices outside the experts, the same expert twice, tokens without any."""
     t, e, k, f, top_k = 20, 6, 144, 80, 4
