@@ -851,7 +851,10 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
  *   the other arguments, the numbers and the errors as nvfp4_kv_attention with
  *   query_starts, which must not be NULL here.
  * Errors besides: tree_words too small (or of 2^25 or more), NULL or
- * misaligned tree or positions.
+ * misaligned tree or positions; UNSUPPORTED where a head has more than 32 rows,
+ * r = max_queries * query_heads / heads, and seqs * heads * (r / 128 rounded up)
+ * * (keys / 256 + 1) is above 2^30, with keys = max_context, or window +
+ * max_queries if that is less.
  */
 size_t nvfp4_kv_tree_attention_workspace_size(const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
                                               int64_t seqs, int64_t max_queries, int64_t max_context,

@@ -1481,6 +1481,12 @@ static nvfp4_status check_kv_attention(const char* op, const nvfp4::KvCache& c, 
   return NVFP4_OK;
 }
 
+static nvfp4_status check_tree_units(const char* op, const nvfp4::KvCache& c, const nvfp4::KvAttention& a) {
+  if (nvfp4::kv_tree_attention_fits(c, a)) return NVFP4_OK;
+  return fail(NVFP4_ERR_UNSUPPORTED,
+              "[%s] Sizes too large (units of 128 rows and 256 keys, of every sequence and head, above 2^30).", op);
+}
+
 static size_t attend_workspace(const char* op, const nvfp4_kv_cache* cache, int64_t tokens, int64_t query_heads,
                                int64_t seqs, int64_t max_queries, int64_t max_context, int64_t window, bool tree) {
   nvfp4::KvCache c;
@@ -1488,6 +1494,7 @@ static size_t attend_workspace(const char* op, const nvfp4_kv_cache* cache, int6
   if (check_kv(op, cache, NVFP4_BF16, tokens, &c) ||
       check_kv_attention(op, c, tokens, query_heads, seqs, max_queries, max_context, window, &a))
     return 0;
+  if (tree && check_tree_units(op, c, a)) return 0;
   if (tokens == 0 || seqs == 0) return 0;
   return tree ? nvfp4::kv_tree_attention_workspace(c, a) : nvfp4::kv_attention_workspace(c, a);
 }
@@ -1539,6 +1546,7 @@ static nvfp4_status attend(const char* op, const nvfp4_kv_cache* cache, const vo
                 "[%s] without query_starts every sequence has one query: tokens must equal seqs "
                 "and max_queries 1.", op);
   if (tree) {
+    if (nvfp4_status st = check_tree_units(op, c, a)) return st;
     if (!query_starts) return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] query_starts must not be NULL.", op);
     if (tree->words <= 0 || tree->words > (INT32_MAX >> 6) || tree->words * 64 < max_queries)
       return fail(NVFP4_ERR_INVALID_ARGUMENT, "[%s] tree_words (%lld) must hold a bit for each of max_queries (%lld).", op,

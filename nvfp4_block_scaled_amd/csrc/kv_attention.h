@@ -1779,7 +1779,14 @@ struct KvPlan {
   size_t sums_bytes, bytes;
 };
 
+constexpr int kFewRows = 32;
 constexpr int few_groups(int dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : dim <= 192 ? 3 : 4; }
+
+// Keys that the rows of a sequence may see at most.
+int64_t kv_most_keys(const KvAttention& a) {
+  const int64_t window = (int64_t)a.window + a.max_queries;
+  return a.window > 0 && window < a.max_keys ? window : a.max_keys;
+}
 
 // Up to 32 rows a (sequence, kv head) the keys are streamed once past all of
 // them; more rows are matrix work.  32 rows, 8 x 30000 keys, 4 heads, few
@@ -1789,11 +1796,10 @@ constexpr int few_groups(int dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : dim 
 KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split, bool tree) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_queries * a.groups;
-  int64_t keys = a.max_keys;
-  if (a.window > 0 && keys > (int64_t)a.window + a.max_queries) keys = (int64_t)a.window + a.max_queries;
+  const int64_t keys = kv_most_keys(a);
   const int64_t pairs = (int64_t)a.seqs * c.heads;
   size_t parts;
-  p.few = rows <= 32;
+  p.few = rows <= kFewRows;
   if (p.few) {
     p.mt = rows <= 16 ? 1 : 2;
     // as many workgroups as run at once, but no more than there can be units

@@ -48,6 +48,8 @@ struct KvAttention {
 };
 size_t kv_attention_workspace(const KvCache& c, const KvAttention& a);
 hipError_t launch_kv_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s);
+// whether the units of a launch can be counted; the next two are for calls that fit
+bool kv_tree_attention_fits(const KvCache& c, const KvAttention& a);
 size_t kv_tree_attention_workspace(const KvCache& c, const KvAttention& a);
 hipError_t launch_kv_tree_attention(const KvCache& c, const KvAttention& a, int dt, void* workspace, hipStream_t s);
 
