@@ -1531,9 +1531,20 @@ constexpr int kManyStep = 256;
 struct KvTreeShare {
   int groups;     // workgroups of the launch
   int row_tiles;  // of a sequence and kv head, at most
-  float* sums;    // [groups + seqs * heads * row_tiles][128][dim], times 2^kBias; null: units are whole
+  bool by_first;  // which number of a tile goes into its parts' (tree_part)
+  float* sums;    // [parts][128][dim], times 2^kBias; null: units are whole
   float* stats;   // .. [2]: maximum (log2), sum
 };
+// The part of a tile (its number among all that there may be) that workgroup
+// `group` has, when the tile's units begin in workgroup `first`'s share and end in
+// another's.  No two parts have the same: of two tiles the later one's number is
+// larger and its units are no earlier workgroups'; and as only the last tile that
+// begins in a share ends in another, the first workgroup will do for a number of the
+// tile.  Parts are as many as workgroups and the numbers, so whichever are fewer
+// are taken: 256 sequences of 8 heads and 256 rows, heads of 128, 68 MB for 307.
+__device__ __forceinline__ int64_t tree_part(const KvTreeShare& sh, int group, int first, int64_t tile) {
+  return group + (sh.by_first ? first : tile);
+}
 // Sequences 64 at a time, one per lane, and the units before them: as KvScan.
 struct KvTreeScan {
   KvRange range;
@@ -1588,11 +1599,11 @@ __global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1)) kv_tree_kernel
     asm volatile("" : "+s"(p));
     return (const KvTreeArgs*)p;
   };
-  int unit, last, base = 0, before = 0;
+  int each, unit, last, base = 0, before = 0;
   {
     const KvTreeArgs& args = *arguments();
     KvTreeScan scan;
-    const int each = __builtin_amdgcn_readfirstlane(tree_units_each(args.c, args.a, args.sh.groups, scan));
+    each = __builtin_amdgcn_readfirstlane(tree_units_each(args.c, args.a, args.sh.groups, scan));
     unit = __builtin_amdgcn_readfirstlane((int)blockIdx.x * each);
     last = unit + each;
   }
@@ -1620,8 +1631,7 @@ __global__ void __launch_bounds__(256, (NG * SPLIT <= 2 ? 2 : 1)) kv_tree_kernel
     const int take = min(units - off, last - unit);
     const int row_tile = __builtin_amdgcn_readfirstlane(tile / c.heads), head = tile - row_tile * c.heads;
     const int begin = rg.lo + off * kManyStep, end = min(rg.hi, begin + take * kManyStep);
-    // Part number: of this workgroup and of the tile, which no other part has both.
-    const int64_t part = (int64_t)blockIdx.x + ((int64_t)b * args.sh.row_tiles * c.heads + tile);
+    const int64_t part = tree_part(args.sh, blockIdx.x, (unit - off) / each, (int64_t)b * args.sh.row_tiles * c.heads + tile);
     kv_many_rows<NG, SPLIT, EXACT, true>(c, a, sp, args.dt, args.q_vec, lds, b, head, row_tile * kManyRows, rg, begin, end, 0,
                                          take == units, part * kManyRows);
     unit += take;
@@ -1738,7 +1748,7 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention
   const int u0 = __builtin_amdgcn_readlane(scan.first, b - base) + tile * units;
   const int g0 = u0 / each, g1 = (u0 + units - 1) / each;
   if (g0 == g1) return;  // one workgroup had it all
-  const int64_t at = ((int64_t)g0 + (int64_t)b * sh.row_tiles * c.heads + tile) * kManyRows + r % kManyRows;
+  const int64_t at = tree_part(sh, g0, g0, (int64_t)b * sh.row_tiles * c.heads + tile) * kManyRows + r % kManyRows;
   kv_join<1>(c, a, dt, sh.sums, sh.stats, at, kManyRows, g1 - g0 + 1, (int64_t)(first + qi) * a.query_heads + qh);
 }
 
@@ -1776,6 +1786,7 @@ struct KvPlan {
   bool few;
   int mt, groups;                 // few rows: row tiles of 16, workgroups
   int row_tiles, chunk, splits;   // many rows
+  bool by_first;                  // trees
   size_t sums_bytes, bytes;
 };
 
@@ -1815,7 +1826,8 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split, bool tree) {
     const int64_t each = keys > kManyStep ? (keys + kManyStep - 1) / kManyStep : 1;
     const int64_t units = tiles > most ? most : tiles * each;  // (without overflow)
     p.groups = (int)(each == 1 ? tiles : units < most ? units : most);
-    parts = each == 1 ? 0 : (size_t)(p.groups + tiles) * kManyRows;
+    p.by_first = tiles > p.groups;
+    parts = each == 1 ? 0 : (size_t)(p.groups + (p.by_first ? p.groups : tiles)) * kManyRows;
   } else {
     p.row_tiles = (int)((rows + kManyRows - 1) / kManyRows);
     const int64_t tiles = pairs * p.row_tiles;
@@ -1909,7 +1921,7 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const KvPlan& p, int d
     if (e != hipSuccess || p.bytes == 0) return e;
     kv_join_few_kernel<TREE><<<rows, 256, 0, s>>>(c, a, sh, dt);
   } else if constexpr (TREE) {
-    const KvTreeShare sh{p.groups, p.row_tiles, sums, stats};
+    const KvTreeShare sh{p.groups, p.row_tiles, p.by_first, sums, stats};
     const hipError_t e = launch_tree<NG, EXACT>(c, a, sh, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
     kv_join_tree_kernel<<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sh, dt);

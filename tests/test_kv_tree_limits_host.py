@@ -66,3 +66,14 @@ def test_few_rows_have_no_row_tiles(L):
         assert "gfx950" in text, text
     text, _ = says(L, 8193, 4, 1, 32, (1 << 22) - 1)
     assert "too large" in text, text
+
+
+def test_workspace_is_that_of_the_workgroups(L):
+    """A workgroup leaves two unfinished tiles at most, however many tiles there are: 512 workgroups of two parts of
+    128 rows, not a part for every (sequence, head, 128 rows)."""
+    cache = nv._KVCacheStruct(A, B, C, D, None, None, 64, 1 << 16, 8, 128)
+    for seqs, queries in ((256, 64), (60000, 64), (16, 4096)):
+        need = L.nvfp4_kv_tree_attention_workspace_size(cache, 2 ** 24, 32, seqs, queries, 4000, 0)
+        assert 0 < need <= 2 * 512 * 128 * (4 * 128 + 8) + 512, (seqs, queries, need)
+    one = L.nvfp4_kv_tree_attention_workspace_size(cache, 64, 32, 1, 64, 4000, 0)
+    assert 0 < one <= (8 * 2 * 16 + 8 * 2) * 128 * (4 * 128 + 8) + 512  # units and tiles of a single sequence
