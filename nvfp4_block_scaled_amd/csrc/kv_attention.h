@@ -1825,7 +1825,13 @@ KvPlan kv_plan(const KvCache& c, const KvAttention& a, int split, bool tree) {
     const int64_t tiles = pairs * p.row_tiles, most = (int64_t)device_cu_count() * (few_groups(c.dim) * split <= 2 ? 2 : 1);
     const int64_t each = keys > kManyStep ? (keys + kManyStep - 1) / kManyStep : 1;
     const int64_t units = tiles > most ? most : tiles * each;  // (without overflow)
-    p.groups = (int)(each == 1 ? tiles : units < most ? units : most);
+    // Tiles of one unit each need no parts: up to twice as many workgroups as run at
+    // once they take one each, more tiles are shared out too (us, one each against
+    // shared out, 8 heads of 128, contexts of up to 256: 64 sequences of 64 drafts,
+    // 1024 tiles, 53 / 57; 200, 3200 tiles, 126 / 121; 2000 of 33 in heads of 64,
+    // 32000 tiles whose workgroups all count the sequences, 2280 / 425), so that no
+    // launch has more than some thousand workgroups.
+    p.groups = (int)(each == 1 && tiles <= 2 * most ? tiles : units < most ? units : most);
     p.by_first = tiles > p.groups;
     parts = each == 1 ? 0 : (size_t)(p.groups + (p.by_first ? p.groups : tiles)) * kManyRows;
   } else {

@@ -185,6 +185,23 @@ def test_short_contexts_without_parts(dtype):
     assert nv.kv_tree_attention_workspace(cache, sum(counts), 32, 90, 64, 256)[1] == 0
 
 
+def test_many_sequences_of_short_contexts():
+    """65535 sequences of 64 heads, four million tiles of one unit: a workgroup each, all of which count the sequences,
+    would take minutes.  Only the last few have queries."""
+    seqs, heads, dim, page = 65535, 64, 16, 16
+    few, n = 9, 40
+    contexts, counts = [0] * (seqs - few) + [200] * few, [0] * (seqs - few) + [n] * few
+    table = torch.full((seqs, 16), -1, dtype=torch.int32)
+    table[-few:, :13] = torch.randperm(13 * few, generator=torch.Generator().manual_seed(1)).view(few, 13).int()
+    cache = _kv.random_cache(13 * few, page, heads, dim, 47)
+    q = torch.randn(few * n, heads, dim, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    starts = [0] * (seqs - few) + [n * i for i in range(few + 1)]
+    tree, depths = nv.kv_trees(random_trees([n] * few, 3))
+    got, lse = call(q, cache, table, contexts, starts, tree, depths, 0, most=n, top=256)
+    ref = reference(q, cache, table[-few:], contexts[-few:], starts[-few - 1:], dim ** -0.5, tree, depths, 0)
+    _kv.check(got, lse, ref, "65535 sequences")
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("seqs", [40, 150])
 def test_few_rows_shared_out(dtype, seqs):
