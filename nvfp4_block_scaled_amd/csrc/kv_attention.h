@@ -1726,9 +1726,10 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention
   kv_join<kFewWaves>(c, a, dt, sh.sums, sh.stats, at, sh.rows, parts, (int64_t)(rg.first + qi) * a.query_heads + qh);
 }
 
-// A wave a row of a tree.
-[[maybe_unused]] __global__ void __launch_bounds__(256) kv_join_tree_kernel(KvCache c, KvAttention a, KvTreeShare sh, int dt) {
-  const int b = blockIdx.y, row_of = blockIdx.x * 4 + (threadIdx.x >> 6);
+// ROWS waves, each of which takes a row of a tree.
+template <int ROWS>
+__global__ void __launch_bounds__(64 * ROWS) kv_join_tree_kernel(KvCache c, KvAttention a, KvTreeShare sh, int dt) {
+  const int b = blockIdx.y, row_of = blockIdx.x * ROWS + (threadIdx.x >> 6);
   const int qi = row_of / a.query_heads, qh = row_of - qi * a.query_heads;
   const int head = qh / a.groups, r = qi * a.groups + qh - head * a.groups;
   KvTreeScan scan;
@@ -1752,8 +1753,9 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(KvCache c, KvAttention
   kv_join<1>(c, a, dt, sh.sums, sh.stats, at, kManyRows, g1 - g0 + 1, (int64_t)(first + qi) * a.query_heads + qh);
 }
 
-[[maybe_unused]] __global__ void __launch_bounds__(256) kv_join_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt) {
-  const int row_of = blockIdx.x * 4 + (threadIdx.x >> 6);
+template <int ROWS>
+__global__ void __launch_bounds__(64 * ROWS) kv_join_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt) {
+  const int row_of = blockIdx.x * ROWS + (threadIdx.x >> 6);
   const int qi = row_of / a.query_heads, qh = row_of - qi * a.query_heads;
   const int r = qi * a.groups + qh % a.groups;  // its row among those of its kv head
   const KvRange rg = kv_range<false>(a, blockIdx.y, r / kManyRows * kManyRows, kManyRows);
@@ -1930,12 +1932,12 @@ hipError_t launch(const KvCache& c, const KvAttention& a, const KvPlan& p, int d
     const KvTreeShare sh{p.groups, p.row_tiles, p.by_first, sums, stats};
     const hipError_t e = launch_tree<NG, EXACT>(c, a, sh, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
-    kv_join_tree_kernel<<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sh, dt);
+    kv_join_tree_kernel<4><<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sh, dt);
   } else {
     const KvChunks sp{p.chunk, p.splits, p.row_tiles, sums, stats};
     const hipError_t e = launch_many<NG, EXACT>(c, a, sp, dt, q_vec, s);
     if (e != hipSuccess || p.bytes == 0) return e;
-    kv_join_many_kernel<<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sp, dt);
+    kv_join_many_kernel<4><<<dim3((rows.x + 3) / 4, rows.y), 256, 0, s>>>(c, a, sp, dt);
   }
   return hipGetLastError();
 }
