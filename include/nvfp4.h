@@ -631,7 +631,8 @@ nvfp4_status nvfp4_mx_gather_qmm(const void* x, nvfp4_dtype dt, nvfp4_mx_mode mo
  * with inputs or each other leave them undefined.
  * Errors: bad dtype or mode, rows < 0 (rows = 0 is a no-op), k not a positive
  * multiple of 32, eps not positive, NULL codes or scales, misaligned pointers,
- * sum equal to normed; UNSUPPORTED for 2^22 rows or more, k above 2^30.
+ * sum equal to normed; UNSUPPORTED for 2^22 rows or more (more than 2^22 - 256
+ * if packed with k above 16384), k above 2^30.
  */
 nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* weight, nvfp4_dtype dt,
                                nvfp4_mx_mode mode, int64_t rows, int64_t k, double eps, int packed,

@@ -1224,8 +1224,10 @@ nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* 
     if (sum && sum == normed)
       return fail(NVFP4_ERR_INVALID_ARGUMENT, "[mx_rms_norm] sum and normed must be different memory.");
   }
-  if (rows >= (int64_t)1 << 22 || k > (int64_t)1 << 30)
-    return fail(NVFP4_ERR_UNSUPPORTED, "[mx_rms_norm] Sizes too large (2^22 rows or more, or k above 2^30).");
+  if (rows >= (int64_t)1 << 22 || k > (int64_t)1 << 30 || (packed && k > nvfp4::kMxNormLong && rows > (1 << 22) - 256))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "[mx_rms_norm] Sizes too large (2^22 rows or more, more than 2^22 - 256 packed ones with k above %d, or k above 2^30).",
+                nvfp4::kMxNormLong);
   if (nvfp4_status st = check_device(op, stream)) return st;
   if (rows == 0) return ok();
   const StreamDevice on(stream);

@@ -19,7 +19,11 @@ struct MxNorm {
   double eps;
   bool packed;                        // codes and scales in the operand layout of mx_codec.hip
 };
-// bits: 4 (mxfp4) or 8 (mxfp8); fewer than 2^31 - 64 rows, k below 2^31
+// A launch has fewer than 2^24 workgroups of 256 threads, and 2^22 of the 1024 that
+// take a row of more than kMxNormLong values; packed rows are rounded up to 256.
+constexpr int kMxNormLong = 16384;
+// bits: 4 (mxfp4) or 8 (mxfp8); fewer than 2^22 rows (packed ones of more than
+// kMxNormLong values: at most 2^22 - 256), k at most 2^30
 hipError_t launch_mx_norm(const MxNorm& n, int dt, int bits, hipStream_t s);
 
 struct KvRotate {

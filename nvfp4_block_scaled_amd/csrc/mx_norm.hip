@@ -230,7 +230,7 @@ hipError_t launch(const MxNorm& n, hipStream_t s) {
   // residual to packed mxfp8: 48 us, 4.9 TB/s; a wave a row, 64 values a lane, 55).
   if (pieces <= 128) MX_NORM(64, 2, false);
   if (pieces <= 512) MX_NORM(256, 2, false);
-  if (pieces <= 2048) MX_NORM(256, 8, false);
+  if (pieces <= kMxNormLong / 8) MX_NORM(256, 8, false);
   MX_NORM(1024, 4, true);
 #undef MX_NORM
 }
