@@ -753,7 +753,7 @@ nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const vo
  *                not overlap the inputs
  * Errors: as nvfp4_kv_write; rotary_dim out of range or no multiple of 16,
  * table_rows < 0, query_heads < 0, NULL or misaligned table, positions, q or
- * q_out; UNSUPPORTED for 2^26 tokens or more, query_heads above 65535,
+ * q_out; UNSUPPORTED for more than 2^26 - 4 tokens, query_heads above 65535,
  * table_rows of 2^31 or more.
  */
 nvfp4_status nvfp4_kv_write_rotated(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,

@@ -1410,7 +1410,8 @@ nvfp4_status nvfp4_kv_write_rotated(const nvfp4_kv_cache* cache, const void* k, 
       return fail(NVFP4_ERR_INVALID_ARGUMENT,
                   "[kv_write_rotated] table and q_out must be 16-byte aligned, the others to their elements.");
   }
-  if (tokens >= (int64_t)1 << 26 || query_heads > 65535 || table_rows > INT32_MAX)
+  // (four tokens a workgroup of 256, of which a launch has fewer than 2^24)
+  if (tokens > ((int64_t)1 << 26) - 4 || query_heads > 65535 || table_rows > INT32_MAX)
     return fail(NVFP4_ERR_UNSUPPORTED, "[kv_write_rotated] Sizes too large.");
   if (nvfp4_status st = check_device(op, stream)) return st;
   if (tokens == 0) return ok();

@@ -29,7 +29,7 @@ hipError_t launch_mx_norm(const MxNorm& n, int dt, int bits, hipStream_t s);
 struct KvRotate {
   const void *k, *v, *q;  // q may be null with query_heads 0
   void* q_out;            // [tokens, query_heads, dim]
-  int64_t tokens;         // below 2^26
+  int64_t tokens;         // at most 2^26 - 4
   int64_t k_token, k_head, v_token, v_head, q_token, q_head;  // strides in elements
   const int64_t* slots;
   const int32_t* positions;

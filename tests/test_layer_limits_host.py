@@ -1,4 +1,4 @@
-"""The largest launches of nvfp4_mx_rms_norm, on the host: a launch has fewer than 2^32 threads in
+"""The largest launches of nvfp4_mx_rms_norm and nvfp4_kv_write_rotated, on the host: a launch has fewer than 2^32 threads in
 a dimension, and what would take more is refused as such, not by the runtime (no GPU, no kernel)."""
 import os
 
@@ -27,5 +27,14 @@ def L():
     (2 ** 22 - 1, 16384, 1, True), (2 ** 22 - 1, 1 << 20, 0, True), (2 ** 22, 32, 0, False)])
 def test_norm(L, rows, k, packed, fits):
     assert L.nvfp4_mx_rms_norm(A, None, None, 2, 8, rows, k, 1e-6, packed, None, None, B, C, None) == UNSUP
+    text = L.nvfp4_last_error().decode()
+    assert ("gfx950" if fits else "too large") in text, text
+
+
+@pytest.mark.parametrize("tokens,fits", [(2 ** 26 - 4, True), (2 ** 26 - 3, False), (2 ** 26, False)])
+def test_rotation(L, tokens, fits):
+    """256 threads take four tokens."""
+    cache = nv._KVCacheStruct(A, B, C, D, None, None, 10, 16, 1, 16)
+    assert L.nvfp4_kv_write_rotated(cache, A, B, 2, tokens, 16, 16, 16, 16, C, D, E, 100, 16, 0, None, 0, 0, 0, None, None) == UNSUP
     text = L.nvfp4_last_error().decode()
     assert ("gfx950" if fits else "too large") in text, text
