@@ -840,7 +840,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp
  *     j > positions[i] - window;
  *   - key L - n + d, draft d's: if bit d % 64 of word d / 64 of its row of
  *     `tree` is set (its ancestors' bits as a rule, and its own; nothing is
- *     added to them, and a window does not touch them)
+ *     added to them, and a window does not touch them: where the ancestors reach
+ *     further back than it, the caller leaves the bits of those out)
  * as far as j < L and the page's number lies in [0, pages).  With L < n the
  * first n - L drafts have no key.
  *   tree        device uint64 [tokens, tree_words], 8-byte aligned; bits from n

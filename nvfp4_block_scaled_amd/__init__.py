@@ -1210,11 +1210,13 @@ def nvfp4_kv_attention(q, cache, page_table, context_lens, query_starts=None, ma
     return (out, lse) if return_lse else out
 
 
-def kv_trees(parents):
+def kv_trees(parents, window=0):
     """(tree int64 [tokens, words], depths int32 [tokens]) of drafted tokens on the CPU, from their parents: a list
     for each sequence with the index of each draft's parent among the drafts before it, -1 for one that follows
-    the context.  A draft sees its ancestors and itself; its position is the context's before the drafts plus its
-    depth."""
+    the context.  A draft sees its ancestors and itself, with window > 0 those that are fewer than window levels
+    above it; its position is the context's before the drafts plus its depth."""
+    if window < 0:
+        raise ValueError("window must be >= 0")
     words = max((-(-len(p) // 64) for p in parents), default=1) or 1
     rows, depths = [], []
     for sequence in parents:
@@ -1224,6 +1226,12 @@ def kv_trees(parents):
                 raise ValueError(f"draft {d}: its parent ({p}) must be an earlier draft, or -1")
             bits.append(1 << d | (bits[p] if p >= 0 else 0))
             depth.append(depth[p] + 1 if p >= 0 else 0)
+            # (the parent sees no further back than its own window: one more ancestor leaves it at most)
+            if window and depth[d] >= window:
+                away = d
+                for _ in range(window):
+                    away = sequence[away]
+                bits[d] &= ~(1 << away)
         depths += depth
         for b in bits:
             parts = [b >> 64 * w & 2 ** 64 - 1 for w in range(words)]
@@ -1250,8 +1258,8 @@ def nvfp4_kv_tree_attention(q, cache, page_table, context_lens, query_starts, tr
                             scale=None, positions=None, window=0, return_lse=False, out=None, workspace=None):
     """nvfp4_kv_attention for drafted tokens that form trees.  A sequence's queries are the last n tokens of its
     context; tree int64 [tokens, words] holds a bit for each draft of the query's sequence that it sees, its own
-    among them (kv_trees); the tokens before the drafts are seen by all, with window > 0 those behind positions
-    (int32 [tokens]) - window.  max_queries bounds a sequence's drafts (without it: all tokens, or as many as
+    among them (kv_trees, which takes the window too); the tokens before the drafts are seen by all, with window > 0
+    those behind positions (int32 [tokens]) - window.  max_queries bounds a sequence's drafts (without it: all tokens, or as many as
     tree has bits, may be one sequence's).  No gradient passes through the call."""
     stream = _kv_stream(cache)
     if stream is None:

@@ -235,6 +235,25 @@ def test_values_that_are_no_number_in_later_runs(dtype, groups):
     assert torch.equal(got[hit][..., rest.cuda()], want[hit][..., rest.cuda()])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,groups", [(7, 4), (70, 4), (130, 1)])
+@pytest.mark.parametrize("window", [1, 3, 65, 150])
+def test_a_chain_with_a_window_is_causal(dtype, n, groups, window):
+    """A chain of drafts behind a window, also one shorter than the chain, is nvfp4_kv_attention's: each answer is
+    within its bound of the 64-bit one."""
+    contexts = [n, 100 + n, 1500, 77 + n]
+    table, cache, starts, q = setup(contexts, [n] * 4, 2, groups, 64, 16, dtype, 90 + n)
+    tree, depths = nv.kv_trees([list(range(-1, n - 1))] * 4, window)
+    positions = (torch.repeat_interleave(torch.tensor(contexts) - n, n) + depths).int()
+    got, lse = call(q, cache, table, contexts, starts, tree, positions, window)
+    ref = _kv.reference(q, cache, table, torch.tensor(contexts), starts, 0.125, window=window)
+    _kv.check(got, lse, ref, f"chain {n} window {window}")
+    same, same_lse = nv.nvfp4_kv_attention(
+        q, cache, table.cuda(), torch.tensor(contexts, dtype=torch.int32, device="cuda"),
+        torch.tensor(starts, dtype=torch.int32, device="cuda"), max_queries=n, window=window, return_lse=True)
+    _kv.check(same, same_lse, ref, f"tokens {n} window {window}")
+
+
 @pytest.mark.parametrize("counts,contexts", [([40, 64, 50], [2600, 5000, 900]), ([4, 8, 2], [2600, 9000, 900])])
 def test_graphs_on_other_contents(counts, contexts):
     """A captured launch with its parts and join, replayed on other queries, codes, lengths and masks."""
