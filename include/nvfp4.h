@@ -651,7 +651,8 @@ nvfp4_status nvfp4_mx_rms_norm(const void* x, const void* residual, const void* 
  *     g = x . gate_up_hat[e, i], u = x . gate_up_hat[e, f + i],
  *     h_i = g / (1 + exp(-g)) * u                                   (i < f)
  *     out[t] = T( sum_j expert_weights[t, j] * down_hat[e_j] h )
- * float32 sums of exact products before the global scales, one rounding to T.
+ * float32 sums of exact products before the global scales, one rounding to T;
+ * g, u, h and out have float32's range, the sums before the scales more.
  * x and h enter the products as float16 times a power of two of their row: x of
  * 16 bits exactly (what is below 2^-27 of its row's largest to within 2^-38 of
  * that), x of float32 and h of float16 and float32 layers with 22 bits, h of

@@ -73,6 +73,18 @@ __device__ __forceinline__ void moe_pieces(const float (&v)[4], int e, u32x2 (&p
   }
 }
 
+// A global scale's decode factor as a number of 0.5 .. 1 and a power of two, which
+// goes with the row's: a sum times the factor alone, or times the row's power alone,
+// can pass float32's range where the layer does not.
+struct MoeFactor {
+  float by;
+  int exponent;
+};
+__device__ __forceinline__ MoeFactor moe_factor(const float* global, int expert) {
+  const float factor = global_decode(global ? global + expert : nullptr);
+  return MoeFactor{__builtin_amdgcn_frexp_mantf(factor), __builtin_amdgcn_frexp_expf(factor)};
+}
+
 // ----------------------------------------------------------------- router
 
 __device__ __forceinline__ double moe_wave_sum(double v) {
@@ -590,13 +602,13 @@ __global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe
   auto hidden = [&](const Job& job, int m, const f32x4& g, const f32x4& v) {
     const int expert = expert_of(job), f0 = job.tile * 16;
     const int t = 16 * m + (lane & 15), p = moe_pair(a, lists, t, expert);
-    const int e = lists.exponent[min(t, a.tokens - 1)];
-    const float factor = global_decode(a.up_global ? a.up_global + expert : nullptr);
+    const MoeFactor factor = moe_factor(a.up_global, expert);
+    const int e = lists.exponent[min(t, a.tokens - 1)] + factor.exponent;
     f32x4 h;
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x1 = __builtin_ldexpf(g[i] * factor, e), x2 = __builtin_ldexpf(v[i] * factor, e);
+      const float x1 = __builtin_ldexpf(g[i] * factor.by, e), x2 = __builtin_ldexpf(v[i] * factor.by, e);
       h[i] = x1 / (1.0f + expf(-x1)) * x2;
       top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
     }
@@ -820,7 +832,7 @@ __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(M
     };
     auto end = [&]() {  // adds the sums of expert `which`
       const int expert = expert_of(which);
-      const float factor = global_decode(a.down_global ? a.down_global + expert : nullptr);
+      const MoeFactor factor = moe_factor(a.down_global, expert);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int t = 16 * m + (lane & 15);
@@ -829,8 +841,8 @@ __global__ void __launch_bounds__(64 * down_waves(MT, NS, PH)) moe_down_kernel(M
         float weight = 0.0f;
         for (int q = p; q < (t + 1) * a.top_k; ++q)  // an expert may stand twice among a token's
           if (lists.idx[q] == expert) weight += lists.weight[q];
-        weight *= factor;
-        const int e = lists.exponent[p];
+        weight *= factor.by;
+        const int e = lists.exponent[p] + factor.exponent;
 #pragma unroll
         for (int i = 0; i < 4; ++i) total[m][i] += weight * __builtin_ldexpf(acc[0][m][i], e);
       }
