@@ -557,12 +557,27 @@ constexpr int kUpWaves = 4, kUpAhead = 2;  // (3 ahead: 126 us for 124, 16 token
 // columns one, over the jobs' ends; at a job's end one wave in turn joins the four
 // sums while the others go on.  CHOOSE: moe_choose_inside, and the last workgroup writes the
 // choice.  PX: pieces of x here (1 or 2).
-constexpr int up_groups_a_cu(int MT, int NS, int PX) { return MT * PX <= 2 && NS <= 8 ? 3 : 2; }
+constexpr size_t kUpRows = kUpWaves * 2 * kMoeMaxTokens * sizeof(int);
+// LDS without the lists: the waves' stages and, for the join, their sums.
+template <int MT, int NS, int PX, int KW>
+constexpr size_t up_bytes() {
+  return kUpWaves * (sizeof(MoeStage<2, NS, PX>) + (KW > 1 ? 2 * MT * 1024 : 0));
+}
+// Workgroups of a CU: what has room in registers, and in LDS beside lists of `lists`
+// bytes (32 tokens, 8 of 64 of 2048 x 1024, bfloat16, two a CU for a launch of three: 120
+// us for 133; float32 with 16 columns at a time, one for two: 42 for 45, 16 tokens, 2 of 2 of 2048 x 4096).
+template <int MT, int NS, int PX, int KW>
+constexpr int up_groups_a_cu(size_t lists) {
+  constexpr int registers = MT * PX <= 2 && NS <= 8 ? 3 : 2;
+  const int room = (int)(160 * 1024 / (up_bytes<MT, NS, PX, KW>() + kUpRows + lists));
+  return room < 1 ? 1 : room < registers ? room : registers;
+}
 
 template <int MT, int NS, int PX, int KW, int ROWS, bool CHOOSE>
-__global__ void __launch_bounds__(64 * kUpWaves, up_groups_a_cu(MT, NS, PX)) moe_up_kernel(MoeLayer a, const uint16_t* x) {
+__global__ void __launch_bounds__(64 * kUpWaves, (up_groups_a_cu<MT, NS, PX, KW>(0))) moe_up_kernel(MoeLayer a, const uint16_t* x) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int rows_of[kUpWaves][2][kMoeMaxTokens];  // of this job's expert and the next one's: its tokens
+  static_assert(sizeof(rows_of) == kUpRows, "LDS");
   const MoeLists lists = moe_lists_at(a, lds);
   uint8_t* const mine = lds + 4 * moe_list_words(a.tokens * a.top_k, a.experts);
   if (threadIdx.x < a.tokens) lists.exponent[threadIdx.x] = a.x_exponent ? a.x_exponent[threadIdx.x] : 0;
@@ -948,7 +963,7 @@ constexpr size_t moe_most_list_bytes(int MT) { return 4 * (size_t)moe_list_words
 template <int DT, int MT, int NS, int KW, int ROWS, bool CHOOSE>
 hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
   constexpr int PX = moe_x_pieces(DT) > 0 ? moe_x_pieces(DT) : 1;
-  constexpr size_t bytes = kUpWaves * (sizeof(MoeStage<2, NS, PX>) + (KW > 1 ? 2 * MT * 1024 : 0));
+  constexpr size_t bytes = up_bytes<MT, NS, PX, KW>();
   static_assert(bytes >= kChooseMost * 8, "the order of the logits fits");
   static std::atomic<bool> set[64];
   if (const hipError_t e = moe_allow_lds(&moe_up_kernel<MT, NS, PX, KW, ROWS, CHOOSE>, bytes + moe_most_list_bytes(MT), set);
@@ -958,7 +973,7 @@ hipError_t launch_up(const MoeLayer& a, hipStream_t s) {
   const uint16_t* x = moe_x_pieces(DT) > 0 ? a.x_pieces : reinterpret_cast<const uint16_t*>(a.x);
   // as many workgroups as run at once
   const int jobs = (most * (a.f / 16) + kUpWaves / KW - 1) / (kUpWaves / KW);
-  const int resident = device_cu_count() * up_groups_a_cu(MT, NS, PX);
+  const int resident = device_cu_count() * up_groups_a_cu<MT, NS, PX, KW>(moe_lists_bytes(a));
   const int groups = (jobs < resident ? jobs : resident) + (CHOOSE ? 1 : 0);
   moe_up_kernel<MT, NS, PX, KW, ROWS, CHOOSE><<<groups, 64 * kUpWaves, bytes + moe_lists_bytes(a), s>>>(a, x);
   return hipGetLastError();
