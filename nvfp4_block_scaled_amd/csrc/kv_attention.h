@@ -1524,8 +1524,9 @@ kv_many_kernel(KvCache c, KvAttention a, KvChunks sp, int dt, bool q_vec) {
 // kManyStep, and each workgroup takes an equal run of all units.  (In chunks of a
 // fixed length, as many as fill the GPU if every sequence is of the largest size,
 // 16 sequences of up to 16384 keys and 64 drafts took 343 us, as long as the
-// longest chunk; 8 heads of 128, 4 queries a head.  In equal runs 215 - 240 by the
-// machine, 470 - 520 TFLOP/s, a join of 20 us included.)
+// longest chunk; 8 heads of 128, 4 queries a head.  In equal runs 203 - 258, 434 -
+// 551 TFLOP/s, a join of 20 us included: by how far the scores spread, as tiles with
+// small weights take further products; 190 for all of them with a quarter of the queries.)
 constexpr int kManyStep = 256;
 
 struct KvTreeShare {
